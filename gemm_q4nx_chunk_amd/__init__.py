@@ -65,6 +65,19 @@ class MoeDebug(ctypes.Structure):
                 ("d_shared", ctypes.c_void_p)]
 
 
+class Lora(ctypes.Structure):
+    """q4nx_lora: the adapters of one projection (see include/q4nx.h)."""
+    _fields_ = [("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("a_stride", ctypes.c_int64), ("b_stride", ctypes.c_int64),
+                ("a_bytes", ctypes.c_int64), ("b_bytes", ctypes.c_int64),
+                ("scale", ctypes.c_void_p), ("ranks", ctypes.c_void_p)]
+
+
+class LoraJob(ctypes.Structure):
+    _fields_ = [("lora", Lora), ("base", ctypes.c_void_p), ("y", ctypes.c_void_p)]
+
+
 class ChunkLayout(ctypes.Structure):
     """q4nx_chunk_layout: where a q4_1 / Q4_K chunk keeps each field (see include/q4nx.h)."""
     _fields_ = [(n, ctypes.c_int32) for n in (
@@ -110,6 +123,16 @@ _lib.q4nx_argmax.argtypes = [_P, _I, _I, _I, _P, _P, _P, ctypes.c_size_t, _P]
 _lib.q4nx_argmax_ws.argtypes = [_I, _I]
 _lib.q4nx_argmax_ws.restype = ctypes.c_size_t
 _lib.q4nx_moe_router.argtypes = [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P]
+_lib.q4nx_lora_add.argtypes = [ctypes.POINTER(Lora), _P, _P, _I, _P, _P, _P, ctypes.c_size_t, _P]
+_lib.q4nx_lora_ws.argtypes = [ctypes.POINTER(Lora), _I]
+_lib.q4nx_lora_ws.restype = ctypes.c_size_t
+_lib.q4nx_lora_add_batched.argtypes = [ctypes.POINTER(LoraJob), _I, _P, _P, _I, _P, ctypes.c_size_t, _P]
+_lib.q4nx_lora_batched_ws.argtypes = [ctypes.POINTER(LoraJob), _I, _I]
+_lib.q4nx_lora_batched_ws.restype = ctypes.c_size_t
+_lib.q4nx_add_rmsnorm.argtypes = [_P, _P, _P, _I, _I, ctypes.c_float, _P, _P, _P]
+_lib.q4nx_token_logprobs_ws.argtypes = [_I, _I, _I]
+_lib.q4nx_token_logprobs_ws.restype = ctypes.c_size_t
+_lib.q4nx_token_logprobs.argtypes = [_P, _I, _I, _I, _P, _I, _P, _P, _I, _P, _P, _P, ctypes.c_size_t, _P]
 _lib.q4nx_plan_create.argtypes = [ctypes.POINTER(GemvJob), ctypes.POINTER(ctypes.c_int32), _I, _I,
                                   ctypes.POINTER(ctypes.c_void_p)]
 _lib.q4nx_plan_run.argtypes = [_P, _P]
@@ -125,7 +148,8 @@ for _f in ("q4nx_weight_check", "q4nx_gemv", "q4nx_gemv_batched", "q4nx_gemm_blo
            "q4nx_moe_experts", "q4nx_unpack", "q4nx_decode", "q4nx_repack_q4k_to_q41", "q4nx_gguf_to_q41", "q4nx_q8_rows", "q4nx_argmax", "q4nx_moe_router", "q4nx_version", "q4nx_plan_create",
            "q4nx_plan_run", "q4nx_plan_errors", "q4nx_gemm_exchange_mode", "q4nx_gemv_topk",
            "q4nx_chunk_layout_default", "q4nx_chunk_layout_check", "q4nx_relayout", "q4nx_plan_set_mode",
-           "q4nx_gemm_block_noalloc"):
+           "q4nx_gemm_block_noalloc", "q4nx_lora_add", "q4nx_lora_add_batched", "q4nx_add_rmsnorm",
+           "q4nx_token_logprobs"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 
@@ -422,6 +446,79 @@ def moe_router(R, X, T: int, D: int, E: int, k: int, ids, p, logits, renorm: boo
     they are picked from) from bf16 R [E][D] and X [T][D]."""
     _check(_lib.q4nx_moe_router(_ptr(R), _ptr(X), T, D, E, k, 1 if renorm else 0, _ptr(ids),
                                 _ptr(p), _ptr(logits), _stream(stream)))
+
+
+def lora_table(n_adapters: int, rank: int, rows: int, cols: int, a, b, scale, ranks=None,
+               a_stride: int | None = None, b_stride: int | None = None,
+               a_bytes: int | None = None, b_bytes: int | None = None) -> Lora:
+    """The adapters of one projection of `rows` outputs and `cols` inputs: a holds each
+    adapter's A [rank][cols] and b its B [rows][rank], bf16, strides in bytes (by default
+    one adapter after the other); scale fp32 [n_adapters], ranks int32 [n_adapters] or None."""
+    L = Lora(n_adapters, rank, rows, cols, _ptr(a), _ptr(b),
+             2 * rank * cols if a_stride is None else a_stride,
+             2 * rank * rows if b_stride is None else b_stride,
+             _nbytes(a) if a_bytes is None else a_bytes, _nbytes(b) if b_bytes is None else b_bytes,
+             _ptr(scale), _ptr(ranks))
+    L._owners = (a, b, scale, ranks)
+    return L
+
+
+def lora_ws(L: Lora, M: int) -> int:
+    """Workspace bytes of lora_add (0 = bad descriptor or M)."""
+    return int(_lib.q4nx_lora_ws(ctypes.byref(L), M))
+
+
+def lora_add(L: Lora, x, ids, M: int, y, ws, base=None, stream=None, ws_bytes: int | None = None) -> None:
+    """y[m] = base[m] + scale[e] * B_e (A_e x[m]), e = ids[m] (-1: none); base=None adds to y in place."""
+    _check(_lib.q4nx_lora_add(ctypes.byref(L), _ptr(x), _ptr(ids), M, _ptr(y if base is None else base),
+                              _ptr(y), _ptr(ws), _nbytes(ws) if ws_bytes is None else ws_bytes,
+                              _stream(stream)))
+
+
+def lora_jobs(jobs):
+    """The job array of [(Lora, base, y), ...] (base None: in place), which lora_add_batched and
+    lora_batched_ws also take; it keeps its tensors alive."""
+    arr = (LoraJob * len(jobs))(*[LoraJob(L, _ptr(y if base is None else base), _ptr(y)) for L, base, y in jobs])
+    arr._owners = list(jobs)
+    return arr
+
+
+def _as_lora_jobs(jobs):
+    return jobs if isinstance(jobs, ctypes.Array) else lora_jobs(jobs)
+
+
+def lora_batched_ws(jobs, M: int) -> int:
+    """Workspace bytes of lora_add_batched (0 = bad jobs or M)."""
+    arr = _as_lora_jobs(jobs)
+    return int(_lib.q4nx_lora_batched_ws(arr, len(arr), M))
+
+
+def lora_add_batched(jobs, x, ids, M: int, ws, stream=None, ws_bytes: int | None = None) -> None:
+    """lora_add for several projections that read the same x with the same ids:
+    jobs = [(Lora, base, y), ...] or what lora_jobs made of it."""
+    arr = _as_lora_jobs(jobs)
+    _check(_lib.q4nx_lora_add_batched(arr, len(arr), _ptr(x), _ptr(ids), M, _ptr(ws),
+                                      _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
+
+
+def add_rmsnorm(r, w, M: int, D: int, eps: float, x, y=None, r_out=None, stream=None) -> None:
+    """s = y + r (y None: s = r), r_out = s (unless None), x = bf16(s * w / sqrt(mean(s^2) + eps))."""
+    _check(_lib.q4nx_add_rmsnorm(_ptr(y), _ptr(r), _ptr(w), M, D, eps, _ptr(r_out), _ptr(x), _stream(stream)))
+
+
+def token_logprobs_ws(n: int, M: int, k: int = 0) -> int:
+    """Workspace bytes of token_logprobs (0 = arguments out of range)."""
+    return int(_lib.q4nx_token_logprobs_ws(n, M, k))
+
+
+def token_logprobs(y, n: int, M: int, ws, tokens=None, n_tok: int = 0, logp=None, entropy=None, k: int = 0,
+                   top_ids=None, top_logp=None, ldy: int | None = None, stream=None,
+                   ws_bytes: int | None = None) -> None:
+    """Of each row of logits y[m][:n]: logp[M, n_tok] of tokens[M, n_tok] (int32), entropy[M], and
+    the k likeliest tokens top_ids[M, k] (int32, best first) with top_logp[M, k]."""
+    _check(_lib.q4nx_token_logprobs(_ptr(y), n, n if ldy is None else ldy, M, _ptr(tokens), n_tok, _ptr(logp),
+                                    _ptr(entropy), k, _ptr(top_ids), _ptr(top_logp), _ptr(ws),
+                                    _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
 
 
 def unpack(w: Weight, codes, meta0, meta1=None, row_meta=None, stream=None) -> None:

@@ -19,12 +19,16 @@
 
 #include "../../include/q4nx.h"
 #include "gemm_args.h"
+#include "logprobs_args.h"
+#include "lora_args.h"
 #include "moe_args.h"
 #include "plan_args.h"
 #include "q4nx_dev.h"
 #include "topk.h"
 
 static_assert(Q4NX_GEMM_BATCH_MAX_JOBS == q4nx::kGemmMaxJobs, "GEMM job table size");
+static_assert(Q4NX_LORA_BATCH_MAX_JOBS == q4nx::kLoraMaxJobs, "adapter job table size");
+static_assert(Q4NX_LORA_MAX_M == q4nx::kLoraMaxRows, "adapter rows of one call");
 
 namespace {
 
@@ -1326,6 +1330,263 @@ int q4nx_moe_router(const uint16_t* R, const uint16_t* X, int T, int D, int E, i
   const hipError_t e = q4nx::launch_moe_router(R, X, T, D, E, k, renorm ? 1 : 0, ids, p, logits,
                                                static_cast<hipStream_t>(stream));
   return hip_status(e, "router launch");
+}
+
+// ---------------------------------------------------------------------------
+// low-rank adapters
+// ---------------------------------------------------------------------------
+}  // extern "C"
+
+namespace {
+
+// Whether [p, p + pn) and [q, q + qn) share a byte.
+bool overlap(const void* p, uint64_t pn, const void* q, uint64_t qn) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b ? b - a < pn : a - b < qn;
+}
+
+int check_lora(const q4nx_lora* L, const char* name) {
+  if (!L) return fail(Q4NX_E_ARG, "%s: null descriptor", name);
+  if (!L->a || !L->b || !L->scale) return fail(Q4NX_E_ARG, "%s: null a, b or scale", name);
+  if (L->n_adapters < 1 || L->n_adapters > q4nx::kLoraMaxAdapters)
+    return fail(Q4NX_E_ARG, "%s: n_adapters = %d outside 1..%d", name, L->n_adapters, q4nx::kLoraMaxAdapters);
+  if (L->rank < 8 || L->rank % 8 || L->rank > q4nx::kLoraMaxRank)
+    return fail(Q4NX_E_SHAPE, "%s: rank %d is not a multiple of 8 in 8..%d", name, L->rank, q4nx::kLoraMaxRank);
+  if (L->rows <= 0 || L->rows % 32 || L->cols <= 0 || L->cols % 256 || L->rows > (1 << 20) || L->cols > (1 << 20))
+    return fail(Q4NX_E_SHAPE, "%s: %d x %d is not a whole number of 32 x 256 tiles of at most 1048576 each way",
+                name, L->rows, L->cols);
+  if (!aligned(L->a, 16) || !aligned(L->b, 16) || L->a_stride % 16 || L->b_stride % 16)
+    return fail(Q4NX_E_ALIGN, "%s: arenas and strides must be 16-byte aligned", name);
+  if (!aligned(L->scale, 4) || !aligned(L->ranks, 4))
+    return fail(Q4NX_E_ALIGN, "%s: scale and ranks must be 4-byte aligned", name);
+  const int64_t need[2] = {(int64_t)L->rank * L->cols * 2, (int64_t)L->rank * L->rows * 2};
+  const int64_t stride[2] = {L->a_stride, L->b_stride}, bytes[2] = {L->a_bytes, L->b_bytes};
+  for (int i = 0; i < 2; ++i) {
+    const char which = i ? 'b' : 'a';
+    if (stride[i] < need[i])
+      return fail(Q4NX_E_SHAPE, "%s: %c_stride %lld below one adapter's %lld bytes", name, which,
+                  (long long)stride[i], (long long)need[i]);
+    if (L->n_adapters > 1 && stride[i] > (INT64_MAX - need[i]) / (L->n_adapters - 1))
+      return fail(Q4NX_E_SHAPE, "%s: %c_stride %lld too large", name, which, (long long)stride[i]);
+    const int64_t total = (int64_t)(L->n_adapters - 1) * stride[i] + need[i];
+    if (bytes[i] < total)
+      return fail(Q4NX_E_SHORT, "%s: arena %c holds %lld bytes, %d adapters need %lld", name, which,
+                  (long long)bytes[i], L->n_adapters, (long long)total);
+  }
+  return Q4NX_OK;
+}
+
+// Launch shape and workspace layout of a call over checked tables.
+struct LoraShape {
+  q4nx::LoraArgs a;
+  size_t hdr, sorted, tiles, u[q4nx::kLoraMaxJobs], total;
+};
+
+void lora_shape(const q4nx_lora* const* L, int n, int M, LoraShape& sh) {
+  memset(&sh, 0, sizeof sh);
+  q4nx::LoraArgs& a = sh.a;
+  a.n_jobs = n;
+  a.n_adapters = L[0]->n_adapters;
+  a.M = M;
+  a.cols = L[0]->cols;
+  a.max_tiles = M <= q4nx::kLoraScanRows ? M : q4nx::lora_max_tiles(M, a.n_adapters);
+  const int tiles = (M + 63) / 64;   // at least
+  int groups = 0;
+  int64_t rows = 0;
+  for (int i = 0; i < n; ++i) {
+    a.job[i].rg_begin = groups;
+    groups += (L[i]->rank + q4nx::kLoraRankGroup - 1) / q4nx::kLoraRankGroup;
+    rows += L[i]->rows;
+  }
+  const int units = a.cols / 256;
+  a.split = std::max(1, std::min({512 / (tiles * groups), units, q4nx::kLoraMaxSplit}));
+  a.n_range = 64;
+  while (a.n_range < 1024 && tiles * (rows / (2 * a.n_range)) >= 512) a.n_range *= 2;
+  int wg = 0;
+  auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+  size_t o = 256;
+  sh.sorted = o;
+  o = up(o + (size_t)M * 4);
+  sh.tiles = o;
+  o = up(o + (size_t)q4nx::lora_max_tiles(M, a.n_adapters) * 12);
+  for (int i = 0; i < n; ++i) {
+    a.job[i].wg_begin = wg;
+    wg += (L[i]->rows + a.n_range - 1) / a.n_range;
+    sh.u[i] = o;
+    o = up(o + (size_t)a.split * M * L[i]->rank * 4);
+  }
+  sh.total = o;
+}
+
+int check_lora_jobs(const q4nx_lora_job* jobs, int n, int M, const char* name) {
+  if (!jobs) return fail(Q4NX_E_ARG, "%s: null job array", name);
+  if (n < 1 || n > Q4NX_LORA_BATCH_MAX_JOBS)
+    return fail(Q4NX_E_ARG, "%s: %d jobs outside 1..%d", name, n, (int)Q4NX_LORA_BATCH_MAX_JOBS);
+  if (M < 1 || M > Q4NX_LORA_MAX_M)
+    return fail(Q4NX_E_ARG, "%s: M = %d outside 1..%d", name, M, (int)Q4NX_LORA_MAX_M);
+  for (int i = 0; i < n; ++i) {
+    char job[64];
+    snprintf(job, sizeof job, "%s job %d", name, i);
+    const int st = check_lora(&jobs[i].lora, n > 1 ? job : name);
+    if (st) return st;
+    if (jobs[i].lora.cols != jobs[0].lora.cols || jobs[i].lora.n_adapters != jobs[0].lora.n_adapters)
+      return fail(Q4NX_E_SHAPE, "%s: job %d differs from job 0 in cols or n_adapters", name, i);
+  }
+  return Q4NX_OK;
+}
+
+int run_lora(const q4nx_lora_job* jobs, int n, const uint16_t* x, const int32_t* ids, int M, void* ws,
+             size_t ws_bytes, void* stream, const char* name) {
+  const int st = check_lora_jobs(jobs, n, M, name);
+  if (st) return st;
+  if (!x || !ids) return fail(Q4NX_E_ARG, "%s: null x or ids", name);
+  if (!aligned(x, 16) || !aligned(ids, 4))
+    return fail(Q4NX_E_ALIGN, "%s: x must be 16-byte, ids 4-byte aligned", name);
+  const q4nx_lora* L[q4nx::kLoraMaxJobs];
+  for (int i = 0; i < n; ++i) {
+    const q4nx_lora_job& j = jobs[i];
+    if (!j.base || !j.y) return fail(Q4NX_E_ARG, "%s: null base or y of job %d", name, i);
+    if (!aligned(j.base, 4) || !aligned(j.y, 4))
+      return fail(Q4NX_E_ALIGN, "%s: base and y of job %d must be 4-byte aligned", name, i);
+    const uint64_t bytes = (uint64_t)M * j.lora.rows * 4;
+    if (j.base != j.y && overlap(j.base, bytes, j.y, bytes))
+      return fail(Q4NX_E_ARG, "%s: y of job %d overlaps its base without being it", name, i);
+    for (int k = 0; k < n; ++k) {
+      const uint64_t kb = (uint64_t)M * jobs[k].lora.rows * 4;
+      if (k != i && (overlap(j.y, bytes, jobs[k].y, kb) || overlap(j.y, bytes, jobs[k].base, kb)))
+        return fail(Q4NX_E_ARG, "%s: y of job %d overlaps y or base of job %d", name, i, k);
+    }
+    if (overlap(j.y, bytes, x, (uint64_t)M * j.lora.cols * 2) || overlap(j.y, bytes, ids, (uint64_t)M * 4))
+      return fail(Q4NX_E_ARG, "%s: y of job %d overlaps x or ids", name, i);
+    L[i] = &j.lora;
+  }
+  LoraShape sh;
+  lora_shape(L, n, M, sh);
+  if (!ws || ws_bytes < sh.total)
+    return fail(Q4NX_E_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", name, ws_bytes, sh.total);
+  if (!aligned(ws, 256)) return fail(Q4NX_E_ALIGN, "%s: workspace not 256-byte aligned", name);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  q4nx::LoraArgs& a = sh.a;
+  a.x = x;
+  a.ids = ids;
+  a.hdr = reinterpret_cast<uint32_t*>(w + sh.hdr);
+  a.sorted = reinterpret_cast<int32_t*>(w + sh.sorted);
+  a.tiles = reinterpret_cast<int32_t*>(w + sh.tiles);
+  for (int i = 0; i < n; ++i) {
+    q4nx::LoraJob& j = a.job[i];
+    j.a = L[i]->a;
+    j.b = L[i]->b;
+    j.a_stride = L[i]->a_stride / 2;
+    j.b_stride = L[i]->b_stride / 2;
+    j.scale = L[i]->scale;
+    j.ranks = L[i]->ranks;
+    j.base = jobs[i].base;
+    j.y = jobs[i].y;
+    j.u = reinterpret_cast<float*>(w + sh.u[i]);
+    j.rank = L[i]->rank;
+    j.rows = L[i]->rows;
+  }
+  return hip_status(q4nx::launch_lora(a, static_cast<hipStream_t>(stream)), name);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t q4nx_lora_batched_ws(const q4nx_lora_job* jobs, int n_jobs, int M) {
+  if (check_lora_jobs(jobs, n_jobs, M, "lora_batched_ws")) return 0;
+  const q4nx_lora* L[q4nx::kLoraMaxJobs];
+  for (int i = 0; i < n_jobs; ++i) L[i] = &jobs[i].lora;
+  LoraShape sh;
+  lora_shape(L, n_jobs, M, sh);
+  return sh.total;
+}
+
+size_t q4nx_lora_ws(const q4nx_lora* L, int M) {
+  if (!L) return 0;
+  const q4nx_lora_job j{*L, nullptr, nullptr};
+  return q4nx_lora_batched_ws(&j, 1, M);
+}
+
+int q4nx_lora_add_batched(const q4nx_lora_job* jobs, int n_jobs, const uint16_t* x, const int32_t* ids, int M,
+                          void* ws, size_t ws_bytes, void* stream) {
+  return run_lora(jobs, n_jobs, x, ids, M, ws, ws_bytes, stream, "lora_add_batched");
+}
+
+int q4nx_lora_add(const q4nx_lora* L, const uint16_t* x, const int32_t* ids, int M, const float* base, float* y,
+                  void* ws, size_t ws_bytes, void* stream) {
+  if (!L) return fail(Q4NX_E_ARG, "lora_add: null descriptor");
+  const q4nx_lora_job j{*L, base, y};
+  return run_lora(&j, 1, x, ids, M, ws, ws_bytes, stream, "lora_add");
+}
+
+// ---------------------------------------------------------------------------
+// residual addition and RMS norm, log probabilities
+// ---------------------------------------------------------------------------
+int q4nx_add_rmsnorm(const float* y, const float* r, const uint16_t* w, int M, int D, float eps, float* r_out,
+                     uint16_t* x, void* stream) {
+  if (!r || !w || !x) return fail(Q4NX_E_ARG, "add_rmsnorm: null r, w or x");
+  if (M < 1 || M > (1 << 20)) return fail(Q4NX_E_ARG, "add_rmsnorm: M = %d outside 1..1048576", M);
+  if (D < 1 || D > q4nx::kNormMaxD)
+    return fail(Q4NX_E_SHAPE, "add_rmsnorm: D = %d outside 1..%d", D, q4nx::kNormMaxD);
+  if (!(eps >= 0.f) || eps > 3.4e38f) return fail(Q4NX_E_ARG, "add_rmsnorm: eps = %g is not a finite number >= 0", eps);
+  if (!aligned(y, 4) || !aligned(r, 4) || !aligned(r_out, 4) || !aligned(w, 2) || !aligned(x, 2))
+    return fail(Q4NX_E_ALIGN, "add_rmsnorm: y, r and r_out must be 4-byte, w and x 2-byte aligned");
+  const uint64_t f = (uint64_t)M * D * 4, h = (uint64_t)M * D * 2, d = (uint64_t)D * 2;
+  if (overlap(x, h, r, f) || (y && overlap(x, h, y, f)) || (r_out && overlap(x, h, r_out, f)) || overlap(x, h, w, d))
+    return fail(Q4NX_E_ARG, "add_rmsnorm: x overlaps another array");
+  if (r_out && ((r_out != r && overlap(r_out, f, r, f)) || (y && r_out != y && overlap(r_out, f, y, f)) ||
+                overlap(r_out, f, w, d)))
+    return fail(Q4NX_E_ARG, "add_rmsnorm: r_out overlaps an input without being r or y");
+  return hip_status(q4nx::launch_add_rmsnorm(y, r, w, M, D, eps, r_out, x, static_cast<hipStream_t>(stream)),
+                    "add_rmsnorm launch");
+}
+
+size_t q4nx_token_logprobs_ws(int n, int M, int k) {
+  if (n < 1 || n > q4nx::kLogprobMaxN || M < 1 || M > 65535 || k < 0 || k > q4nx::kLogprobMaxK) return 0;
+  return q4nx::logprob_ws_layout(n, M, k).total;
+}
+
+int q4nx_token_logprobs(const float* y, int n, int ldy, int M, const int32_t* tokens, int n_tok, float* logp,
+                        float* entropy, int k, int32_t* top_ids, float* top_logp, void* ws, size_t ws_bytes,
+                        void* stream) {
+  if (!y) return fail(Q4NX_E_ARG, "token_logprobs: null y");
+  if (n < 1 || n > q4nx::kLogprobMaxN || ldy < n || M < 1 || M > 65535)
+    return fail(Q4NX_E_ARG, "token_logprobs: n = %d, ldy = %d, M = %d (need 1 <= n <= min(ldy, %d), 1 <= M <= 65535)",
+                n, ldy, M, q4nx::kLogprobMaxN);
+  if (n_tok < 0 || n_tok > q4nx::kLogprobMaxTok)
+    return fail(Q4NX_E_ARG, "token_logprobs: n_tok = %d outside 0..%d", n_tok, q4nx::kLogprobMaxTok);
+  if (k < 0 || k > q4nx::kLogprobMaxK || k > n)
+    return fail(Q4NX_E_ARG, "token_logprobs: k = %d outside 0..min(%d, n)", k, q4nx::kLogprobMaxK);
+  if (n_tok > 0 && (!tokens || !logp)) return fail(Q4NX_E_ARG, "token_logprobs: null tokens or logp");
+  if (k > 0 && !top_ids) return fail(Q4NX_E_ARG, "token_logprobs: null top_ids");
+  if (n_tok == 0 && k == 0 && !entropy) return fail(Q4NX_E_ARG, "token_logprobs: nothing is asked for");
+  if (!aligned(y, 4) || !aligned(tokens, 4) || !aligned(logp, 4) || !aligned(entropy, 4) || !aligned(top_ids, 4) ||
+      !aligned(top_logp, 4))
+    return fail(Q4NX_E_ALIGN, "token_logprobs: every array must be 4-byte aligned");
+  const q4nx::LogprobWsLayout lay = q4nx::logprob_ws_layout(n, M, k);
+  if (!ws || ws_bytes < lay.total)
+    return fail(Q4NX_E_WORKSPACE, "token_logprobs: workspace of %zu bytes, %zu needed", ws_bytes, lay.total);
+  if (!aligned(ws, 256)) return fail(Q4NX_E_ALIGN, "token_logprobs: workspace not 256-byte aligned");
+  q4nx::LogprobArgs a;
+  memset(&a, 0, sizeof a);
+  a.y = y;
+  a.n = n;
+  a.ldy = ldy;
+  a.M = M;
+  a.k = k;
+  a.n_tok = n_tok;
+  a.part_n = q4nx::logprob_part_n(n, M);
+  a.parts = (n + a.part_n - 1) / a.part_n;
+  a.tokens = tokens;
+  a.logp = logp;
+  a.entropy = entropy;
+  a.top_ids = top_ids;
+  a.top_logp = top_logp;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  a.stats = reinterpret_cast<q4nx::f32x4*>(wsb + lay.stats);
+  a.keys = reinterpret_cast<uint64_t*>(wsb + lay.keys);
+  return hip_status(q4nx::launch_token_logprobs(a, static_cast<hipStream_t>(stream)), "token_logprobs launch");
 }
 
 int q4nx_decode(const q4nx_weight* w, float* out, void* stream) {

@@ -1,0 +1,50 @@
+// Device-side arguments of the log-probability kernels (one struct, passed by value).
+#pragma once
+
+#include "q4nx_dev.h"
+
+namespace q4nx {
+
+constexpr int kLogprobMaxK = 32;       // alternatives of a row
+constexpr int kLogprobMaxTok = 64;     // given tokens of a row
+constexpr int kLogprobMaxN = 1 << 20;  // logits of a row
+constexpr int kLogprobMaxParts = 256;  // parts of a row: four lists a lane in the join
+
+struct LogprobArgs {
+  const float* y;          // [M] rows of n logits, ldy apart
+  int32_t n, ldy, M;
+  int32_t k, n_tok;
+  int32_t parts, part_n;   // parts of a row, logits of a part
+  const int32_t* tokens;   // [M][n_tok]
+  float* logp;             // [M][n_tok]
+  float* entropy;          // [M] or null
+  int32_t* top_ids;        // [M][k]
+  float* top_logp;         // [M][k] or null
+  f32x4* stats;            // [M][parts]: m, rest, sum e d, -
+  uint64_t* keys;          // [M][parts][k], decreasing, 0 past the last
+};
+
+// Logits of a part: 4096 (a wave's 64 registers a lane) where that makes
+// enough waves to fill the GPU, else 1024.
+inline int logprob_part_n(int n, int M) {
+  const int64_t waves = (int64_t)M * ((n + 4095) / 4096);
+  return waves < 1024 && n <= kLogprobMaxParts * 1024 ? 1024 : 4096;
+}
+
+// Workspace: the parts' stats, then their keys.
+struct LogprobWsLayout {
+  size_t stats, keys, total;
+};
+inline LogprobWsLayout logprob_ws_layout(int n, int M, int k) {
+  const int pn = logprob_part_n(n, M);
+  const size_t units = (size_t)M * ((n + pn - 1) / pn);
+  LogprobWsLayout l;
+  l.stats = 0;
+  l.keys = units * 16;
+  l.total = (l.keys + units * k * 8 + 255) & ~(size_t)255;
+  return l;
+}
+
+hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t s);
+
+}  // namespace q4nx

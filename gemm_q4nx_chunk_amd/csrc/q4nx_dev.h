@@ -185,5 +185,8 @@ hipError_t launch_argmax(const float* y, int n, int ldy, int M, int32_t* idx, fl
                          hipStream_t s);
 hipError_t launch_moe_router(const uint16_t* R, const uint16_t* X, int T, int D, int E, int k,
                              int renorm, int32_t* ids, float* p, float* logits, hipStream_t s);
+constexpr int kNormMaxD = 32768;   // a row's values stay in one workgroup's registers
+hipError_t launch_add_rmsnorm(const float* y, const float* r, const uint16_t* w, int M, int D, float eps,
+                              float* r_out, uint16_t* x, hipStream_t s);
 
 }  // namespace q4nx

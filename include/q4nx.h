@@ -518,6 +518,128 @@ int q4nx_moe_router(const uint16_t* R, const uint16_t* X, int T, int D, int E, i
                     int32_t* ids, float* p, float* logits, void* stream);
 
 /*
+ * Low-rank adapters beside a shared projection (onw technical notes, "computing
+ * MoE prompts together": rows that use the same weights are taken together, and
+ * each weight is read once for them).  One quantised projection serves many
+ * tuned variants: adapter e adds scale[e] * B_e (A_e x) to the projection's
+ * output, with A_e and B_e in bf16.
+ *
+ * The adapters of one projection lie in two arenas, adapter e's A [rank][cols]
+ * at a + e*a_stride and its B [rows][rank] at b + e*b_stride, each row-major.
+ */
+typedef struct q4nx_lora {
+  int32_t n_adapters;   /* adapters in the arenas, 1..4096 */
+  int32_t rank;         /* stored rank: a multiple of 8, 8..256 */
+  int32_t rows, cols;   /* the projection's: rows a multiple of 32, cols of 256 (at most 1048576) */
+  const uint16_t* a;    /* DEVICE bf16, 16-byte aligned */
+  const uint16_t* b;    /* DEVICE bf16, 16-byte aligned */
+  int64_t a_stride, b_stride;   /* bytes between adapters, 16-byte multiples */
+  int64_t a_bytes, b_bytes;     /* bytes available in each arena */
+  const float* scale;   /* DEVICE fp32 [n_adapters] */
+  const int32_t* ranks; /* DEVICE int32 [n_adapters], or NULL: adapter e uses the first ranks[e]
+                           rows of its A and columns of its B (clamped to 0..rank) and what lies
+                           past them may hold anything; NULL: all of them */
+} q4nx_lora;
+
+/* One projection's adapters, with its output. */
+typedef struct q4nx_lora_job {
+  q4nx_lora lora;
+  const float* base;    /* DEVICE fp32 [M][rows]: what the shared projection wrote */
+  float* y;             /* DEVICE fp32 [M][rows]; base itself (in place), or apart from it */
+} q4nx_lora_job;
+
+/* Most jobs of one q4nx_lora_add_batched call; most activation rows of a call. */
+enum { Q4NX_LORA_BATCH_MAX_JOBS = 8, Q4NX_LORA_MAX_M = 4096 };
+
+/*
+ * y[m] = base[m] + scale[e] * B_e (A_e x[m]) with e = ids[m], for m < M; y[m] =
+ * base[m] for a row without an adapter (ids[m] = -1).
+ *   x    DEVICE bf16 [M][cols], row-major, 16-byte aligned: what the projection read
+ *   ids  DEVICE int32 [M], in any order
+ *   base, y  4-byte aligned; every row of y is written (in place, rows without
+ *        an adapter are left as they are); y and base may not overlap in part
+ *   M    1..Q4NX_LORA_MAX_M
+ *   ws   DEVICE workspace of q4nx_lora_ws(L, M) bytes, 256-byte aligned.  Nothing
+ *        in it needs initialising; calls that share it must not overlap.
+ * Rows of one adapter are found on the device and taken together, up to 64 (16
+ * for M <= 64) at a time, so an adapter is read once per tile of rows.  Sums
+ * are fp32 in an order fixed by the call's sizes: a row's bits depend neither on
+ * the other rows nor on its place.  B_e (A_e x) keeps fp32's precision (A_e x
+ * enters the second product as three bf16 parts that hold its 24 bits).
+ * An id below -1 or past the last adapter is never dereferenced: its row is
+ * taken as one without an adapter and bit 0 of the uint32 at ws[0] is set
+ * (cleared at the start of each call; read it after synchronising).
+ * E_SHAPE: rank, rows or cols outside their rules; E_SHORT: an arena smaller
+ * than its adapters need.
+ */
+int q4nx_lora_add(const q4nx_lora* L, const uint16_t* x, const int32_t* ids, int M, const float* base,
+                  float* y, void* ws, size_t ws_bytes, void* stream);
+/* Workspace bytes of q4nx_lora_add (0 = bad descriptor or M). */
+size_t q4nx_lora_ws(const q4nx_lora* L, int M);
+
+/*
+ * q4nx_lora_add for several projections that read the same x with the same ids
+ * (q|k|v, gate|up), in as many launches as one.
+ *   jobs  HOST array of n_jobs (1..Q4NX_LORA_BATCH_MAX_JOBS), with the cols and
+ *         n_adapters of jobs[0] (E_SHAPE otherwise); rank and rows may differ.
+ *         Each y must lie apart from every other job's y and base.
+ */
+int q4nx_lora_add_batched(const q4nx_lora_job* jobs, int n_jobs, const uint16_t* x, const int32_t* ids,
+                          int M, void* ws, size_t ws_bytes, void* stream);
+size_t q4nx_lora_batched_ws(const q4nx_lora_job* jobs, int n_jobs, int M);
+
+/*
+ * Residual addition and RMS norm, the step from one projection's fp32 output to
+ * the bf16 activations of the next (NPU engine page, "From a GGUF": the packed
+ * model keeps its norms in bf16):
+ *   s = y + r,  r_out = s,  x = bf16(s * w / sqrt(mean(s^2) + eps))
+ *   y      DEVICE fp32 [M][D], or NULL (s = r: the norm alone, as of q and k heads)
+ *   r      DEVICE fp32 [M][D], the residual
+ *   w      DEVICE bf16 [D]
+ *   r_out  DEVICE fp32 [M][D] or NULL (not written); may be r or y itself
+ *   x      DEVICE bf16 [M][D], rounded once to nearest even
+ *   M      1..1048576;  D  1..32768, any;  eps >= 0
+ * fp32 arrays 4-byte, bf16 arrays 2-byte aligned.  x and r_out must lie apart
+ * from each other and from every input, but for r_out in place (E_ARG).  Sums are fp32 in a fixed order;
+ * a row whose squares overflow fp32 gives x = 0 (or NaN where s is not finite).
+ */
+int q4nx_add_rmsnorm(const float* y, const float* r, const uint16_t* w, int M, int D, float eps,
+                     float* r_out, uint16_t* x, void* stream);
+
+/*
+ * Log probabilities over logits already in memory (NPU engine page, "Q4NX
+ * chunks": the tied Q8 lm_head whose logits it reads): for each row m of y
+ * (fp32, row stride ldy, n logits), with log Z = log(sum_i exp(y[m][i])):
+ *   logp[m][c]      = y[m][t] - log Z,  t = tokens[m][c]
+ *   entropy[m]      = -sum_i p_i log p_i
+ *   top_ids[m][j], top_logp[m][j]: the k likeliest tokens in decreasing order,
+ *                     the lower index first among equal logits (zeros of either
+ *                     sign are equal), and their log probabilities
+ * A logit of -Inf (a token ruled out) or NaN has probability 0: it is no
+ * alternative (past the last one top_ids is -1 and top_logp NaN), and as a
+ * given token its logp is -Inf.  A given token outside [0, n) gets NaN.  A row
+ * that leaves nothing has NaN for logp and entropy.  Logits of +Inf share the
+ * whole probability equally.
+ *   y        DEVICE fp32, 4-byte aligned; 1 <= n <= min(ldy, 1048576)
+ *   M        1..65535
+ *   tokens   DEVICE int32 [M][n_tok], logp DEVICE fp32 [M][n_tok]; n_tok 0..64
+ *            (both may be NULL when 0)
+ *   entropy  DEVICE fp32 [M] or NULL
+ *   k        0..32; top_ids DEVICE int32 [M][k] (NULL when 0), top_logp DEVICE
+ *            fp32 [M][k] or NULL
+ *   ws       DEVICE workspace of q4nx_token_logprobs_ws(n, M, k) bytes, 256-byte
+ *            aligned.  Nothing in it needs initialising; calls that share it
+ *            must not overlap.
+ * E_ARG also when nothing is asked for.  The largest logit is set apart from
+ * the sum, so that the log probability of a likely token, and the entropy of a
+ * sharp distribution, keep their digits.
+ */
+size_t q4nx_token_logprobs_ws(int n, int M, int k);
+int q4nx_token_logprobs(const float* y, int n, int ldy, int M, const int32_t* tokens, int n_tok,
+                        float* logp, float* entropy, int k, int32_t* top_ids, float* top_logp, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/*
  * Test surface of the decoders (NPU engine page, "Q4NX chunks": the decoders
  * of all three kinds are checked bit for bit).  Writes the fields of every
  * chunk in logical [rows][cols] order:

@@ -13,6 +13,8 @@ the HIP kernels.  It is plain, slow and written to be checked by eye:
   the router (logits, softmax, top-k, renormalisation), the greedy / top-k
   pick from the head's logits, and the Q4_K -> q4_1 repack with its rounding
   bound;
+* ``tail``    -- low-rank adapters beside a projection, the residual RMS norm
+  and log probabilities over logits, from their definitions;
 * ``gguf``    -- GGUF Q4_0 / Q4_1 / Q4_K blocks decoded from their own
   definition, and the q4_1 fields the GGUF -> q4_1 conversion must give.
 
@@ -35,6 +37,7 @@ from .ref import (gemv_ref, check_tol, tol_ratio, silu, swiglu, moe_layer_ref, m
                   repack_q4k_to_q41, repack_bound, router_topk, router_logits_ref, head_topk)
 from .gguf import (GGUF_Q4_0, GGUF_Q4_1, GGUF_Q4_K, gguf_bytes, gguf_fields, gguf_dequant,
                    gguf_to_q41, gguf_to_q41_bound)
+from .tail import add_rmsnorm_ref, lora_ref, token_logprobs_ref
 
 __all__ = [
     "KIND_BYTES", "decode_fields", "weights_exact", "weights_f32", "unpack_expected",
@@ -43,4 +46,5 @@ __all__ = [
     "moe_layer_ref", "moe_combine_ref", "repack_q4k_to_q41", "repack_bound", "router_topk",
     "router_logits_ref", "head_topk", "GGUF_Q4_0", "GGUF_Q4_1", "GGUF_Q4_K", "gguf_bytes", "gguf_fields",
     "gguf_dequant", "gguf_to_q41", "gguf_to_q41_bound",
+    "lora_ref", "add_rmsnorm_ref", "token_logprobs_ref",
 ]

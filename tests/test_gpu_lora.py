@@ -1,0 +1,243 @@
+"""Low-rank adapters beside a projection (q4nx_lora_add, q4nx_lora_add_batched)
+against the float64 reference.
+
+Tolerance: bf16 x bf16 products are exact in fp32, so an element of A x is off
+by at most K roundings of 2^-23 (2^-24, doubled for a matrix core that truncates)
+of sum |a x|.  Its three bf16 parts hold it exactly; scaling is one rounding, the
+second product adds 3 R roundings, the parts of K 64 at most, the base two:
+  |y - y_ref| <= 2^-23 ((K + 3 R + 80) sum |scale b| sum |a x| + |base| + |y_ref|).
+"""
+import numpy as np
+import pytest
+
+import oracle
+import synth
+
+from _gpu import dev_bf16, dev_f32, dev_i32, have_gpu, host, q, torch
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not have_gpu(), reason="needs a GPU")]
+
+
+class Case:
+    """Inputs of one call and their device copies; adapters lie `pad` elements apart."""
+
+    def __init__(self, tag, M, K, N, R, E, ids, ranks=None, pad=0, garbage=False):
+        g = synth.rng("gpu-lora", tag, M, K, N, R, E)
+        self.M, self.K, self.N, self.R, self.E = M, K, N, R, E
+        self.x = synth.bf16_bits(g.standard_normal((M, K)))
+        A = synth.bf16_bits(g.standard_normal((E, R, K)) / np.sqrt(K))
+        B = synth.bf16_bits(g.standard_normal((E, N, R)) / np.sqrt(R))
+        if garbage:      # what lies past an adapter's rank may hold anything
+            for e in range(E):
+                A[e, ranks[e]:] = 0x7FC0
+                B[e, :, ranks[e]:] = 0x7F80
+        self.A, self.B = synth.bf16_to_f32(A), synth.bf16_to_f32(B)
+        self.scale = (0.25 + g.random(E)).astype(np.float32)
+        self.ids = np.asarray(ids, dtype=np.int32)
+        self.ranks = None if ranks is None else np.asarray(ranks, dtype=np.int32)
+        self.base = g.standard_normal((M, N)).astype(np.float32)
+
+        def arena(v):
+            flat = np.full((E, v[0].size + pad), 0x7FC0, np.uint16)
+            flat[:, :v[0].size] = v.reshape(E, -1)
+            return dev_bf16(flat)
+        self.dx, self.dids, self.dbase = dev_bf16(self.x), dev_i32(self.ids), dev_f32(self.base)
+        self.table = q().lora_table(E, R, N, K, arena(A), arena(B), dev_f32(self.scale),
+                                    ranks=None if ranks is None else dev_i32(self.ranks),
+                                    a_stride=2 * (R * K + pad), b_stride=2 * (R * N + pad))
+
+    def ref(self):
+        return oracle.lora_ref(synth.bf16_to_f32(self.x), self.A, self.B, self.scale, self.ids, self.base, self.ranks)
+
+    def check(self, y):
+        want, mag = self.ref()
+        tol = 2.0 ** -23 * ((self.K + 3 * self.R + 80) * mag + np.abs(self.base) + np.abs(want))
+        assert np.isfinite(y).all()
+        bad = np.abs(y - want) > tol
+        assert not bad.any(), (np.argwhere(bad)[:5], np.abs(y - want).max())
+        none = (self.ids < 0) | (self.ids >= self.E)
+        np.testing.assert_array_equal(y[none], self.base[none])
+
+    def run(self, in_place=False, ws=None):
+        print(f"lora M={self.M} K={self.K} N={self.N} R={self.R} E={self.E} in_place={in_place}", flush=True)
+        if ws is None:      # stale contents
+            ws = torch.full((q().lora_ws(self.table, self.M),), 0xAB, dtype=torch.uint8, device="cuda")
+        y = self.dbase.clone() if in_place else torch.full((self.M, self.N), float("nan"), device="cuda")
+        q().lora_add(self.table, self.dx, self.dids, self.M, y, ws, base=None if in_place else self.dbase)
+        out = host(y)
+        self.flag = int(host(ws[:4].view(torch.int32))[0])
+        return out
+
+
+def _ids(kind, M, E, seed=1):
+    g = np.random.default_rng(seed)
+    return {"one": np.zeros(M), "each": np.arange(M) % E, "random": g.integers(0, E, M),
+            "some": np.where(g.random(M) < 0.5, -1, g.integers(0, E, M)), "none": np.full(M, -1),
+            "runs": np.sort(g.integers(0, E, M))[::-1]}[kind].astype(np.int32)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("M,kind", [(1, "one"), (1, "none"), (2, "each"), (8, "random"), (17, "one"), (16, "one"),
+                                    (64, "each"), (64, "one"), (63, "some"), (33, "none")])
+def test_decode_rows(M, kind, in_place):
+    c = Case("decode", M, 512, 96, 16, 40, _ids(kind, M, 40))
+    c.check(c.run(in_place))
+    assert c.flag == 0
+
+
+@pytest.mark.parametrize("M,kind,E", [(65, "one", 3), (128, "each", 128), (200, "random", 5), (255, "some", 9),
+                                      (256, "runs", 4), (257, "runs", 4), (300, "each", 300), (400, "some", 7),
+                                      (513, "one", 1), (1000, "runs", 6), (1024, "none", 2)])
+def test_prompt_rows(M, kind, E):
+    c = Case("prompt", M, 256, 64, 8, E, _ids(kind, M, E))
+    c.check(c.run())
+    c.check(c.run(in_place=True))
+    assert c.flag == 0
+
+
+@pytest.mark.parametrize("M", [3, 100, 300])
+@pytest.mark.parametrize("R", [8, 16, 24, 32, 40, 64, 72, 128, 200, 256])
+def test_ranks_stored(R, M):
+    c = Case("rank", M, 768, 160, R, 5, _ids("random", M, 5))
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("M", [6, 90, 270])
+def test_ranks_of_each_adapter(M):
+    ranks = [0, 1, 7, 8, 9, 31, 33, 63, 64, 72]
+    c = Case("mixed", M, 512, 64, 72, len(ranks), _ids("random", M, len(ranks)), ranks, garbage=True)
+    c.check(c.run())
+    c.ranks = np.array([-3, 1, 7, 8, 9, 31, 33, 63, 64, 1000], dtype=np.int32)     # clamped to 0..72
+    c.A[~np.isfinite(c.A)] = 0
+    c.B[~np.isfinite(c.B)] = 0
+    d = Case("mixed", M, 512, 64, 72, len(ranks), c.ids, list(c.ranks))
+    d.check(d.run())
+
+
+@pytest.mark.parametrize("K,N", [(256, 32), (2560, 4096), (9728, 2560), (28672, 96), (256, 14336), (7424, 1056)])
+@pytest.mark.parametrize("M", [1, 5, 70])
+def test_shapes(M, K, N):
+    c = Case("shape", M, K, N, 16, 3, _ids("random", M, 3))
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("M", [4, 300])
+def test_padded_arenas(M):
+    c = Case("pad", M, 256, 64, 16, 3, _ids("random", M, 3), pad=24)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("M", [5, 64, 256, 270])
+def test_ids_outside(M):
+    ids = _ids("random", M, 4)
+    ids[[0, 3]] = [4, -2]
+    ids[2] = 2 ** 31 - 1
+    ids[M - 1] = -2 ** 31
+    c = Case("outside", M, 256, 64, 8, 4, ids)
+    c.check(c.run())
+    assert c.flag == 1
+    ids[:] = -1
+    c = Case("outside", M, 256, 64, 8, 4, ids)
+    c.check(c.run())
+    assert c.flag == 0
+
+
+@pytest.mark.parametrize("M", [40, 200, 500])
+def test_a_rows_bits_depend_on_its_own_inputs_only(M):
+    c = Case("bits", M, 512, 128, 32, 6, _ids("random", M, 6))
+    y0 = c.run()
+    np.testing.assert_array_equal(c.run().view(np.int32), y0.view(np.int32))
+    # the same rows in another order
+    p = np.random.default_rng(3).permutation(M)
+    c.dx, c.dids, c.dbase = dev_bf16(c.x[p]), dev_i32(c.ids[p]), dev_f32(c.base[p])
+    np.testing.assert_array_equal(c.run().view(np.int32), y0[p].view(np.int32))
+    # every row but 7 with another adapter
+    ids = (c.ids + 1) % 6
+    ids[7] = c.ids[7]
+    c.dx, c.dids, c.dbase = dev_bf16(c.x), dev_i32(ids), dev_f32(c.base)
+    np.testing.assert_array_equal(c.run()[7].view(np.int32), y0[7].view(np.int32))
+
+
+def test_values_out_of_the_ordinary():
+    """Infinities and NaN stay in their rows; large and small values keep their digits."""
+    c = Case("inf", 6, 256, 64, 8, 2, [0, 1, 0, 1, 0, 0])
+    c.x[1, 3] = 0x7F80                       # +inf
+    c.x[2, 5] = 0x7FC0                       # NaN
+    c.x[3] = synth.bf16_bits(synth.bf16_to_f32(c.x[3]) * np.float32(1e30))
+    c.x[4] = synth.bf16_bits(synth.bf16_to_f32(c.x[4]) * np.float32(1e-30))
+    c.base[4:5] = 0
+    c.dx, c.dbase = dev_bf16(c.x), dev_f32(c.base)
+    y = c.run()
+    with np.errstate(invalid="ignore"):
+        want, mag = c.ref()
+    assert np.isnan(y[2]).all() and not np.isfinite(y[1]).any()
+    for m in (0, 3, 4, 5):
+        tol = 2.0 ** -23 * ((c.K + 3 * c.R + 80) * mag[m] + np.abs(c.base[m]) + np.abs(want[m]))
+        assert (np.abs(y[m] - want[m]) <= tol).all(), m
+    # an infinite A x against finite B: infinite of B's sign, as the formula has it
+    c = Case("inf2", 1, 256, 32, 8, 1, [0], ranks=[1])
+    c.x[:] = 0
+    c.x[0, 0] = 0x7F80
+    c.dx = dev_bf16(c.x)
+    y = c.run()
+    a0, b0 = c.A[0, 0, 0], c.B[0, :, 0]
+    rest = c.A[0, 0, 1:]
+    assert a0 != 0 and np.isfinite(rest).all() and (b0 != 0).all()
+    np.testing.assert_array_equal(y[0], np.sign(b0) * np.sign(a0) * np.inf)
+
+
+@pytest.mark.parametrize("M", [1, 9, 64, 300])
+def test_batched_projections(M):
+    """q, k and v of one layer, at different ranks: each job as its own call gives it, up to the
+    order of its sums."""
+    ids = _ids("some", M, 5)
+    cs = [Case(f"qkv{i}", M, 512, n, r, 5, ids) for i, (n, r) in enumerate([(256, 16), (64, 40), (96, 128)])]
+    for c in cs[1:]:
+        c.x, c.dx = cs[0].x, cs[0].dx
+    ys = [torch.full((M, c.N), float("nan"), device="cuda") for c in cs]
+    jobs = q().lora_jobs([(c.table, c.dbase, y) for c, y in zip(cs, ys)])
+    ws = torch.full((q().lora_batched_ws(jobs, M),), 0xCD, dtype=torch.uint8, device="cuda")
+    print(f"lora batched M={M}", flush=True)
+    q().lora_add_batched(jobs, cs[0].dx, cs[0].dids, M, ws)
+    for c, y in zip(cs, ys):
+        c.check(host(y))
+    # in place, from a list
+    ys = [c.dbase.clone() for c in cs]
+    q().lora_add_batched([(c.table, None, y) for c, y in zip(cs, ys)], cs[0].dx, cs[0].dids, M, ws)
+    for c, y in zip(cs, ys):
+        c.check(host(y))
+
+
+def test_workspace_is_not_written_past_its_size():
+    for M, E in [(1, 1), (64, 3), (65, 2), (256, 300), (257, 300), (600, 2)]:
+        c = Case("ws", M, 256, 64, 24, E, _ids("random", M, E))
+        n = q().lora_ws(c.table, M)
+        ws = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+        c.check(c.run(ws=ws))
+        assert (host(ws[n:]) == 0x5A).all()
+
+
+@pytest.mark.parametrize("M", [1, 8, 300])
+def test_captured_replayed_and_on_another_stream(M):
+    c = Case("graph", M, 512, 128, 16, 4, _ids("random", M, 4))
+    ws = torch.full((q().lora_ws(c.table, M),), 0xAB, dtype=torch.uint8, device="cuda")
+    y = torch.empty((M, c.N), device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    q().lora_add(c.table, c.dx, c.dids, M, y, ws, base=c.dbase, stream=s)
+    s.synchronize()
+    eager = host(y)
+    c.check(eager)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q().lora_add(c.table, c.dx, c.dids, M, y, ws, base=c.dbase)
+    for i in range(3):
+        y.fill_(float("nan"))
+        ws.fill_(i)
+        graph.replay()
+        np.testing.assert_array_equal(host(y).view(np.int32), eager.view(np.int32))
+    # new ids in the same buffer reach the next replay
+    c.ids = ((c.ids + 1) % 4).astype(np.int32)
+    c.dids.copy_(dev_i32(c.ids))
+    graph.replay()
+    c.check(host(y))

@@ -9,18 +9,21 @@
 // probability is -log1p(rest), where log(1 + rest) of the whole sum would lose
 // what lies below 2^-24.
 //
-// Two launches.  k_logprob_part: one wave takes a part of a row (64 * 4 * NQ
-// logits) into registers, forms the part's (m, rest, sum e d) and its top k.
-// k_logprob_join: one wave a row joins the parts: of two parts with
-// m1 >= m2, f = exp(m2 - m1),
-//   rest = rest1 + (1 + rest2) f,   t = t1 + f (t2 + (1 + rest2)(m2 - m1)).
+// Two launches.  k_logprob_part: a wave streams a part of a row through
+// registers in chunks of 256 NQ logits, the next chunk's loads in flight, and
+// keeps (m, rest, t = sum e d) against the wave's maximum so far, and the top k
+// so far.  k_logprob_join: one wave a row adds the parts, each by
+// f = exp(m_part - m): rest += (1 + rest_p) f (rest_p alone for one part that
+// has m), t += f (t_p + (1 + rest_p)(m_part - m)).
 //
-// Top k of a part: T, the k-th largest of the 64 lanes' own maxima, is at most
-// the k-th largest value, so the top k are among the values above T and, if
-// fewer than k are, the first of those equal to T.  These few (about 1.3 k of
-// random logits) are gathered by ballots and ordered by counting, for each,
-// how many have a larger key.  The key is topk.h's: larger value, then lower
-// index.  Should more values lie above T than the gathering space holds, T is
+// Top k of a wave: a threshold T that at least k values seen reach, and a
+// gathering space in LDS that holds every value seen above T and, of those
+// equal to T, the first ones.  The first chunk's T comes from the 64 lanes' own
+// maxima: a value that k of them reach.  After that only the values above T
+// are gathered (k / j of chunk j on average, for random logits), by ballots; a
+// full space is cut down to its k largest.  Order among the gathered: count,
+// for each, how many have a larger key.  The key is topk.h's: larger value,
+// then lower index.  Should more values lie above T than the space holds, T is
 // raised by bisection over the order of fp32 first.
 #include <algorithm>
 
@@ -34,24 +37,38 @@ namespace {
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));   // rows start at any 4 bytes
 
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr int kGather = 192;   // values above T that a part can gather
+constexpr int kGather = 256;   // keys above T that a wave can gather
+constexpr int kRoom = kGather + kLogprobMaxK;   // with those equal to it
+constexpr int kSlots = (kRoom + 63) / 64;
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-  return v;
+// Reductions over the wave by DPP: within rows of 16 lanes, then across them;
+// lane 63 ends with the result, which every lane gets as a scalar.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float old, float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(old), __float_as_uint(v), CTRL, ROWS, 0xF, false));
 }
-__device__ __forceinline__ float wave_min(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v = fminf(v, __shfl_xor(v, off));
-  return v;
+__device__ __forceinline__ float last_lane(float v) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, dpp<0x111, 0xF>(v, v));   // row_shr 1, 2, 4, 8
+  v = fmaxf(v, dpp<0x112, 0xF>(v, v));
+  v = fmaxf(v, dpp<0x114, 0xF>(v, v));
+  v = fmaxf(v, dpp<0x118, 0xF>(v, v));
+  v = fmaxf(v, dpp<0x142, 0xA>(v, v));   // row_bcast 15 into rows 1 and 3
+  v = fmaxf(v, dpp<0x143, 0xC>(v, v));   // row_bcast 31 into rows 2 and 3
+  return last_lane(v);
 }
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  return v;
+  v += dpp<0x111, 0xF>(0.f, v);
+  v += dpp<0x112, 0xF>(0.f, v);
+  v += dpp<0x114, 0xF>(0.f, v);
+  v += dpp<0x118, 0xF>(0.f, v);
+  v += dpp<0x142, 0xA>(0.f, v);
+  v += dpp<0x143, 0xC>(0.f, v);
+  return last_lane(v);
 }
 
 __device__ __forceinline__ int lanes_below(uint64_t mask, int lane) {
@@ -68,16 +85,22 @@ __device__ __forceinline__ float of_ord(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 
-// The k-th largest of the 64 lanes' values (k <= 64): the least value that
-// fewer than k lanes exceed.
-__device__ __forceinline__ float kth_of_lanes(float v, int k) {
-  int above = 0;
-#pragma unroll
-  for (int j = 0; j < 64; ++j) {
-    const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), j));
-    above += o > v ? 1 : 0;
+// A bound that at least k lanes' values reach (k <= 64) and, unless values are
+// alike, not many more: bisection over unsigned order between 0, which all
+// reach, and past the largest.
+__device__ __forceinline__ uint32_t reached_by_k(uint32_t v, uint32_t top, int k) {
+  uint32_t lo = 0, hi = top;
+  if (__popcll(__ballot(v >= top)) >= k) return top;
+  while (hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    const int c = __popcll(__ballot(v >= mid));
+    if (c < k) hi = mid;
+    else {
+      lo = mid;
+      if (c <= k + k / 4 + 1) break;
+    }
   }
-  return wave_min(above < k ? v : __builtin_inff());
+  return lo;
 }
 
 // How many of the wave's values are above T.
@@ -91,230 +114,384 @@ __device__ __forceinline__ int count_above(const f32x4 (&v)[NQ], float T) {
   return c;
 }
 
-}  // namespace
-
-template <int NQ>
-__global__ __launch_bounds__(256) void k_logprob_part(LogprobArgs a) {
-  __shared__ uint64_t gath[4][kGather + kLogprobMaxK];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
-  if (unit >= (int64_t)a.M * a.parts) return;   // whole waves; no barrier below
-  const int m_row = (int)(unit / a.parts), part = (int)(unit - (int64_t)m_row * a.parts);
-  const float* row = a.y + (size_t)m_row * a.ldy;
-  const int i0 = part * (256 * NQ) + 4 * lane;   // index of v[q][c]: i0 + 256 q + c
-  f32x4 v[NQ];
-  if ((part + 1) * (256 * NQ) <= a.n) {
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) v[q] = *reinterpret_cast<const f32x4u*>(row + i0 + 256 * q);
-  } else {
-#pragma unroll
-    for (int q = 0; q < NQ; ++q)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[q][c] = i0 + 256 * q + c < a.n ? row[i0 + 256 * q + c] : neg_inf();
-  }
-  // NaNs are passed over: a maximum takes the other operand, comparisons are
-  // false, and the clamp of d below turns them into nothing.
-  float qm[NQ], lm = neg_inf();
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    qm[q] = fmaxf(fmaxf(v[q][0], v[q][1]), fmaxf(v[q][2], v[q][3]));
-    lm = fmaxf(lm, qm[q]);
-  }
-  const float m = wave_max(lm);
-  uint64_t* keys = a.keys + (size_t)unit * a.k;
-  if (m == neg_inf()) {   // nothing left in this part
-    if (lane == 0) a.stats[unit] = f32x4{m, 0.f, 0.f, 0.f};
-    if (lane < a.k) keys[lane] = 0;
-    return;
-  }
-
-  if (a.k > 0) {
-    uint64_t* g = gath[wave];
-    float T = kth_of_lanes(lm, a.k);
-    int n_above;
-    for (;;) {
-      n_above = 0;
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        if (__ballot(qm[q] > T) == 0) continue;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint64_t b = __ballot(v[q][c] > T);
-          const int at = n_above + lanes_below(b, lane);
-          if (v[q][c] > T && at < kGather) g[at] = topk_key(v[q][c], i0 + 256 * q + c);
-          n_above += __popcll(b);
-        }
-      }
-      if (n_above <= kGather) break;
-      // raise T: more than kGather values above lo, fewer than k above hi
-      uint32_t lo = ord_of(T), hi = ord_of(m);
-      while (hi - lo > 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        const int c = count_above(v, of_ord(mid));
-        if (c > kGather) lo = mid;
-        else {
-          hi = mid;
-          if (c >= a.k) break;
-        }
-      }
-      T = of_ord(hi);
-    }
-    // ties at T, the lowest indexes first
-    int n_all = n_above;
-    if (n_above < a.k && T > neg_inf()) {
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        if (n_all >= a.k) continue;
-        uint64_t b[4];
-        int before = 0, all = 0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          b[c] = __ballot(v[q][c] == T);
-          before += lanes_below(b[c], lane);
-          all += __popcll(b[c]);
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (v[q][c] == T) {
-            if (n_all + before < a.k) g[n_all + before] = topk_key(v[q][c], i0 + 256 * q + c);
-            ++before;
-          }
-        n_all = min(n_all + all, a.k);
-      }
-    }
-    // The wave's own LDS writes and reads run in order; the fence keeps the
-    // compiler from moving them.
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    for (int e0 = 0; e0 < n_all; e0 += 64) {
-      const uint64_t mine = e0 + lane < n_all ? g[e0 + lane] : 0;
-      int above = 0;
-      for (int j = 0; j < n_all; ++j) above += g[j] > mine ? 1 : 0;
-      if (mine && above < a.k) keys[above] = mine;
-    }
-    if (lane >= n_all && lane < a.k) keys[lane] = 0;
-  }
-
-  float rest = 0.f, t = 0.f;
-  int n_max = 0;   // values equal to m: all but one of them count 1 in rest, and 0 in t
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    const bool has_max = __ballot(qm[q] == m) != 0;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      // exp(-200) is 0 in fp32: the clamp changes no sum and keeps -inf and NaN out of e * d
-      const float d = fmaxf(v[q][c] - m, -200.f);
-      float e = __builtin_amdgcn_exp2f(d * kLog2e);
-      if (has_max) {
-        n_max += __popcll(__ballot(v[q][c] == m));
-        e = v[q][c] == m ? 0.f : e;
-      }
-      rest += e;
-      t = fmaf(e, d, t);
-    }
-  }
-  rest = wave_sum(rest) + (float)(n_max - 1);
-  t = wave_sum(t);
-  if (lane == 0) a.stats[unit] = f32x4{m, rest, t, 0.f};
+// Orders a wave's LDS writes before its reads that follow, and the other way
+// round: a wave's LDS operations run in order, the compiler must keep them so.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
-// Joins the parts of a row, one wave a row.  The top k of the row: lane l owns
-// the lists of parts l, l + 64, ...; T, the k-th largest of the lanes' best
-// keys, is at most the row's k-th key, and at most k lanes reach it, so at most
-// k * k keys of each of their lists have to be gathered (kLogprobLists lists a
-// lane at most: the host sizes the LDS for it) and ordered by counting.
+// How many of the n keys at g (padded with zeros to a multiple of 8) are larger than `key`.
+__device__ __forceinline__ int larger_keys(const uint64_t* g, int n, uint64_t key) {
+  int c = 0;
+  for (int j = 0; j < n; j += 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c += g[j + i] > key ? 1 : 0;
+  }
+  return c;
+}
+
+// The largest min(k, n) of the n keys at g, in decreasing order, to out (LDS:
+// g itself, or memory).  Returns the last of them when n >= k (else 0).
+__device__ __forceinline__ uint64_t select_k(uint64_t* g, int n, int k, int lane, uint64_t* out) {
+  if (lane < 8) g[n + lane] = 0;
+  wave_lds_fence();
+  uint64_t mine[kSlots];
+  int at[kSlots];
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    mine[i] = 0;
+    at[i] = k;
+    if (64 * i < n) {
+      mine[i] = 64 * i + lane < n ? g[64 * i + lane] : 0;
+      at[i] = larger_keys(g, n, mine[i]);
+    }
+  }
+  wave_lds_fence();
+  uint64_t kth = 0;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    if (mine[i] != 0 && at[i] < k) out[at[i]] = mine[i];
+    const uint64_t b = __ballot(mine[i] != 0 && at[i] == k - 1);
+    if (b) {
+      const int l = __builtin_ctzll(b);
+      kth = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(mine[i] >> 32), l) << 32) |
+            (uint32_t)__builtin_amdgcn_readlane((uint32_t)mine[i], l);
+    }
+  }
+  wave_lds_fence();
+  return kth;
+}
+
+__device__ __forceinline__ uint64_t raw_key(float v, int i) {
+  return ((uint64_t)__float_as_uint(v) << 32) | ~(uint32_t)i;
+}
+
+// The running state of a wave.
+struct TopState {
+  int n;     // gathered keys
+  float T;   // at least k values seen reach it; -inf before there are k
+};
+
+// Takes a chunk's values (value q, c of lane l has index i0 + 256 q + c, i0
+// with 4 l in it) into the gathered keys.  qm: maxima of the quads, lm: the
+// lane's, cm: the chunk's.
+template <int NQ>
+__device__ __forceinline__ void take_chunk(const f32x4 (&v)[NQ], const float (&qm)[NQ], float lm, float cm, int i0,
+                                           int k, int lane, uint64_t* g, TopState& st) {
+  const bool fresh = st.T == neg_inf();   // fewer than k so far: this chunk's own bound
+  float T = st.T;
+  if (fresh) {
+    const uint32_t o = k == 1 ? ord_of(cm) : reached_by_k(ord_of(lm), ord_of(cm), k);
+    T = o <= ord_of(neg_inf()) ? neg_inf() : of_ord(o);
+  }
+  // Gathered as (value bits, ~index) and made into keys afterwards: the few
+  // that are there, not every value.
+  int n;
+  for (;;) {
+    n = st.n;
+    int i1 = i0;
+    asm volatile("" : "+v"(i1));   // keeps the indexes of all values from being held through the loop
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      if (__ballot(qm[q] > T) == 0) continue;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint64_t b = __ballot(v[q][c] > T);
+        const int at = n + lanes_below(b, lane);
+        if (v[q][c] > T && at < kGather) g[at] = raw_key(v[q][c], i1 + 256 * q + c);
+        n += __popcll(b);
+      }
+    }
+    if (n <= kGather) break;
+    if (st.n > k) {   // make room
+      const uint64_t kth = select_k(g, st.n, k, lane, g);
+      st.n = k;
+      T = fmaxf(T, of_ord((uint32_t)(kth >> 32)));
+      continue;
+    }
+    // more above T than there is room for: raise it
+    uint32_t lo = ord_of(T), hi = ord_of(cm);
+    while (hi - lo > 1) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      const int c = count_above(v, of_ord(mid));
+      if (c > kGather - k) lo = mid;
+      else {
+        hi = mid;
+        if (c >= k) break;
+      }
+    }
+    T = of_ord(hi);
+  }
+  // fewer than k of this chunk above its own bound: those equal to it, the lowest indexes first
+  if (T != st.T && T > neg_inf()) {
+    int need = k - (n - st.n);
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      if (need <= 0) continue;
+      uint64_t b[4];
+      int before = 0, all = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        b[c] = __ballot(v[q][c] == T);
+        before += lanes_below(b[c], lane);
+        all += __popcll(b[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (v[q][c] == T) {
+          if (before < need) g[n + before] = raw_key(v[q][c], i0 + 256 * q + c);
+          ++before;
+        }
+      n += min(all, need);
+      need -= all;
+    }
+  }
+  wave_lds_fence();
+  for (int e = st.n + lane; e < n; e += 64) g[e] = topk_key(__uint_as_float((uint32_t)(g[e] >> 32)), ~(uint32_t)g[e]);
+  st.n = n;
+  st.T = T;
+}
+
+}  // namespace
+
+// The chunk whose value q, c of lane l has index i0 + 256 q + c (4 l in i0), -inf
+// from `end` on.  A group that crosses the end is read from the last four
+// logits before it (in a row of fewer than four, the first again and again)
+// and moved down.
+template <int NQ>
+__device__ __forceinline__ void load_chunk(const float* row, int end, int i0, bool whole, f32x4 (&v)[NQ]) {
+  if (whole) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) v[q] = *reinterpret_cast<const f32x4u*>(row + i0 + 256 * q);
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    const int i = i0 + 256 * q, from = min(i, end - 4);
+    const int by = i - from;   // 0: as it lies; 4 and up: nothing left
+    if (end >= 4) {
+      v[q] = *reinterpret_cast<const f32x4u*>(row + from);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[q][c] = row[max(0, from + c)];
+    }
+    const float n = neg_inf();
+    const f32x4 o = v[q];
+    v[q][0] = by == 0 ? o[0] : by == 1 ? o[1] : by == 2 ? o[2] : by == 3 ? o[3] : n;
+    v[q][1] = by == 0 ? o[1] : by == 1 ? o[2] : by == 2 ? o[3] : n;
+    v[q][2] = by == 0 ? o[2] : by == 1 ? o[3] : n;
+    v[q][3] = by == 0 ? o[3] : n;
+  }
+}
+
+#ifndef Q4NX_LP_OCC
+#define Q4NX_LP_OCC
+#endif
+template <int NQ>
+__global__ __launch_bounds__(256 Q4NX_LP_OCC) void k_logprob_part(LogprobArgs a) {
+  constexpr int kChunk = 256 * NQ;
+  __shared__ uint64_t gath[4][kRoom + 8];
+  // the wave's number as a scalar: rows, bounds and branches then are scalar too
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const uint32_t unit = blockIdx.x * 4 + wave;
+  if (unit >= (uint32_t)a.M * a.parts) return;   // no barrier below
+  const int m_row = unit / (uint32_t)a.parts, part = unit - (uint32_t)m_row * a.parts;
+  const float* row = a.y + (size_t)m_row * a.ldy;
+  const int begin = part * a.part_n, end = min(a.n, begin + a.part_n);
+  uint64_t* g = gath[wave];
+  TopState st = {0, neg_inf()};
+  float m = neg_inf(), rest = 0.f, t = 0.f;   // rest, t: this lane's share, but for the one maximum set apart
+  for (int c0 = begin; c0 < end; c0 += kChunk) {
+    f32x4 v[NQ];
+    load_chunk<NQ>(row, end, c0 + 4 * lane, c0 + kChunk <= end, v);
+    // NaNs are passed over: a maximum takes the other operand, comparisons are
+    // false, and the clamp of d below turns them into nothing.
+    float qm[NQ], lm = neg_inf();
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      qm[q] = fmaxf(fmaxf(v[q][0], v[q][1]), fmaxf(v[q][2], v[q][3]));
+      lm = fmaxf(lm, qm[q]);
+    }
+    const float cm = wave_max(lm);
+    if (cm == neg_inf()) continue;   // nothing left in this chunk
+    if (a.k > 0 && cm > st.T) take_chunk<NQ>(v, qm, lm, cm, c0 + 4 * lane, a.k, lane, g, st);
+    // exp(-200) is 0 in fp32: the clamp changes no sum and keeps -inf and NaN out of e * d
+    if (cm >= m) {
+      if (cm > m && m != neg_inf()) {   // the old maximum joins the rest
+        const float d = fmaxf(m - cm, -200.f), f = __builtin_amdgcn_exp2f(d * kLog2e);
+        rest += lane == 0 ? 1.f : 0.f;
+        t = f * fmaf(rest, d, t);
+        rest *= f;
+      }
+      int same = cm > m ? -1 : 0;   // values equal to the maximum, but for the one set apart
+      m = cm;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const bool is = v[q][c] == m;
+          same += __popcll(__ballot(is));
+          const float d = fmaxf(v[q][c] - m, -200.f);
+          const float e = is ? 0.f : __builtin_amdgcn_exp2f(d * kLog2e);
+          rest += e;
+          t = fmaf(e, d, t);
+        }
+      rest += lane == 0 ? (float)same : 0.f;
+    } else {
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float d = fmaxf(v[q][c] - m, -200.f);
+          const float e = __builtin_amdgcn_exp2f(d * kLog2e);
+          rest += e;
+          t = fmaf(e, d, t);
+        }
+    }
+  }
+  rest = wave_sum(rest);
+  t = wave_sum(t);
+  if (lane == 0) a.stats[unit] = f32x4{m, rest, t, 0.f};
+  if (a.k > 0) {
+    uint64_t* keys = a.keys + (size_t)unit * a.k;
+    select_k(g, st.n, a.k, lane, keys);
+    if (lane >= st.n && lane < a.k) keys[lane] = 0;
+  }
+}
+
+// Joins the parts of a row, one wave a row.  Lane l owns parts l, l + 64, ...
+// (four at most) and loads the first four keys of each of their lists ahead.
+// The row's top k: T, a key that at least k known keys reach, is at most the
+// row's k-th, so the keys of at least T are gathered from the lists (in
+// decreasing order each: a list ends at its first smaller key) and ordered by
+// counting.  The known keys are the lanes' best ones where every lane has a
+// list, else (fewer than 64 parts, of which k may be more than there are) the
+// loaded ones.  At most k + k / 4 + 1 of them reach T: so many lanes' lists whole,
+// or so many keys and what follows the fours among them, bound the room.
+constexpr int kFirst = 4;
+inline int join_room(int parts, int k) {
+  const int reach = k + k / 4 + 1;
+  return parts >= 64 ? std::min(64, reach) * ((parts + 63) / 64) * k : reach + reach / kFirst * std::max(0, k - kFirst);
+}
+
 __global__ __launch_bounds__(64) void k_logprob_join(LogprobArgs a) {
-  extern __shared__ uint64_t g[];
-  const int m_row = blockIdx.x, lane = threadIdx.x;
+  extern __shared__ uint64_t g[];   // join_room keys and 8
+  const int m_row = blockIdx.x, lane = threadIdx.x, k = a.k;
   const float* row = a.y + (size_t)m_row * a.ldy;
   const size_t u0 = (size_t)m_row * a.parts;
-  float m = neg_inf(), rest = 0.f, t = 0.f;
-  auto join = [&](float m2, float rest2, float t2) {
-    if (m2 == neg_inf()) return;
-    if (m == neg_inf()) { m = m2; rest = rest2; t = t2; return; }
-    const bool up = m2 > m;
-    const float d = fmaxf(up ? m - m2 : m2 - m, -200.f);   // of equal maxima (also +inf) 0
-    const float dd = m == m2 ? 0.f : d;
-    const float f = __builtin_amdgcn_exp2f(dd * kLog2e);
-    const float rl = up ? rest : rest2, tl = up ? t : t2;      // the lower part
-    const float rh = up ? rest2 : rest, th = up ? t2 : t;
-    rest = rh + (1.f + rl) * f;
-    t = th + f * (tl + (1.f + rl) * dd);
-    m = up ? m2 : m;
-  };
-  uint64_t best = 0;
-  for (int p = lane; p < a.parts; p += 64) {
-    const f32x4 s = a.stats[u0 + p];
-    join(s[0], s[1], s[2]);
-    if (a.k > 0) {
-      const uint64_t h = a.keys[(u0 + p) * a.k];
-      best = h > best ? h : best;
+  // everything whose place is known, in flight at once
+  const int tok = lane < a.n_tok ? a.tokens[(size_t)m_row * a.n_tok + lane] : -1;
+  f32x4 s[4];
+  uint64_t key[4][kFirst];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int p = lane + 64 * i;
+    s[i] = f32x4{neg_inf(), 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kFirst; ++j) key[i][j] = 0;
+    if (p < a.parts) {
+      s[i] = a.stats[u0 + p];
+#pragma unroll
+      for (int j = 0; j < kFirst; ++j)
+        if (j < k) key[i][j] = a.keys[(u0 + p) * k + j];
     }
+  }
+  const bool inside = tok >= 0 && tok < a.n;
+  const float yt = inside ? row[tok] : 0.f;
+
+  const float m = wave_max(fmaxf(fmaxf(s[0][0], s[1][0]), fmaxf(s[2][0], s[3][0])));
+  const bool left = m != neg_inf();
+  float rest = 0.f, t = 0.f;
+  bool apart = false;   // one part with the row's maximum has been met (in part order within a lane, lanes in order)
+  {
+    bool has = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) has |= s[i][0] == m;
+    const uint64_t b = __ballot(has);
+    apart = b == 0 || lane != __builtin_ctzll(b);
   }
 #pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    // both lanes of a pair join the lower lane's side first, so they end with the same bits
-    const float om = __shfl_xor(m, off), orr = __shfl_xor(rest, off), ot = __shfl_xor(t, off);
-    if (lane & off) {
-      const float m2 = m, r2 = rest, t2 = t;
-      m = om; rest = orr; t = ot;
-      join(m2, r2, t2);
-    } else {
-      join(om, orr, ot);
-    }
+  for (int i = 0; i < 4; ++i) {
+    if (s[i][0] == neg_inf()) continue;
+    const bool is = s[i][0] == m;
+    const float d = is ? 0.f : fmaxf(s[i][0] - m, -200.f);
+    const float f = __builtin_amdgcn_exp2f(d * kLog2e);
+    const float one = is && !apart ? 0.f : 1.f;
+    if (is) apart = true;
+    rest += (one + s[i][1]) * f;
+    t += f * fmaf(1.f + s[i][1], d, s[i][2]);
   }
-  const bool left = m != neg_inf();
+  rest = wave_sum(rest);
+  t = wave_sum(t);
   const float lz = log1pf(rest);
   auto logp_of = [&](float v) { return (v == m ? 0.f : v - m) - lz; };
-  for (int c = lane; c < a.n_tok; c += 64) {
-    const int tok = a.tokens[(size_t)m_row * a.n_tok + c];
+  if (lane < a.n_tok) {
     float lp = __builtin_nanf("");
-    if (left && tok >= 0 && tok < a.n) {
-      const float v = row[tok];
-      lp = v == v ? logp_of(v) : neg_inf();
-    }
-    a.logp[(size_t)m_row * a.n_tok + c] = lp;
+    if (left && inside) lp = yt == yt ? logp_of(yt) : neg_inf();
+    a.logp[(size_t)m_row * a.n_tok + lane] = lp;
   }
   if (a.entropy && lane == 0) a.entropy[m_row] = left ? lz - t / (1.f + rest) : __builtin_nanf("");
-  if (a.k == 0) return;
+  if (k == 0) return;
 
-  int above = 0;
-#pragma unroll 16
-  for (int j = 0; j < 64; ++j) {
-    const uint64_t o = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(best >> 32), j) << 32) |
-                       (uint32_t)__builtin_amdgcn_readlane((uint32_t)best, j);
-    above += o > best ? 1 : 0;
-  }
-  uint64_t T = above < a.k ? best : ~0ull;
+  const int lists = (a.parts + 63) / 64;
+  uint64_t best = 0;
 #pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const uint64_t o = __shfl_xor(T, off);
-    T = o < T ? o : T;
-  }
-  int n_all = 0;
-  for (int p0 = 0; p0 < a.parts; p0 += 64) {
-    const uint64_t* list = a.keys + (u0 + min(p0 + lane, a.parts - 1)) * a.k;
-    const bool own = p0 + lane < a.parts && best >= T;
-    for (int s = 0; s < a.k; ++s) {
-      const uint64_t key = own ? list[s] : 0;
-      const uint64_t b = __ballot(key != 0 && key >= T);
-      if (b == 0) break;
-      if (key != 0 && key >= T) g[n_all + lanes_below(b, lane)] = key;
-      n_all += __popcll(b);
+  for (int i = 0; i < 4; ++i) best = key[i][0] > best ? key[i][0] : best;
+  const bool by_lane = a.parts >= 64;
+  const uint64_t top = wave_max_u64(best);
+  uint64_t T = k == 1 ? top : 0;
+  for (uint64_t hi = k == 1 ? 0 : top + 1; hi > T + 1;) {   // fewer than k reach hi
+    const uint64_t mid = T + (hi - T) / 2;
+    int c = __popcll(__ballot((by_lane ? best : key[0][0]) >= mid));
+    if (!by_lane) {
+#pragma unroll
+      for (int j = 1; j < kFirst; ++j) c += __popcll(__ballot(key[0][j] >= mid));
+    }
+    if (c < k) hi = mid;
+    else {
+      T = mid;
+      if (c <= k + k / 4 + 1) break;
     }
   }
-  __syncthreads();
-  const size_t o0 = (size_t)m_row * a.k;
-  for (int e0 = 0; e0 < n_all; e0 += 64) {
-    const uint64_t mine = e0 + lane < n_all ? g[e0 + lane] : 0;
-    int larger = 0;
-    for (int j = 0; j < n_all; ++j) larger += g[j] > mine ? 1 : 0;
-    if (mine && larger < a.k) {
-      a.top_ids[o0 + larger] = (int32_t)~(uint32_t)mine;
-      if (a.top_logp) a.top_logp[o0 + larger] = logp_of(of_ord((uint32_t)(mine >> 32)));
+  int n = 0;
+  auto add = [&](uint64_t v) {
+    const bool in = v != 0 && v >= T;
+    const uint64_t b = __ballot(in);
+    const int at = n + lanes_below(b, lane);
+    if (in) g[at] = v;
+    n += __popcll(b);
+    return b;
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i >= lists) continue;
+    uint64_t b = 0;
+#pragma unroll
+    for (int j = 0; j < kFirst; ++j) b = add(key[i][j]);
+    const uint64_t* list = a.keys + (u0 + min(lane + 64 * i, a.parts - 1)) * k;
+    bool mine = key[i][kFirst - 1] != 0 && key[i][kFirst - 1] >= T;
+    for (int j0 = kFirst; b != 0 && j0 < k; j0 += kFirst) {
+      uint64_t v[kFirst];
+#pragma unroll
+      for (int j = 0; j < kFirst; ++j) v[j] = mine && j0 + j < k ? list[j0 + j] : 0;
+#pragma unroll
+      for (int j = 0; j < kFirst; ++j) b = add(v[j]);
+      mine = v[kFirst - 1] != 0 && v[kFirst - 1] >= T;
     }
   }
-  if (lane >= n_all && lane < a.k) {
+  if (lane < 8) g[n + lane] = 0;
+  wave_lds_fence();
+  const size_t o0 = (size_t)m_row * k;
+  for (int e0 = 0; e0 < n; e0 += 64) {
+    const uint64_t mine = e0 + lane < n ? g[e0 + lane] : 0;
+    const int at = larger_keys(g, n, mine);
+    if (mine && at < k) {
+      a.top_ids[o0 + at] = (int32_t)~(uint32_t)mine;
+      if (a.top_logp) a.top_logp[o0 + at] = logp_of(of_ord((uint32_t)(mine >> 32)));
+    }
+  }
+  if (lane >= n && lane < k) {
     a.top_ids[o0 + lane] = -1;
     if (a.top_logp) a.top_logp[o0 + lane] = __builtin_nanf("");
   }
@@ -323,12 +500,11 @@ __global__ __launch_bounds__(64) void k_logprob_join(LogprobArgs a) {
 hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t s) {
   const int64_t units = (int64_t)a.M * a.parts;
   const dim3 grid((unsigned)((units + 3) / 4));
-  if (a.part_n == 1024)
+  if (a.part_n < kLogprobChunk)
     hipLaunchKernelGGL((k_logprob_part<4>), grid, dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((k_logprob_part<16>), grid, dim3(256), 0, s, a);
-  const size_t lds = (size_t)std::min(a.k, 64) * ((a.parts + 63) / 64) * a.k * sizeof(uint64_t);
-  hipLaunchKernelGGL(k_logprob_join, dim3(a.M), dim3(64), lds, s, a);
+    hipLaunchKernelGGL((k_logprob_part<kLogprobChunk / 256>), grid, dim3(256), 0, s, a);
+  hipLaunchKernelGGL(k_logprob_join, dim3(a.M), dim3(64), (join_room(a.parts, a.k) + 8) * sizeof(uint64_t), s, a);
   return hipGetLastError();
 }
 

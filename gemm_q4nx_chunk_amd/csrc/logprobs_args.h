@@ -24,11 +24,23 @@ struct LogprobArgs {
   uint64_t* keys;          // [M][parts][k], decreasing, 0 past the last
 };
 
-// Logits of a part: 4096 (a wave's 64 registers a lane) where that makes
-// enough waves to fill the GPU, else 1024.
+constexpr int kLogprobChunk = 2048;    // logits that a wave holds in registers at a time
+#ifndef Q4NX_LP_WAVES
+#define Q4NX_LP_WAVES 16384
+#endif
+#ifndef Q4NX_LP_SMALL
+#define Q4NX_LP_SMALL 2048
+#endif
+
+// Logits of a part.  Few waves: 1024 in one go.  Else whole chunks, as many as
+// leave about 16384 waves.
 inline int logprob_part_n(int n, int M) {
-  const int64_t waves = (int64_t)M * ((n + 4095) / 4096);
-  return waves < 1024 && n <= kLogprobMaxParts * 1024 ? 1024 : 4096;
+  if ((int64_t)M * ((n + 1023) / 1024) <= Q4NX_LP_SMALL && n <= kLogprobMaxParts * 1024) return 1024;
+  const int chunks = (n + kLogprobChunk - 1) / kLogprobChunk;
+  int parts = Q4NX_LP_WAVES / M;
+  parts = parts < 1 ? 1 : parts > chunks ? chunks : parts;
+  parts = parts > kLogprobMaxParts ? kLogprobMaxParts : parts;
+  return (chunks + parts - 1) / parts * kLogprobChunk;
 }
 
 // Workspace: the parts' stats, then their keys.

@@ -2,7 +2,7 @@
 
 Picks are on fp32 values on both sides: equal.  Sums: an exponential carries
 2^-23 relative (one unit of the instruction) and the roundings of its exponent,
-3 |d| 2^-24 with d = y - max; a value passes at most 64 additions in its lane, 12
+3 |d| 2^-24 with d = y - max; a value passes at most 160 additions in its lane, 12
 in the wave's and rows' trees and, joined with other parts, the exponentials of
 six levels and of up to four parts a lane, whose distances add up to its own.  So rest is off by at most
   r = 2^-23 (120 + 3 spread)  relative to 1 + rest,  spread = sum p |d|,

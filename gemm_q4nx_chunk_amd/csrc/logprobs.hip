@@ -39,7 +39,7 @@ typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));   // rows 
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr int kGather = 256;   // keys above T that a wave can gather
 constexpr int kRoom = kGather + kLogprobMaxK;   // with those equal to it
-constexpr int kSlots = (kRoom + 63) / 64;
+constexpr int kGatherLds = kRoom + 4 + kLogprobMaxK;   // with the padding, and the best of them when cut down
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
@@ -121,46 +121,27 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// How many of the n keys at g (padded with zeros to a multiple of 8) are larger than `key`.
+// How many of the n keys at g (padded with zeros to a multiple of 4) are larger than `key`.
 __device__ __forceinline__ int larger_keys(const uint64_t* g, int n, uint64_t key) {
   int c = 0;
-  for (int j = 0; j < n; j += 8) {
+  for (int j = 0; j < n; j += 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c += g[j + i] > key ? 1 : 0;
+    for (int i = 0; i < 4; ++i) c += g[j + i] > key ? 1 : 0;
   }
   return c;
 }
 
-// The largest min(k, n) of the n keys at g, in decreasing order, to out (LDS:
-// g itself, or memory).  Returns the last of them when n >= k (else 0).
-__device__ __forceinline__ uint64_t select_k(uint64_t* g, int n, int k, int lane, uint64_t* out) {
-  if (lane < 8) g[n + lane] = 0;
+// The largest min(k, n) of the n keys at g, in decreasing order, to out (not g).
+// One piece of 64 at a time, so that few registers are held beside the chunk's.
+__device__ __forceinline__ void select_k(uint64_t* g, int n, int k, int lane, uint64_t* out) {
+  if (lane < 4) g[n + lane] = 0;
   wave_lds_fence();
-  uint64_t mine[kSlots];
-  int at[kSlots];
-#pragma unroll
-  for (int i = 0; i < kSlots; ++i) {
-    mine[i] = 0;
-    at[i] = k;
-    if (64 * i < n) {
-      mine[i] = 64 * i + lane < n ? g[64 * i + lane] : 0;
-      at[i] = larger_keys(g, n, mine[i]);
-    }
+#pragma unroll 1
+  for (int e = lane; e - lane < n; e += 64) {
+    const uint64_t mine = e < n ? g[e] : 0;
+    const int at = larger_keys(g, n, mine);
+    if (mine != 0 && at < k) out[at] = mine;
   }
-  wave_lds_fence();
-  uint64_t kth = 0;
-#pragma unroll
-  for (int i = 0; i < kSlots; ++i) {
-    if (mine[i] != 0 && at[i] < k) out[at[i]] = mine[i];
-    const uint64_t b = __ballot(mine[i] != 0 && at[i] == k - 1);
-    if (b) {
-      const int l = __builtin_ctzll(b);
-      kth = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(mine[i] >> 32), l) << 32) |
-            (uint32_t)__builtin_amdgcn_readlane((uint32_t)mine[i], l);
-    }
-  }
-  wave_lds_fence();
-  return kth;
 }
 
 __device__ __forceinline__ uint64_t raw_key(float v, int i) {
@@ -205,9 +186,13 @@ __device__ __forceinline__ void take_chunk(const f32x4 (&v)[NQ], const float (&q
     }
     if (n <= kGather) break;
     if (st.n > k) {   // make room
-      const uint64_t kth = select_k(g, st.n, k, lane, g);
+      uint64_t* best = g + kRoom + 4;
+      select_k(g, st.n, k, lane, best);
+      wave_lds_fence();
+      if (lane < k) g[lane] = best[lane];
+      wave_lds_fence();
       st.n = k;
-      T = fmaxf(T, of_ord((uint32_t)(kth >> 32)));
+      T = fmaxf(T, of_ord((uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(best[k - 1] >> 32))));
       continue;
     }
     // more above T than there is room for: raise it
@@ -291,7 +276,7 @@ __device__ __forceinline__ void load_chunk(const float* row, int end, int i0, bo
 template <int NQ>
 __global__ __launch_bounds__(256 Q4NX_LP_OCC) void k_logprob_part(LogprobArgs a) {
   constexpr int kChunk = 256 * NQ;
-  __shared__ uint64_t gath[4][kRoom + 8];
+  __shared__ uint64_t gath[4][kGatherLds];
   // the wave's number as a scalar: rows, bounds and branches then are scalar too
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t unit = blockIdx.x * 4 + wave;
@@ -336,6 +321,7 @@ __global__ __launch_bounds__(256 Q4NX_LP_OCC) void k_logprob_part(LogprobArgs a)
           const float e = is ? 0.f : __builtin_amdgcn_exp2f(d * kLog2e);
           rest += e;
           t = fmaf(e, d, t);
+          if (c == 3) __builtin_amdgcn_sched_barrier(0);
         }
       rest += lane == 0 ? (float)same : 0.f;
     } else {
@@ -347,6 +333,7 @@ __global__ __launch_bounds__(256 Q4NX_LP_OCC) void k_logprob_part(LogprobArgs a)
           const float e = __builtin_amdgcn_exp2f(d * kLog2e);
           rest += e;
           t = fmaf(e, d, t);
+          if (c == 3) __builtin_amdgcn_sched_barrier(0);
         }
     }
   }
@@ -376,7 +363,7 @@ inline int join_room(int parts, int k) {
 }
 
 __global__ __launch_bounds__(64) void k_logprob_join(LogprobArgs a) {
-  extern __shared__ uint64_t g[];   // join_room keys and 8
+  extern __shared__ uint64_t g[];   // join_room keys and 4
   const int m_row = blockIdx.x, lane = threadIdx.x, k = a.k;
   const float* row = a.y + (size_t)m_row * a.ldy;
   const size_t u0 = (size_t)m_row * a.parts;
@@ -480,7 +467,7 @@ __global__ __launch_bounds__(64) void k_logprob_join(LogprobArgs a) {
       mine = v[kFirst - 1] != 0 && v[kFirst - 1] >= T;
     }
   }
-  if (lane < 8) g[n + lane] = 0;
+  if (lane < 4) g[n + lane] = 0;
   wave_lds_fence();
   const size_t o0 = (size_t)m_row * k;
   for (int e0 = 0; e0 < n; e0 += 64) {
@@ -504,7 +491,7 @@ hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_logprob_part<4>), grid, dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((k_logprob_part<kLogprobChunk / 256>), grid, dim3(256), 0, s, a);
-  hipLaunchKernelGGL(k_logprob_join, dim3(a.M), dim3(64), (join_room(a.parts, a.k) + 8) * sizeof(uint64_t), s, a);
+  hipLaunchKernelGGL(k_logprob_join, dim3(a.M), dim3(64), (join_room(a.parts, a.k) + 4) * sizeof(uint64_t), s, a);
   return hipGetLastError();
 }
 

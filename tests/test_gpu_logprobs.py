@@ -241,3 +241,26 @@ def test_same_bits_every_time():
     a, b = _run(y, n, tokens, 20), _run(y, n, tokens, 20)
     for name in a:
         np.testing.assert_array_equal(a[name], b[name])
+
+
+@pytest.mark.parametrize("k", [1, 7, 32])
+def test_waves_that_take_many_chunks(k):
+    """Enough rows that a wave streams several chunks of its row: rising, falling, level, masked at the
+    start, and runs whose values keep passing the k-th so far."""
+    M, n = 3000, 20001
+    g = np.random.default_rng(11)
+    y = (2 * g.standard_normal((8, n))).astype(np.float32)
+    y[0].sort()
+    y[1] = np.sort(y[1])[::-1]
+    y[2] = 1.25
+    y[3, :9000] = -np.inf
+    y[4, ::2] = np.arange(0, n, 2) / 1000
+    y[5] = np.floor(np.arange(n) / 300)
+    y[6, :] = np.finfo(np.float32).min
+    y[6, n - 5:] = 3
+    big = np.tile(y, (M // 8, 1))
+    tokens = np.full((M, 1), n - 2, np.int32)
+    got = _run(big, n, tokens, k)
+    _check(got, big, n, tokens, k, rows=range(8))
+    for name in ("logp", "entropy", "top_ids", "top_logp"):
+        np.testing.assert_array_equal(got[name].reshape(M // 8, 8, -1), np.broadcast_to(got[name][:8].reshape(1, 8, -1), (M // 8, 8, got[name][0].size)))

@@ -1376,11 +1376,32 @@ int check_lora(const q4nx_lora* L, const char* name) {
   return Q4NX_OK;
 }
 
+#ifndef Q4NX_LORA_STEPS
+#define Q4NX_LORA_STEPS 2
+#endif
+#ifndef Q4NX_LORA_FILL
+#define Q4NX_LORA_FILL 256
+#endif
+#ifndef Q4NX_LORA_RANGE
+#define Q4NX_LORA_RANGE 256
+#endif
+#ifndef Q4NX_LORA_RWG
+#define Q4NX_LORA_RWG 512
+#endif
+
 // Launch shape and workspace layout of a call over checked tables.
 struct LoraShape {
   q4nx::LoraArgs a;
   size_t hdr, sorted, tiles, u[q4nx::kLoraMaxJobs], total;
 };
+
+// Rows of one set of launches: the kernels address x and y by 31-bit offsets,
+// so longer calls are cut, each piece after the other with the same workspace.
+int lora_rows(const q4nx_lora* const* L, int n, int M) {
+  int64_t row_bytes = (int64_t)L[0]->cols * 2;
+  for (int i = 0; i < n; ++i) row_bytes = std::max(row_bytes, (int64_t)L[i]->rows * 4);
+  return (int)std::min((int64_t)M, ((int64_t)1 << 31) / row_bytes);
+}
 
 void lora_shape(const q4nx_lora* const* L, int n, int M, LoraShape& sh) {
   memset(&sh, 0, sizeof sh);
@@ -1398,17 +1419,24 @@ void lora_shape(const q4nx_lora* const* L, int n, int M, LoraShape& sh) {
     groups += (L[i]->rank + q4nx::kLoraRankGroup - 1) / q4nx::kLoraRankGroup;
     rows += L[i]->rows;
   }
-  const int units = a.cols / 256;
-  a.split = std::max(1, std::min({512 / (tiles * groups), units, q4nx::kLoraMaxSplit}));
-  a.n_range = 64;
-  while (a.n_range < 1024 && tiles * (rows / (2 * a.n_range)) >= 512) a.n_range *= 2;
+  // Parts of the columns: a wave takes about Q4NX_LORA_STEPS steps.  For many
+  // rows, only as many parts as fill the GPU: every part is a row of u that
+  // the expand reads again for each of its ranges.
+  const int steps = a.cols / q4nx::kLoraStepCols;
+  const int per = q4nx::lora_shrink_waves(M <= q4nx::kLoraWaveRows ? 1 : 4) * Q4NX_LORA_STEPS;
+  a.split = std::max(1, std::min((steps + per - 1) / per, q4nx::kLoraMaxSplit));
+  if (M > q4nx::kLoraWaveRows)
+    a.split = std::max(1, std::min(a.split, Q4NX_LORA_FILL / (std::min(a.max_tiles, 2 * tiles) * groups)));
+  a.n_range = 128;
+  while (a.n_range < Q4NX_LORA_RANGE && tiles * (rows / (2 * a.n_range)) >= Q4NX_LORA_RWG) a.n_range *= 2;
+  while (rows / a.n_range > 32768) a.n_range *= 2;   // grid limit
   int wg = 0;
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   size_t o = 256;
   sh.sorted = o;
-  o = up(o + (size_t)M * 4);
+  o = up(o + (size_t)a.max_tiles * 64 * 4);
   sh.tiles = o;
-  o = up(o + (size_t)q4nx::lora_max_tiles(M, a.n_adapters) * 12);
+  o = up(o + (size_t)a.max_tiles * sizeof(q4nx::LoraTile));
   for (int i = 0; i < n; ++i) {
     a.job[i].wg_begin = wg;
     wg += (L[i]->rows + a.n_range - 1) / a.n_range;
@@ -1461,32 +1489,39 @@ int run_lora(const q4nx_lora_job* jobs, int n, const uint16_t* x, const int32_t*
     L[i] = &j.lora;
   }
   LoraShape sh;
-  lora_shape(L, n, M, sh);
+  const int per = lora_rows(L, n, M);
+  lora_shape(L, n, per, sh);
   if (!ws || ws_bytes < sh.total)
     return fail(Q4NX_E_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", name, ws_bytes, sh.total);
   if (!aligned(ws, 256)) return fail(Q4NX_E_ALIGN, "%s: workspace not 256-byte aligned", name);
   uint8_t* w = static_cast<uint8_t*>(ws);
-  q4nx::LoraArgs& a = sh.a;
-  a.x = x;
-  a.ids = ids;
-  a.hdr = reinterpret_cast<uint32_t*>(w + sh.hdr);
-  a.sorted = reinterpret_cast<int32_t*>(w + sh.sorted);
-  a.tiles = reinterpret_cast<int32_t*>(w + sh.tiles);
-  for (int i = 0; i < n; ++i) {
-    q4nx::LoraJob& j = a.job[i];
-    j.a = L[i]->a;
-    j.b = L[i]->b;
-    j.a_stride = L[i]->a_stride / 2;
-    j.b_stride = L[i]->b_stride / 2;
-    j.scale = L[i]->scale;
-    j.ranks = L[i]->ranks;
-    j.base = jobs[i].base;
-    j.y = jobs[i].y;
-    j.u = reinterpret_cast<float*>(w + sh.u[i]);
-    j.rank = L[i]->rank;
-    j.rows = L[i]->rows;
+  for (int m0 = 0; m0 < M; m0 += per) {
+    if (m0) lora_shape(L, n, std::min(per, M - m0), sh);
+    q4nx::LoraArgs& a = sh.a;
+    a.more = m0 > 0;
+    a.x = x + (size_t)m0 * a.cols;
+    a.ids = ids + m0;
+    a.hdr = reinterpret_cast<uint32_t*>(w + sh.hdr);
+    a.sorted = reinterpret_cast<int32_t*>(w + sh.sorted);
+    a.tiles = reinterpret_cast<q4nx::LoraTile*>(w + sh.tiles);
+    for (int i = 0; i < n; ++i) {
+      q4nx::LoraJob& j = a.job[i];
+      j.a = L[i]->a;
+      j.b = L[i]->b;
+      j.a_stride = L[i]->a_stride / 2;
+      j.b_stride = L[i]->b_stride / 2;
+      j.scale = L[i]->scale;
+      j.ranks = L[i]->ranks;
+      j.base = jobs[i].base + (size_t)m0 * L[i]->rows;
+      j.y = jobs[i].y + (size_t)m0 * L[i]->rows;
+      j.u = reinterpret_cast<float*>(w + sh.u[i]);
+      j.rank = L[i]->rank;
+      j.rows = L[i]->rows;
+    }
+    const hipError_t e = q4nx::launch_lora(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_status(e, name);
   }
-  return hip_status(q4nx::launch_lora(a, static_cast<hipStream_t>(stream)), name);
+  return ok();
 }
 
 }  // namespace
@@ -1498,7 +1533,7 @@ size_t q4nx_lora_batched_ws(const q4nx_lora_job* jobs, int n_jobs, int M) {
   const q4nx_lora* L[q4nx::kLoraMaxJobs];
   for (int i = 0; i < n_jobs; ++i) L[i] = &jobs[i].lora;
   LoraShape sh;
-  lora_shape(L, n_jobs, M, sh);
+  lora_shape(L, n_jobs, lora_rows(L, n_jobs, M), sh);
   return sh.total;
 }
 

@@ -29,51 +29,71 @@ namespace {
 
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 
-// A tile of rows of one adapter.
-struct Tile {
-  int e;      // adapter, -1: rows without one
-  int cnt;    // rows
-  int rank;   // ranks of job j that adapter e uses
-};
+// A buffer offset past every range, also with a column's or output's offset
+// added (ranges are at most 2^31 bytes: the host cuts calls so): such loads give
+// 0, such stores do nothing.
+constexpr uint32_t kOutside = 0x80000000u;
+
+// Keeps the compiler from moving a wave's LDS reads before its writes (which
+// the hardware runs in order) or the other way round.
+__device__ __forceinline__ void lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// A tile of rows of one adapter, the same for the whole workgroup.
+using Tile = LoraTile;
 
 __device__ __forceinline__ int valid_id(const LoraArgs& a, int id) {
   return id >= 0 && id < a.n_adapters ? id : -1;
 }
 
-// Fills rows[0..cnt) and returns the tile of workgroup t (cnt = 0: none).
-// Call with all 256 threads; ends with a barrier.  LIM: most rows of a tile.
-template <int LIM>
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Fills rows[0..cnt) with the tile of workgroup t.  Call with all threads of
+// the workgroup (at least 256).  SUB: 16-row pieces of a tile.
+//   M <= 64 (SUB == 1): every wave finds it by itself, and all write the same
+//     rows: a wave reads what it wrote, no barrier.
+//   M <= 256: a row a thread, the waves' counts meet in LDS.
+//   above: from the route's tables.
+template <int SUB>
 __device__ __forceinline__ Tile find_tile(const LoraArgs& a, int t, int32_t* rows, int32_t* scratch) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int kTile = 16 * SUB;
+  const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6);
   Tile tile;
+  if constexpr (SUB == 1) {
+    const int id = lane < a.M ? a.ids[lane] : 0;
+    tile.e = scalar(valid_id(a, a.ids[t]));
+    const bool same = lane < a.M && valid_id(a, id) == tile.e;
+    const uint64_t b = __ballot(same);
+    const int before = __popcll(b & ((1ull << t) - 1ull)), at = __popcll(b & ((1ull << lane) - 1ull));
+    tile.cnt = before % kTile ? 0 : min(kTile, __popcll(b) - before);   // row t opens a tile, or lies in one
+    if (same && at >= before && at < before + tile.cnt) rows[at - before] = lane;
+    lds_order();
+    return tile;
+  }
   if (a.M > kLoraScanRows) {
-    tile.e = -1;
-    tile.cnt = 0;
-    if (t < (int)a.hdr[1]) {
-      tile.e = a.tiles[3 * t];
-      const int p0 = a.tiles[3 * t + 1];
-      tile.cnt = a.tiles[3 * t + 2];
-      if (tid < tile.cnt) rows[tid] = a.sorted[p0 + tid];
-    }
+    // everything at once: places past the tile's rows hold no row and are not used
+    if (tid < 64) rows[tid] = a.sorted[64 * t + tid];
+    tile.e = scalar(a.tiles[t].e);
+    tile.cnt = scalar(a.tiles[t].cnt);
     __syncthreads();
     return tile;
   }
   // rows with row t's id: how many come before t, and which come from t on
-  const int want = valid_id(a, a.ids[t]);
-  const bool same = tid < a.M && valid_id(a, a.ids[tid < a.M ? tid : 0]) == want;
+  tile.e = scalar(valid_id(a, a.ids[t]));
+  const bool same = tid < a.M && valid_id(a, a.ids[tid < a.M ? tid : 0]) == tile.e;
   const uint64_t b = __ballot(same);
-  const uint64_t below_t = t >= 64 * wave + 64 ? b : t <= 64 * wave ? 0ull : b & ((1ull << (t - 64 * wave)) - 1ull);
-  if (lane == 0) {
+  if (wave < 4 && lane == 0) {
     scratch[wave] = __popcll(b);
-    scratch[4 + wave] = __popcll(below_t);
+    scratch[4 + wave] = t >= 64 * wave + 64 ? __popcll(b) : t <= 64 * wave ? 0 : __popcll(b & ((1ull << (t - 64 * wave)) - 1ull));
   }
   __syncthreads();
-  const int before = scratch[4] + scratch[5] + scratch[6] + scratch[7];
-  const int total = scratch[0] + scratch[1] + scratch[2] + scratch[3];
+  const int before = scalar(scratch[4] + scratch[5] + scratch[6] + scratch[7]);
+  const int total = scalar(scratch[0] + scratch[1] + scratch[2] + scratch[3]);
   int at = __popcll(b & ((1ull << lane) - 1ull));
-  for (int w = 0; w < wave; ++w) at += scratch[w];
-  tile.e = want;
-  tile.cnt = before % LIM ? 0 : min(LIM, total - before);   // row t opens a tile, or belongs to an earlier one
+  for (int w = 0; w < min(wave, 4); ++w) at += scratch[w];
+  tile.cnt = before % kTile ? 0 : min(kTile, total - before);
   if (same && at >= before && at < before + tile.cnt) rows[at - before] = tid;
   __syncthreads();
   return tile;
@@ -81,7 +101,7 @@ __device__ __forceinline__ Tile find_tile(const LoraArgs& a, int t, int32_t* row
 
 __device__ __forceinline__ int used_rank(const LoraJob& j, int e) {
   if (!j.ranks) return j.rank;
-  const int r = j.ranks[e];
+  const int r = scalar(j.ranks[e]);
   return r < 0 ? 0 : r > j.rank ? j.rank : r;
 }
 
@@ -98,7 +118,7 @@ __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast
 __global__ __launch_bounds__(1024) void k_lora_route(LoraArgs a) {
   constexpr int kBins = kLoraMaxAdapters + 1, kPer = (kBins + 1023) / 1024;
   __shared__ int32_t cnt[kPer * 1024], start[kPer * 1024];
-  __shared__ int32_t wsum[2][16];
+  __shared__ int32_t wsum[16];
   __shared__ uint32_t bad;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (tid == 0) bad = 0;
@@ -115,90 +135,131 @@ __global__ __launch_bounds__(1024) void k_lora_route(LoraArgs a) {
       const int id = a.ids[m];
       bin[i] = valid_id(a, id) < 0 ? a.n_adapters : id;
       if (id < -1 || id >= a.n_adapters) atomicOr(&bad, 1u);
-      slot[i] = atomicAdd(&cnt[bin[i]], 1);
     }
+    // A prompt's rows come in runs: the first lanes' bins are counted for all
+    // their lanes at once, what is left lane by lane.
+    slot[i] = -1;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const uint64_t todo = __ballot(bin[i] >= 0 && slot[i] < 0);
+      if (todo == 0) continue;
+      const int b = __builtin_amdgcn_readlane(bin[i], __builtin_ctzll(todo));
+      const uint64_t mine = __ballot(bin[i] == b && slot[i] < 0);
+      int first = 0;
+      if (lane == 0) first = atomicAdd(&cnt[b], __popcll(mine));
+      first = __builtin_amdgcn_readfirstlane(first);
+      if (bin[i] == b && slot[i] < 0) slot[i] = first + __popcll(mine & ((1ull << lane) - 1ull));
+    }
+    if (bin[i] >= 0 && slot[i] < 0) slot[i] = atomicAdd(&cnt[bin[i]], 1);
   }
   __syncthreads();
-  // prefix sums of rows and tiles over the bins, kPer neighbouring bins a thread
-  int c[kPer], rows = 0, tiles = 0;
+  // prefix sum of the tiles over the bins, kPer neighbouring bins a thread
+  int c[kPer], tiles = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     c[i] = cnt[tid * kPer + i];
-    rows += c[i];
     tiles += (c[i] + 63) / 64;
   }
-  int ir = rows, it = tiles;
+  int it = tiles;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const int r = __shfl_up(ir, off), t = __shfl_up(it, off);
-    if (lane >= off) { ir += r; it += t; }
+    const int t = __shfl_up(it, off);
+    if (lane >= off) it += t;
   }
-  if (lane == 63) { wsum[0][wave] = ir; wsum[1][wave] = it; }
+  if (lane == 63) wsum[wave] = it;
   __syncthreads();
-  int r0 = ir - rows, t0 = it - tiles;
-  for (int w = 0; w < wave; ++w) { r0 += wsum[0][w]; t0 += wsum[1][w]; }
-  if (tid == 1023) {
-    a.hdr[0] = bad;
-    a.hdr[1] = (uint32_t)(t0 + tiles);
-  }
+  int t0 = it - tiles;
+  for (int w = 0; w < wave; ++w) t0 += wsum[w];
+  if (tid == 0) a.hdr[0] = (a.more ? a.hdr[0] : 0u) | bad;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = tid * kPer + i;
-    start[e] = r0;
-    for (int k = 0; k < c[i]; k += 64) {
-      a.tiles[3 * t0] = e < a.n_adapters ? e : -1;
-      a.tiles[3 * t0 + 1] = r0 + k;
-      a.tiles[3 * t0 + 2] = min(64, c[i] - k);
-      ++t0;
-    }
-    r0 += c[i];
+    start[e] = t0;
+    for (int k = 0; k < c[i]; k += 64, ++t0)
+      a.tiles[t0] = {e < a.n_adapters ? e : -1, min(64, c[i] - k)};
   }
   __syncthreads();
+  if (tid == 1023) start[0] = t0;   // bin 0 starts at tile 0: its place holds the number of tiles
+  __syncthreads();
+  for (int t = start[0] + tid; t < a.max_tiles; t += 1024) a.tiles[t] = {-1, 0};
 #pragma unroll
   for (int i = 0; i < kRowsPer; ++i)
-    if (bin[i] >= 0) a.sorted[start[bin[i]] + slot[i]] = i * 1024 + tid;
+    if (bin[i] >= 0) {
+      const int t = (bin[i] > 0 ? start[bin[i]] : 0) + slot[i] / 64;
+      a.sorted[64 * t + slot[i] % 64] = i * 1024 + tid;
+    }
 }
 
 // ---------------------------------------------------------------------------
 // shrink
 // ---------------------------------------------------------------------------
 // Workgroup (t, s, z): tile t, part s of the columns, rank group z of up to 16
-// RB ranks.  A wave takes every fourth step of 64 columns, for all ranks and
-// rows of its workgroup: matrix-core tiles of 16 ranks x 16 rows x 32 columns,
-// operands straight from memory (16 lanes read 16 ranks' or rows' next 128
-// bytes, 32 bytes a lane; A and x use the same order of columns within a step).
-// SUB: 16-row pieces of a tile.
-template <int RB, int SUB>
-__global__ __launch_bounds__(256) void k_lora_shrink(LoraArgs a) {
-  __shared__ int32_t rows[16 * SUB], scratch[8];
-  __shared__ f32x4 red[2][RB * SUB][64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// RB ranks.  Its W waves take every W-th step of 64 columns each, for all ranks
+// and rows of the tile: matrix-core tiles of 16 ranks x 16 rows x 32 columns.
+// The matrix cores want lane l to hold row l % 16, but 16 neighbouring lanes
+// that read 16 rows touch 16 cache lines for 256 bytes, so a wave loads a step
+// with eight lanes to a row, a whole 128-byte line, and hands it over through
+// LDS of its own: group c of 8 columns of row r at slot c ^ (r % 8) of the row,
+// which spreads any eight rows over all banks.  No barrier: a wave's LDS
+// operations run in order.  kAhead steps are in flight in registers.
+//
+// Measured (4096 rows, 14336 columns, rank 64; 64 rows of 40 adapters, 9728
+// columns): operands straight from memory 75 and 14 us; 64 bytes of a row at a
+// time through LDS 51 and 12.
+inline size_t lora_shrink_lds(int waves, int blocks, int sub) {
+  return (size_t)waves * blocks * 2048 + (16 * sub + 8) * sizeof(int32_t);
+}
+
+template <int W, int RB, int SUB>
+__global__ __launch_bounds__(64 * W, SUB == 1 ? 4 : 2) void k_lora_shrink(LoraArgs a) {
+  constexpr int kAhead = SUB == 1 && RB <= 2 ? 2 : 1;   // 128 registers a wave, 256 for SUB == 4
+  constexpr int B = RB + SUB;   // 16-row blocks of a step: A's, then x's
+  extern __shared__ u32x4 lds[];   // lora_shrink_lds(W, B, SUB) bytes
+  u32x4(*stage)[B][128] = reinterpret_cast<u32x4(*)[B][128]>(lds);
+  int32_t* rows = reinterpret_cast<int32_t*>(lds + W * B * 128);
+  int32_t* scratch = rows + 16 * SUB;
+  f32x4(*red)[RB][64] = reinterpret_cast<f32x4(*)[RB][64]>(stage);   // after the loop: B > RB, so it fits
+  const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6);
   const int n = lane & 15, h = lane >> 4;
   if (a.M <= kLoraScanRows && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
     const int id = tid < a.M ? a.ids[tid] : -1;
     const int bad = __syncthreads_or(id < -1 || id >= a.n_adapters);
-    if (tid == 0) a.hdr[0] = bad ? 1u : 0u;
+    if (tid == 0) a.hdr[0] = (a.more ? a.hdr[0] : 0u) | (bad ? 1u : 0u);
   }
   int ji = 0;
   for (int i = 1; i < a.n_jobs; ++i)
     if ((int)blockIdx.z >= a.job[i].rg_begin) ji = i;
   const LoraJob& J = a.job[ji];
   const int r0 = ((int)blockIdx.z - J.rg_begin) * kLoraRankGroup;
-  const Tile tile = find_tile<16 * SUB>(a, blockIdx.x, rows, scratch);
+  const Tile tile = find_tile<SUB>(a, blockIdx.x, rows, scratch);
   if (tile.cnt == 0 || tile.e < 0) return;
   const int rank = used_rank(J, tile.e);
   if (r0 >= rank) return;
-  const int n_rb = min(RB, (rank - r0 + 15) / 16), n_sub = (tile.cnt + 15) / 16;
+  const int n_sub = (tile.cnt + 15) / 16;
 
-  // Ranks and rows past the last repeat one that exists: their products land
-  // in rows and columns of the result that nothing reads.
-  const uint16_t* pa[RB];
-  const uint16_t* px[SUB];
+  // Ranks and rows past the last are out of the buffers' range: they read as 0
+  // without touching memory, and so do steps past the last.  No load is under
+  // a branch, so none waits for another.
+  const int lr = lane >> 3, lc = lane & 7;   // a load's row of half a block, its group of 8 columns
+  const uint32_t row_bytes = (uint32_t)a.cols * 2;
+  const uint16_t* pa = J.a + (size_t)tile.e * J.a_stride;
+  const uint32_t na = rank * row_bytes, nx = a.M * row_bytes;
+  uint32_t src[B][2];
 #pragma unroll
-  for (int i = 0; i < RB; ++i)
-    pa[i] = J.a + (size_t)tile.e * J.a_stride + (size_t)min(r0 + 16 * i + n, rank - 1) * a.cols + 16 * h;
+  for (int p = 0; p < 2; ++p) {
 #pragma unroll
-  for (int i = 0; i < SUB; ++i) px[i] = a.x + (size_t)rows[min(16 * i + n, tile.cnt - 1)] * a.cols + 16 * h;
+    for (int i = 0; i < RB; ++i) {
+      const int r = r0 + 16 * i + 8 * p + lr;
+      src[i][p] = r < rank ? r * row_bytes + 16 * lc : kOutside;
+    }
+#pragma unroll
+    for (int i = 0; i < SUB; ++i) {
+      const int r = 16 * i + 8 * p + lr;
+      src[RB + i][p] = r < tile.cnt ? rows[r] * row_bytes + 16 * lc : kOutside;
+    }
+  }
+  const int to = 8 * lr + (lc ^ lr);   // of half 1: 64 further
+  const int from[2] = {8 * n + (h ^ (n & 7)), 8 * n + ((4 + h) ^ (n & 7))};
 
   f32x4 acc[RB][SUB];
 #pragma unroll
@@ -206,61 +267,64 @@ __global__ __launch_bounds__(256) void k_lora_shrink(LoraArgs a) {
 #pragma unroll
     for (int j = 0; j < SUB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int steps = a.cols / kLoraStepCols;
-  const int s0 = (int)((int64_t)steps * blockIdx.y / a.split), s1 = (int)((int64_t)steps * (blockIdx.y + 1) / a.split);
-  for (int s = s0 + wave; s < s1; s += 4) {
-    const int c0 = s * kLoraStepCols;
-    u32x4 va[RB][2], vx[SUB][2];
+  const int s0 = steps * (int)blockIdx.y / a.split, s1 = steps * ((int)blockIdx.y + 1) / a.split;
+  u32x4 in[kAhead][B][2];
+  auto load = [&](u32x4 (&v)[B][2], int s) {
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(pa, s < s1 ? na : 0), rx = make_rsrc(a.x, s < s1 ? nx : 0);
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
-      if (i < n_rb) {
-        va[i][0] = load16(pa[i] + c0);
-        va[i][1] = load16(pa[i] + c0 + 8);
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        v[i][p] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                i < RB ? ra : rx, src[i][p] + s * kLoraStepCols * 2, 0, 0));
+  };
+#pragma unroll
+  for (int p = 0; p < kAhead; ++p) load(in[p], s0 + wave + p * W);
+  for (int s = s0 + wave; s < s1; s += kAhead * W) {
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p) {
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        stage[wave][i][to] = in[p][i][0];
+        stage[wave][i][to + 64] = in[p][i][1];
       }
+      load(in[p], s + (p + kAhead) * W);
+      lds_order();
 #pragma unroll
-    for (int i = 0; i < SUB; ++i)
-      if (i < n_sub) {
-        vx[i][0] = load16(px[i] + c0);
-        vx[i][1] = load16(px[i] + c0 + 8);
-      }
+      for (int g = 0; g < 2; ++g) {
+        bf16x8 fa[RB];
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
+        for (int i = 0; i < RB; ++i) fa[i] = as_bf16x8(stage[wave][i][from[g]]);
 #pragma unroll
-      for (int j = 0; j < SUB; ++j)
-        if (i < n_rb && j < n_sub) {
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(va[i][0]), as_bf16x8(vx[j][0]), acc[i][j], 0, 0, 0);
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(va[i][1]), as_bf16x8(vx[j][1]), acc[i][j], 0, 0, 0);
+        for (int j = 0; j < SUB; ++j) {
+          const bf16x8 fx = as_bf16x8(stage[wave][RB + j][from[g]]);
+#pragma unroll
+          for (int i = 0; i < RB; ++i)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fx, acc[i][j], 0, 0, 0);
         }
-  }
-  // the four waves' sums: (0 + 2) + (1 + 3)
-  if (wave >= 2)
-#pragma unroll
-    for (int i = 0; i < RB; ++i)
-#pragma unroll
-      for (int j = 0; j < SUB; ++j) red[wave - 2][i * SUB + j][lane] = acc[i][j];
-  __syncthreads();
-  if (wave < 2)
-#pragma unroll
-    for (int i = 0; i < RB; ++i)
-#pragma unroll
-      for (int j = 0; j < SUB; ++j) acc[i][j] += red[wave][i * SUB + j][lane];
-  __syncthreads();
-  if (wave == 1)
-#pragma unroll
-    for (int i = 0; i < RB; ++i)
-#pragma unroll
-      for (int j = 0; j < SUB; ++j) red[0][i * SUB + j][lane] = acc[i][j];
-  __syncthreads();
-  if (wave != 0) return;
-  // lane (n, h): ranks 16 i + 4 h .. + 3 of row 16 j + n
-#pragma unroll
-  for (int i = 0; i < RB; ++i)
-#pragma unroll
-    for (int j = 0; j < SUB; ++j) {
-      const int rr = r0 + 16 * i + 4 * h, row = 16 * j + n;
-      if (rr < J.rank && row < tile.cnt)
-        *reinterpret_cast<f32x4*>(J.u + ((size_t)blockIdx.y * a.M + rows[row]) * J.rank + rr) =
-            acc[i][j] + red[0][i * SUB + j][lane];
+      }
+      lds_order();
     }
+  }
+  __syncthreads();   // every wave is done with its stage
+  // The waves' sums meet in LDS, 16 rows at a time, and are added in order.
+  // Lane (n, h) of a piece: ranks 4 h .. + 3 of row n.
+#pragma unroll
+  for (int j = 0; j < SUB; ++j) {
+    if (j >= n_sub) break;
+    if (j > 0) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RB; ++i) red[wave][i][lane] = acc[i][j];
+    __syncthreads();
+    if (tid < 64 * RB) {
+      f32x4 sum = red[0][wave][lane];
+#pragma unroll
+      for (int w = 1; w < W; ++w) sum += red[w][wave][lane];
+      const int rr = r0 + 16 * wave + 4 * h, row = 16 * j + n;
+      if (rr < J.rank && row < tile.cnt)
+        *reinterpret_cast<f32x4*>(J.u + ((size_t)blockIdx.y * a.M + rows[row]) * J.rank + rr) = sum;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -283,22 +347,26 @@ __device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
   p[2] = __float_as_uint(r1 - __uint_as_float(b1 & 0xFFFF0000u)) >> 16;
 }
 
-// Workgroup (t, g): tile t, outputs n0 .. n0 + n_range of one job.  First u of
-// the tile's rows goes to LDS in the order in which the matrix cores take it;
-// then each wave takes 16 outputs at a time: B's rows straight from memory
-// (16 bytes a lane, 8 ranks of one output), the base and y 16 bytes a lane.
-template <int SUB>
-__global__ __launch_bounds__(256) void k_lora_expand(LoraArgs a) {
-  extern __shared__ u32x4 lu[];   // [3 parts][ksteps][SUB][64 lanes]
+// Workgroup (t, g): tile t, outputs n0 .. n0 + n_range of one job.  u of the
+// tile's rows goes to LDS in the order in which the matrix cores take it; a
+// wave takes 32 outputs at a time, two tiles of 16: B's rows straight from
+// memory (16 bytes a lane: 8 ranks of one output), the base and y 32 bytes a
+// lane, 128 of a row.  For that, row i of tile q stands for output
+// 8 (i / 4) + 4 q + i % 4 of the 32.  B and the base of a wave's next outputs
+// are loaded before the present ones are computed, the first before u is
+// summed.  KS: 32-rank steps of the largest rank.
+template <int KS, int SUB>
+__global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 ? 3 : 2) void k_lora_expand(LoraArgs a) {
+  extern __shared__ u32x4 lu[];   // [3 parts][KS][SUB][64 lanes]
   __shared__ int32_t rows[16 * SUB], scratch[8];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6);
   const int n = lane & 15, h = lane >> 4;
   int ji = 0;
   for (int i = 1; i < a.n_jobs; ++i)
     if ((int)blockIdx.y >= a.job[i].wg_begin) ji = i;
   const LoraJob& J = a.job[ji];
   const int n0 = ((int)blockIdx.y - J.wg_begin) * a.n_range, n1 = min(J.rows, n0 + a.n_range);
-  const Tile tile = find_tile<16 * SUB>(a, blockIdx.x, rows, scratch);
+  const Tile tile = find_tile<SUB>(a, blockIdx.x, rows, scratch);
   if (tile.cnt == 0) return;
   const int rank = tile.e < 0 ? 0 : used_rank(J, tile.e);
   if (rank == 0) {   // no adapter: y is the base
@@ -310,15 +378,49 @@ __global__ __launch_bounds__(256) void k_lora_expand(LoraArgs a) {
     }
     return;
   }
-  const int ks = (rank + 31) / 32, n_sub = (tile.cnt + 15) / 16;
+  const int n_sub = (tile.cnt + 15) / 16;
+  // This lane's B row within 32 outputs (of tile 0; tile 1: 4 further) and its
+  // ranks 8 h .. of each step; ranks past the adapter's are not read.
+  const __amdgpu_buffer_rsrc_t rb = make_rsrc(J.b + (size_t)tile.e * J.b_stride, (uint32_t)J.rows * J.rank * 2);
+  const uint32_t row_bytes = J.rank * 2;
+  uint32_t pb[KS];
+#pragma unroll
+  for (int s = 0; s < KS; ++s)
+    pb[s] = 32 * s + 8 * h < rank ? (8 * (n >> 2) + (n & 3)) * row_bytes + 64 * s + 16 * h : kOutside;
+  // this lane's outputs: row 16 j + n, 8 h .. + 7
+  const uint32_t ny = (uint32_t)a.M * J.rows * 4;
+  const __amdgpu_buffer_rsrc_t rbase = make_rsrc(J.base, ny), ry = make_rsrc(J.y, ny);
+  uint32_t po[SUB];
+#pragma unroll
+  for (int j = 0; j < SUB; ++j)
+    po[j] = 16 * j + n < tile.cnt ? ((uint32_t)rows[16 * j + n] * J.rows + 8 * h) * 4 : kOutside;
+
+  u32x4 vb[2][KS];
+  f32x4 vy[SUB][2];
+  auto load = [&](int o0) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        vb[q][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rb, pb[s] + (o0 + 4 * q) * row_bytes, 0, 0));
+#pragma unroll
+    for (int j = 0; j < SUB; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        vy[j][q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rbase, po[j] + (o0 + 4 * q) * 4, 0, 0));
+  };
+  const int o_first = n0 + 32 * wave, o_last = n1 - 32;   // rows is a multiple of 32
+  load(min(o_first, o_last));
+
   const float scale = J.scale[tile.e];
   // item (row, 8-rank block): lane 16 * (block % 4) + row % 16 of k step block / 4
-  for (int it = tid; it < 16 * n_sub * 4 * ks; it += 256) {
-    const int row = it % (16 * n_sub), blk = it / (16 * n_sub), rr = 8 * blk;
+  for (int it = tid; it < 16 * n_sub * 4 * KS; it += 256) {
+    const int blk = it % (4 * KS), row = it / (4 * KS), rr = 8 * blk;
     u32x4 w[3] = {};
     if (row < tile.cnt && rr < rank) {
       f32x4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
       const float* p = J.u + (size_t)rows[row] * J.rank + rr;
+#pragma unroll 4
       for (int s = 0; s < a.split; ++s, p += (size_t)a.M * J.rank) {
         v0 += *reinterpret_cast<const f32x4*>(p);
         v1 += *reinterpret_cast<const f32x4*>(p + 4);
@@ -333,37 +435,46 @@ __global__ __launch_bounds__(256) void k_lora_expand(LoraArgs a) {
     }
 #pragma unroll
     for (int q = 0; q < 3; ++q)
-      lu[((q * ks + blk / 4) * SUB + row / 16) * 64 + 16 * (blk & 3) + (row & 15)] = w[q];
+      lu[((q * KS + blk / 4) * SUB + row / 16) * 64 + 16 * (blk & 3) + (row & 15)] = w[q];
   }
+  // what the adapter does not use of the 8 ranks in which it ends counts as 0
+  const int end_step = (rank - 1) / 32, left = rank - 32 * end_step - 8 * h;
+  u32x4 mask;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mask[i] = 2 * i + 1 < left ? ~0u : 2 * i < left ? 0xFFFFu : 0u;
   __syncthreads();
-  const uint16_t* pb = J.b + (size_t)tile.e * J.b_stride;
-  for (int o0 = n0 + 16 * wave; o0 < n1; o0 += 64) {   // rows is a multiple of 32: whole tiles of 16
-    f32x4 acc[SUB];
+  for (int o0 = o_first; o0 < n1; o0 += 128) {
+    f32x4 cy[SUB][2];
+    u32x4 cb[2][KS];
 #pragma unroll
-    for (int j = 0; j < SUB; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < ks; ++s) {
-      const int rr = 32 * s + 8 * h, left = rank - rr;   // ranks of this lane's 8 that the adapter uses
-      u32x4 vb = {0u, 0u, 0u, 0u};
-      if (left > 0) {
-        vb = load16(pb + (size_t)(o0 + n) * J.rank + rr);
+    for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vb[i] &= 2 * i + 1 < left ? ~0u : 2 * i < left ? 0xFFFFu : 0u;
-      }
-#pragma unroll
-      for (int j = 0; j < SUB; ++j)
-        if (j < n_sub)
-#pragma unroll
-          for (int q = 2; q >= 0; --q)
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(vb), as_bf16x8(lu[((q * ks + s) * SUB + j) * 64 + lane]),
-                                                             acc[j], 0, 0, 0);
-    }
-    // lane (n, h): outputs o0 + 4 h .. + 3 of row 16 j + n
+      for (int s = 0; s < KS; ++s) cb[q][s] = s == end_step ? vb[q][s] & mask : vb[q][s];
 #pragma unroll
     for (int j = 0; j < SUB; ++j)
-      if (16 * j + n < tile.cnt) {
-        const size_t o = (size_t)rows[16 * j + n] * J.rows + o0 + 4 * h;
-        *reinterpret_cast<f32x4u*>(J.y + o) = *reinterpret_cast<const f32x4u*>(J.base + o) + acc[j];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) cy[j][q] = vy[j][q];
+    load(min(o0 + 128, o_last));   // of the last outputs again, once, where there is no next
+#pragma unroll
+    for (int j = 0; j < SUB; ++j) {
+      f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      if (j < n_sub) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int p = 2; p >= 0; --p) {
+            const bf16x8 u = as_bf16x8(lu[((p * KS + s) * SUB + j) * 64 + lane]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(cb[q][s]), u, acc[q], 0, 0, 0);
+          }
       }
+      // rows past the last are outside the buffer: no branch around a store, or every load would be waited for
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, cy[j][q] + acc[q]), ry,
+                                               po[j] + (o0 + 4 * q) * 4, 0, 0);
+    }
   }
 }
 
@@ -377,23 +488,40 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
   const int g = last.wg_begin + (last.rows + a.n_range - 1) / a.n_range;
   if (a.M > kLoraScanRows) hipLaunchKernelGGL(k_lora_route, dim3(1), dim3(1024), 0, s, a);
   const dim3 gs(a.max_tiles, a.split, z), ge(a.max_tiles, g);
-  const size_t lds_row = (size_t)3 * ((max_rank + 31) / 32) * 64 * sizeof(u32x4);
+  constexpr size_t kLdsStep = 3 * 64 * sizeof(u32x4);   // u of 16 rows and 32 ranks
+  const int ks = (max_rank + 31) / 32;
+#define Q4NX_LORA_EXPAND(KS, SUB)                                                                   \
+  do {                                                                                              \
+    const size_t lds = KS * SUB * kLdsStep;                                                         \
+    if (lds > 65536)                                                                                \
+      (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_lora_expand<KS, SUB>),              \
+                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);              \
+    hipLaunchKernelGGL((k_lora_expand<KS, SUB>), ge, dim3(256), lds, s, a);                         \
+  } while (0)
+#define Q4NX_LORA_SHRINK(RB, SUB)                                                                   \
+  do {                                                                                              \
+    constexpr int W = lora_shrink_waves(SUB);                                                       \
+    const size_t lds = lora_shrink_lds(W, RB + SUB, SUB);                                           \
+    if (lds > 65536)                                                                                \
+      (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_lora_shrink<W, RB, SUB>),           \
+                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);              \
+    hipLaunchKernelGGL((k_lora_shrink<W, RB, SUB>), gs, dim3(64 * W), lds, s, a);                   \
+  } while (0)
 #define Q4NX_LORA(SUB)                                                                              \
   do {                                                                                              \
-    if (SUB * lds_row > 65536)                                                                      \
-      (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_lora_expand<SUB>),                  \
-                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)(SUB * lds_row));  \
-    if (max_rank <= 16)                                                                             \
-      hipLaunchKernelGGL((k_lora_shrink<1, SUB>), gs, dim3(256), 0, s, a);                          \
-    else if (max_rank <= 32)                                                                        \
-      hipLaunchKernelGGL((k_lora_shrink<2, SUB>), gs, dim3(256), 0, s, a);                          \
-    else                                                                                            \
-      hipLaunchKernelGGL((k_lora_shrink<4, SUB>), gs, dim3(256), 0, s, a);                          \
-    hipLaunchKernelGGL((k_lora_expand<SUB>), ge, dim3(256), (size_t)SUB * lds_row, s, a);           \
+    if (max_rank <= 16) Q4NX_LORA_SHRINK(1, SUB);                                                   \
+    else if (max_rank <= 32) Q4NX_LORA_SHRINK(2, SUB);                                              \
+    else Q4NX_LORA_SHRINK(4, SUB);                                                                  \
+    if (ks <= 1) Q4NX_LORA_EXPAND(1, SUB);                                                          \
+    else if (ks <= 2) Q4NX_LORA_EXPAND(2, SUB);                                                     \
+    else if (ks <= 4) Q4NX_LORA_EXPAND(4, SUB);                                                     \
+    else Q4NX_LORA_EXPAND(8, SUB);                                                                  \
   } while (0)
-  if (a.M <= 64) Q4NX_LORA(1);
+  if (a.M <= kLoraWaveRows) Q4NX_LORA(1);
   else Q4NX_LORA(4);
 #undef Q4NX_LORA
+#undef Q4NX_LORA_SHRINK
+#undef Q4NX_LORA_EXPAND
   return hipGetLastError();
 }
 

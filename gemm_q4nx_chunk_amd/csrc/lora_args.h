@@ -10,7 +10,12 @@ constexpr int kLoraMaxJobs = 8;
 constexpr int kLoraMaxRank = 256;
 constexpr int kLoraMaxAdapters = 4096;   // the route kernel counts rows per adapter in LDS
 constexpr int kLoraMaxRows = 4096;       // activation rows of one call
+constexpr int kLoraWaveRows = 64;        // up to here each wave finds its tile's rows itself, 16 at most
 constexpr int kLoraScanRows = 256;       // up to here each workgroup finds its tile's rows itself
+#ifndef Q4NX_LORA_W4
+#define Q4NX_LORA_W4 8
+#endif
+constexpr int lora_shrink_waves(int sub) { return sub == 1 ? 8 : Q4NX_LORA_W4; }
 constexpr int kLoraStepCols = 64;        // columns of x that a wave multiplies per step
 constexpr int kLoraRankGroup = 64;       // ranks of one shrink workgroup
 constexpr int kLoraMaxSplit = 64;
@@ -29,17 +34,24 @@ struct LoraJob {
   int32_t rg_begin;        // shrink: first rank group (along grid z) of this job
 };
 
+// A tile of rows of one adapter.
+struct LoraTile {
+  int32_t e;     // adapter, -1: rows without one
+  int32_t cnt;   // rows; 0: no tile
+};
+
 struct LoraArgs {
   LoraJob job[kLoraMaxJobs];
   int32_t n_jobs, n_adapters;
   int32_t M, cols;
+  int32_t more;            // not the call's first rows: the error bit stays set
   int32_t split;           // parts of the columns in the shrink
   int32_t n_range;         // outputs of one expand workgroup
   const uint16_t* x;       // [M][cols]
   const int32_t* ids;      // [M]
-  uint32_t* hdr;           // [0]: bit 0 = an id outside [-1, n_adapters); [1]: tiles
-  int32_t* sorted;         // [M] rows by adapter (M > kLoraScanRows)
-  int32_t* tiles;          // [tiles][3]: adapter (-1: none), first place in sorted, rows
+  uint32_t* hdr;           // [0]: bit 0 = an id outside [-1, n_adapters)
+  int32_t* sorted;         // [max_tiles][64] each tile's rows (M > kLoraScanRows)
+  LoraTile* tiles;         // [max_tiles]
   int32_t max_tiles;       // grid x
 };
 

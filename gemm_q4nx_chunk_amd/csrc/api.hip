@@ -1376,19 +1376,6 @@ int check_lora(const q4nx_lora* L, const char* name) {
   return Q4NX_OK;
 }
 
-#ifndef Q4NX_LORA_STEPS
-#define Q4NX_LORA_STEPS 2
-#endif
-#ifndef Q4NX_LORA_FILL
-#define Q4NX_LORA_FILL 256
-#endif
-#ifndef Q4NX_LORA_RANGE
-#define Q4NX_LORA_RANGE 256
-#endif
-#ifndef Q4NX_LORA_RWG
-#define Q4NX_LORA_RWG 512
-#endif
-
 // Launch shape and workspace layout of a call over checked tables.
 struct LoraShape {
   q4nx::LoraArgs a;
@@ -1410,7 +1397,7 @@ void lora_shape(const q4nx_lora* const* L, int n, int M, LoraShape& sh) {
   a.n_adapters = L[0]->n_adapters;
   a.M = M;
   a.cols = L[0]->cols;
-  a.max_tiles = M <= q4nx::kLoraScanRows ? M : q4nx::lora_max_tiles(M, a.n_adapters);
+  a.max_tiles = q4nx::lora_max_tiles(M, a.n_adapters);
   const int tiles = (M + 63) / 64;   // at least
   int groups = 0;
   int64_t rows = 0;
@@ -1419,16 +1406,20 @@ void lora_shape(const q4nx_lora* const* L, int n, int M, LoraShape& sh) {
     groups += (L[i]->rank + q4nx::kLoraRankGroup - 1) / q4nx::kLoraRankGroup;
     rows += L[i]->rows;
   }
-  // Parts of the columns: a wave takes about Q4NX_LORA_STEPS steps.  For many
-  // rows, only as many parts as fill the GPU: every part is a row of u that
-  // the expand reads again for each of its ranges.
+  // Parts of the columns.  Each part is a row of u that the expand reads again
+  // for each of its ranges, so no more than give a wave two steps, than fill
+  // the GPU, or than the expand loads at once.  Up to 64 rows, with an adapter
+  // each: 64 rows of 9728 columns, rank 64, 17.6 us with 4 parts, 19.6 with 8,
+  // 22.9 with 10; 32 rows of 14336 columns 19.7, 18.9, 22.1.  More rows: 4096 of
+  // 14336 columns, rank 64, 91 us with 3 parts, 104 with 7.
   const int steps = a.cols / q4nx::kLoraStepCols;
-  const int per = q4nx::lora_shrink_waves(M <= q4nx::kLoraWaveRows ? 1 : 4) * Q4NX_LORA_STEPS;
+  const int per = q4nx::kLoraShrinkWaves * 2;
   a.split = std::max(1, std::min((steps + per - 1) / per, q4nx::kLoraMaxSplit));
-  if (M > q4nx::kLoraWaveRows)
-    a.split = std::max(1, std::min(a.split, Q4NX_LORA_FILL / (std::min(a.max_tiles, 2 * tiles) * groups)));
-  a.n_range = 128;
-  while (a.n_range < Q4NX_LORA_RANGE && tiles * (rows / (2 * a.n_range)) >= Q4NX_LORA_RWG) a.n_range *= 2;
+  if (M <= q4nx::kLoraWaveRows) a.split = std::min(a.split, std::max(4, 256 / (M * groups)));
+  else a.split = std::max(1, std::min(a.split, 256 / (std::min(a.max_tiles, 2 * tiles) * groups)));
+  // Outputs of a workgroup: 128, or 256 where that still makes 512 workgroups
+  // (4096 x 4096, rank 64: 83 us, 89 with 128; 1000 x 4096: 20.7 with 128, 21.7 with 512).
+  a.n_range = tiles * (rows / 256) >= 512 ? 256 : 128;
   while (rows / a.n_range > 32768) a.n_range *= 2;   // grid limit
   int wg = 0;
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };

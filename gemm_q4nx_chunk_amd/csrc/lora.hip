@@ -8,10 +8,9 @@
 // MoE prompts together", make for experts).
 //
 // Launches, on one stream:
-//   route   (more than 256 rows) one workgroup counts the rows of each adapter
-//           and cuts them into tiles of up to 64.  Up to 256 rows every
-//           workgroup of the other two finds its tile itself: workgroup t is
-//           row t's, and works if row t is the first of a tile of its adapter.
+//   route   (more than 64 rows) one workgroup counts the rows of each adapter
+//           and cuts them into tiles of up to 64.  Up to 64 rows every wave of
+//           the other two finds its tile, of up to 16 rows, itself.
 //   shrink  u = A_e x for a tile, columns split over workgroups and waves,
 //           bf16 matrix cores, fp32 sums: the parts go to the workspace.
 //   expand  sums the parts of u in order, times scale_e, and adds B_e u to the
@@ -51,51 +50,57 @@ __device__ __forceinline__ int valid_id(const LoraArgs& a, int id) {
 __device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // Fills rows[0..cnt) with the tile of workgroup t.  Call with all threads of
-// the workgroup (at least 256).  SUB: 16-row pieces of a tile.
-//   M <= 64 (SUB == 1): every wave finds it by itself, and all write the same
-//     rows: a wave reads what it wrote, no barrier.
-//   M <= 256: a row a thread, the waves' counts meet in LDS.
-//   above: from the route's tables.
+// the workgroup.  SUB: 16-row pieces of a tile.
+//   SUB == 1 (at most 64 rows): every wave finds it by itself, and all write the
+//     same rows: a wave reads what it wrote, no barrier.  With few adapters, so
+//     that few tiles are possible, by walking the adapters in order of their
+//     first rows; else workgroup t is row t's, and has a tile if row t opens one.
+//   above: from the route's tables; ends with a barrier.
 template <int SUB>
-__device__ __forceinline__ Tile find_tile(const LoraArgs& a, int t, int32_t* rows, int32_t* scratch) {
+__device__ __forceinline__ Tile find_tile(const LoraArgs& a, int t, int32_t* rows) {
   constexpr int kTile = 16 * SUB;
-  const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63;
   Tile tile;
-  if constexpr (SUB == 1) {
-    const int id = lane < a.M ? a.ids[lane] : 0;
-    tile.e = scalar(valid_id(a, a.ids[t]));
-    const bool same = lane < a.M && valid_id(a, id) == tile.e;
-    const uint64_t b = __ballot(same);
-    const int before = __popcll(b & ((1ull << t) - 1ull)), at = __popcll(b & ((1ull << lane) - 1ull));
-    tile.cnt = before % kTile ? 0 : min(kTile, __popcll(b) - before);   // row t opens a tile, or lies in one
-    if (same && at >= before && at < before + tile.cnt) rows[at - before] = lane;
-    lds_order();
-    return tile;
-  }
-  if (a.M > kLoraScanRows) {
+  if constexpr (SUB > 1) {
     // everything at once: places past the tile's rows hold no row and are not used
-    if (tid < 64) rows[tid] = a.sorted[64 * t + tid];
+    if (tid < kTile) rows[tid] = a.sorted[kTile * t + tid];
     tile.e = scalar(a.tiles[t].e);
     tile.cnt = scalar(a.tiles[t].cnt);
     __syncthreads();
     return tile;
   }
-  // rows with row t's id: how many come before t, and which come from t on
-  tile.e = scalar(valid_id(a, a.ids[t]));
-  const bool same = tid < a.M && valid_id(a, a.ids[tid < a.M ? tid : 0]) == tile.e;
-  const uint64_t b = __ballot(same);
-  if (wave < 4 && lane == 0) {
-    scratch[wave] = __popcll(b);
-    scratch[4 + wave] = t >= 64 * wave + 64 ? __popcll(b) : t <= 64 * wave ? 0 : __popcll(b & ((1ull << (t - 64 * wave)) - 1ull));
+  const int id = lane < a.M ? valid_id(a, a.ids[lane]) : 0;
+  const uint64_t all = __ballot(lane < a.M);
+  uint64_t b;
+  int before;   // rows of this adapter in tiles before this one
+  if (a.max_tiles == a.M) {
+    tile.e = __builtin_amdgcn_readlane(id, t);
+    b = __ballot(id == tile.e) & all;
+    before = __popcll(b & ((1ull << t) - 1ull));
+    tile.cnt = before % kTile ? 0 : min(kTile, __popcll(b) - before);
+  } else {
+    tile.e = -1;
+    tile.cnt = 0;
+    before = 0;
+    b = 0;
+    int first = 0;   // tiles of the adapters passed
+    for (uint64_t todo = all; todo;) {
+      const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+      b = __ballot(id == e) & all;
+      const int n = __popcll(b), tiles = (n + kTile - 1) / kTile;
+      if (t < first + tiles) {
+        before = kTile * (t - first);
+        tile.e = e;
+        tile.cnt = min(kTile, n - before);
+        break;
+      }
+      first += tiles;
+      todo &= ~b;
+    }
   }
-  __syncthreads();
-  const int before = scalar(scratch[4] + scratch[5] + scratch[6] + scratch[7]);
-  const int total = scalar(scratch[0] + scratch[1] + scratch[2] + scratch[3]);
-  int at = __popcll(b & ((1ull << lane) - 1ull));
-  for (int w = 0; w < min(wave, 4); ++w) at += scratch[w];
-  tile.cnt = before % kTile ? 0 : min(kTile, total - before);
-  if (same && at >= before && at < before + tile.cnt) rows[at - before] = tid;
-  __syncthreads();
+  const int at = __popcll(b & ((1ull << lane) - 1ull));
+  if ((b >> lane & 1) && at >= before && at < before + tile.cnt) rows[at - before] = lane;
+  lds_order();
   return tile;
 }
 
@@ -120,38 +125,50 @@ __global__ __launch_bounds__(1024) void k_lora_route(LoraArgs a) {
   __shared__ int32_t cnt[kPer * 1024], start[kPer * 1024];
   __shared__ int32_t wsum[16];
   __shared__ uint32_t bad;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6);
+  constexpr int kRowsPer = kLoraMaxRows / 1024;
+  int id[kRowsPer];
+#pragma unroll
+  for (int i = 0; i < kRowsPer; ++i) id[i] = i * 1024 + tid < a.M ? a.ids[i * 1024 + tid] : -1;
   if (tid == 0) bad = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) cnt[i * 1024 + tid] = 0;
   __syncthreads();
-  constexpr int kRowsPer = kLoraMaxRows / 1024;
+  uint32_t wrong = 0;
   int bin[kRowsPer], slot[kRowsPer];
 #pragma unroll
   for (int i = 0; i < kRowsPer; ++i) {
-    const int m = i * 1024 + tid;
-    bin[i] = -1;
-    if (m < a.M) {
-      const int id = a.ids[m];
-      bin[i] = valid_id(a, id) < 0 ? a.n_adapters : id;
-      if (id < -1 || id >= a.n_adapters) atomicOr(&bad, 1u);
-    }
-    // A prompt's rows come in runs: the first lanes' bins are counted for all
-    // their lanes at once, what is left lane by lane.
+    const bool row = i * 1024 + tid < a.M;
+    bin[i] = !row ? -1 : valid_id(a, id[i]) < 0 ? a.n_adapters : id[i];
     slot[i] = -1;
+    wrong |= row && (id[i] < -1 || id[i] >= a.n_adapters) ? 1u : 0u;
+  }
+  if (wrong) atomicOr(&bad, 1u);
+  // A prompt's rows come in runs: the first lanes' bins are counted for all
+  // their lanes at once, what is left lane by lane.
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+  for (int r = 0; r < 2; ++r) {
+    uint64_t mine[kRowsPer];
+    int first[kRowsPer];
+#pragma unroll
+    for (int i = 0; i < kRowsPer; ++i) {
       const uint64_t todo = __ballot(bin[i] >= 0 && slot[i] < 0);
+      mine[i] = 0;
+      first[i] = 0;
       if (todo == 0) continue;
       const int b = __builtin_amdgcn_readlane(bin[i], __builtin_ctzll(todo));
-      const uint64_t mine = __ballot(bin[i] == b && slot[i] < 0);
-      int first = 0;
-      if (lane == 0) first = atomicAdd(&cnt[b], __popcll(mine));
-      first = __builtin_amdgcn_readfirstlane(first);
-      if (bin[i] == b && slot[i] < 0) slot[i] = first + __popcll(mine & ((1ull << lane) - 1ull));
+      mine[i] = __ballot(bin[i] == b && slot[i] < 0);
+      if (lane == 0) first[i] = atomicAdd(&cnt[b], __popcll(mine[i]));
     }
-    if (bin[i] >= 0 && slot[i] < 0) slot[i] = atomicAdd(&cnt[bin[i]], 1);
+#pragma unroll
+    for (int i = 0; i < kRowsPer; ++i) {
+      const int f = __builtin_amdgcn_readfirstlane(first[i]);
+      if (mine[i] >> lane & 1) slot[i] = f + __popcll(mine[i] & ((1ull << lane) - 1ull));
+    }
   }
+#pragma unroll
+  for (int i = 0; i < kRowsPer; ++i)
+    if (bin[i] >= 0 && slot[i] < 0) slot[i] = atomicAdd(&cnt[bin[i]], 1);
   __syncthreads();
   // prefix sum of the tiles over the bins, kPer neighbouring bins a thread
   int c[kPer], tiles = 0;
@@ -169,7 +186,8 @@ __global__ __launch_bounds__(1024) void k_lora_route(LoraArgs a) {
   if (lane == 63) wsum[wave] = it;
   __syncthreads();
   int t0 = it - tiles;
-  for (int w = 0; w < wave; ++w) t0 += wsum[w];
+#pragma unroll
+  for (int w = 0; w < 16; ++w) t0 += w < wave ? wsum[w] : 0;
   if (tid == 0) a.hdr[0] = (a.more ? a.hdr[0] : 0u) | bad;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -194,7 +212,7 @@ __global__ __launch_bounds__(1024) void k_lora_route(LoraArgs a) {
 // shrink
 // ---------------------------------------------------------------------------
 // Workgroup (t, s, z): tile t, part s of the columns, rank group z of up to 16
-// RB ranks.  Its W waves take every W-th step of 64 columns each, for all ranks
+// RB ranks.  Its eight waves take every eighth step of 64 columns each, for all ranks
 // and rows of the tile: matrix-core tiles of 16 ranks x 16 rows x 32 columns.
 // The matrix cores want lane l to hold row l % 16, but 16 neighbouring lanes
 // that read 16 rows touch 16 cache lines for 256 bytes, so a wave loads a step
@@ -206,32 +224,32 @@ __global__ __launch_bounds__(1024) void k_lora_route(LoraArgs a) {
 // Measured (4096 rows, 14336 columns, rank 64; 64 rows of 40 adapters, 9728
 // columns): operands straight from memory 75 and 14 us; 64 bytes of a row at a
 // time through LDS 51 and 12.
-inline size_t lora_shrink_lds(int waves, int blocks, int sub) {
-  return (size_t)waves * blocks * 2048 + (16 * sub + 8) * sizeof(int32_t);
+inline size_t lora_shrink_lds(int blocks, int sub) {
+  return (size_t)kLoraShrinkWaves * blocks * 2048 + 16 * sub * sizeof(int32_t);
 }
 
-template <int W, int RB, int SUB>
-__global__ __launch_bounds__(64 * W, SUB == 1 ? 4 : 2) void k_lora_shrink(LoraArgs a) {
+template <int RB, int SUB>
+__global__ __launch_bounds__(64 * kLoraShrinkWaves, SUB == 1 ? 4 : 2) void k_lora_shrink(LoraArgs a) {
+  constexpr int W = kLoraShrinkWaves;
   constexpr int kAhead = SUB == 1 && RB <= 2 ? 2 : 1;   // 128 registers a wave, 256 for SUB == 4
   constexpr int B = RB + SUB;   // 16-row blocks of a step: A's, then x's
-  extern __shared__ u32x4 lds[];   // lora_shrink_lds(W, B, SUB) bytes
+  extern __shared__ u32x4 lds[];   // lora_shrink_lds(B, SUB) bytes
   u32x4(*stage)[B][128] = reinterpret_cast<u32x4(*)[B][128]>(lds);
   int32_t* rows = reinterpret_cast<int32_t*>(lds + W * B * 128);
-  int32_t* scratch = rows + 16 * SUB;
   f32x4(*red)[RB][64] = reinterpret_cast<f32x4(*)[RB][64]>(stage);   // after the loop: B > RB, so it fits
   const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6);
   const int n = lane & 15, h = lane >> 4;
-  if (a.M <= kLoraScanRows && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
-    const int id = tid < a.M ? a.ids[tid] : -1;
-    const int bad = __syncthreads_or(id < -1 || id >= a.n_adapters);
-    if (tid == 0) a.hdr[0] = (a.more ? a.hdr[0] : 0u) | (bad ? 1u : 0u);
+  if (SUB == 1 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && wave == 0) {
+    const int id = lane < a.M ? a.ids[lane] : -1;
+    const uint64_t bad = __ballot(id < -1 || id >= a.n_adapters);
+    if (lane == 0) a.hdr[0] = (a.more ? a.hdr[0] : 0u) | (bad ? 1u : 0u);
   }
   int ji = 0;
   for (int i = 1; i < a.n_jobs; ++i)
     if ((int)blockIdx.z >= a.job[i].rg_begin) ji = i;
   const LoraJob& J = a.job[ji];
   const int r0 = ((int)blockIdx.z - J.rg_begin) * kLoraRankGroup;
-  const Tile tile = find_tile<SUB>(a, blockIdx.x, rows, scratch);
+  const Tile tile = find_tile<SUB>(a, blockIdx.x, rows);
   if (tile.cnt == 0 || tile.e < 0) return;
   const int rank = used_rank(J, tile.e);
   if (r0 >= rank) return;
@@ -349,16 +367,18 @@ __device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
 
 // Workgroup (t, g): tile t, outputs n0 .. n0 + n_range of one job.  u of the
 // tile's rows goes to LDS in the order in which the matrix cores take it; a
-// wave takes 32 outputs at a time, two tiles of 16: B's rows straight from
-// memory (16 bytes a lane: 8 ranks of one output), the base and y 32 bytes a
-// lane, 128 of a row.  For that, row i of tile q stands for output
-// 8 (i / 4) + 4 q + i % 4 of the 32.  B and the base of a wave's next outputs
-// are loaded before the present ones are computed, the first before u is
-// summed.  KS: 32-rank steps of the largest rank.
+// wave takes 32 outputs at a time, two tiles of 16, B's rows straight from
+// memory (16 bytes a lane: 8 ranks of one output).  The result of 16 rows goes
+// through LDS of the wave's own, so that the base and y move eight lanes to a
+// row, a whole 128-byte line (group c of 4 outputs of row r at slot c ^ (r % 8);
+// 16 rows to 16 lanes instead, as the matrix cores leave them, 47 and 15 us at
+// 4096 x 4096 rank 64 and 1000 x 4096 rank 16).  B and the base of a wave's next
+// outputs are loaded before the present ones are computed, the first before u
+// is summed.  KS: 32-rank steps of the largest rank.
 template <int KS, int SUB>
 __global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 ? 3 : 2) void k_lora_expand(LoraArgs a) {
-  extern __shared__ u32x4 lu[];   // [3 parts][KS][SUB][64 lanes]
-  __shared__ int32_t rows[16 * SUB], scratch[8];
+  extern __shared__ u32x4 lu[];   // [3 parts][KS][SUB][64 lanes], then [4 waves][16 rows][8 groups]
+  __shared__ int32_t rows[16 * SUB];
   const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6);
   const int n = lane & 15, h = lane >> 4;
   int ji = 0;
@@ -366,7 +386,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 ? 3 : 2) void k_lora_exp
     if ((int)blockIdx.y >= a.job[i].wg_begin) ji = i;
   const LoraJob& J = a.job[ji];
   const int n0 = ((int)blockIdx.y - J.wg_begin) * a.n_range, n1 = min(J.rows, n0 + a.n_range);
-  const Tile tile = find_tile<SUB>(a, blockIdx.x, rows, scratch);
+  const Tile tile = find_tile<SUB>(a, blockIdx.x, rows);
   if (tile.cnt == 0) return;
   const int rank = tile.e < 0 ? 0 : used_rank(J, tile.e);
   if (rank == 0) {   // no adapter: y is the base
@@ -379,59 +399,78 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 ? 3 : 2) void k_lora_exp
     return;
   }
   const int n_sub = (tile.cnt + 15) / 16;
-  // This lane's B row within 32 outputs (of tile 0; tile 1: 4 further) and its
+  // This lane's B row within 32 outputs (of tile 0; tile 1: 16 further) and its
   // ranks 8 h .. of each step; ranks past the adapter's are not read.
   const __amdgpu_buffer_rsrc_t rb = make_rsrc(J.b + (size_t)tile.e * J.b_stride, (uint32_t)J.rows * J.rank * 2);
   const uint32_t row_bytes = J.rank * 2;
   uint32_t pb[KS];
 #pragma unroll
-  for (int s = 0; s < KS; ++s)
-    pb[s] = 32 * s + 8 * h < rank ? (8 * (n >> 2) + (n & 3)) * row_bytes + 64 * s + 16 * h : kOutside;
-  // this lane's outputs: row 16 j + n, 8 h .. + 7
+  for (int s = 0; s < KS; ++s) pb[s] = 32 * s + 8 * h < rank ? n * row_bytes + 64 * s + 16 * h : kOutside;
+  // this lane's part of the base and y: row 16 j + 8 p + lane / 8, outputs 4 (lane % 8) .. + 3 of the 32
   const uint32_t ny = (uint32_t)a.M * J.rows * 4;
   const __amdgpu_buffer_rsrc_t rbase = make_rsrc(J.base, ny), ry = make_rsrc(J.y, ny);
-  uint32_t po[SUB];
+  const int lr = lane >> 3, lc = lane & 7;
+  uint32_t po[SUB][2];
 #pragma unroll
   for (int j = 0; j < SUB; ++j)
-    po[j] = 16 * j + n < tile.cnt ? ((uint32_t)rows[16 * j + n] * J.rows + 8 * h) * 4 : kOutside;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int r = 16 * j + 8 * p + lr;
+      po[j][p] = r < tile.cnt ? ((uint32_t)rows[r] * J.rows + 4 * lc) * 4 : kOutside;
+    }
 
+  constexpr bool kAheadB = KS * SUB < 32;   // else B's registers are needed twice over, which there are not
   u32x4 vb[2][KS];
   f32x4 vy[SUB][2];
-  auto load = [&](int o0) {
+  auto load_b = [&](int o0) {
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        vb[q][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rb, pb[s] + (o0 + 4 * q) * row_bytes, 0, 0));
+        vb[q][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rb, pb[s] + (o0 + 16 * q) * row_bytes, 0, 0));
+  };
+  auto load = [&](int o0) {
+    if constexpr (kAheadB) load_b(o0);
 #pragma unroll
     for (int j = 0; j < SUB; ++j)
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        vy[j][q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rbase, po[j] + (o0 + 4 * q) * 4, 0, 0));
+      for (int p = 0; p < 2; ++p)
+        vy[j][p] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rbase, po[j][p] + o0 * 4, 0, 0));
   };
   const int o_first = n0 + 32 * wave, o_last = n1 - 32;   // rows is a multiple of 32
   load(min(o_first, o_last));
 
   const float scale = J.scale[tile.e];
-  // item (row, 8-rank block): lane 16 * (block % 4) + row % 16 of k step block / 4
+  // Item (row, 8-rank block) goes to lane 16 * (block % 4) + row % 16 of k step
+  // block / 4.  The parts of u are loaded four at a time; past the last they
+  // are outside the buffer and add 0.
+  const uint32_t part_bytes = (uint32_t)a.M * J.rank * 4;
+  const __amdgpu_buffer_rsrc_t ru = make_rsrc(J.u, part_bytes * a.split);
   for (int it = tid; it < 16 * n_sub * 4 * KS; it += 256) {
     const int blk = it % (4 * KS), row = it / (4 * KS), rr = 8 * blk;
+    uint32_t at = row < tile.cnt && rr < rank ? ((uint32_t)rows[row] * J.rank + rr) * 4 : kOutside;
+    f32x4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
+    for (int s0 = 0; s0 < a.split; s0 += 4) {
+      f32x4 p0[4], p1[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        p0[s] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ru, at + s * part_bytes, 0, 0));
+        p1[s] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ru, at + s * part_bytes + 16, 0, 0));
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        v0 += p0[s];
+        v1 += p1[s];
+      }
+      at += 4 * part_bytes;
+    }
     u32x4 w[3] = {};
-    if (row < tile.cnt && rr < rank) {
-      f32x4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
-      const float* p = J.u + (size_t)rows[row] * J.rank + rr;
-#pragma unroll 4
-      for (int s = 0; s < a.split; ++s, p += (size_t)a.M * J.rank) {
-        v0 += *reinterpret_cast<const f32x4*>(p);
-        v1 += *reinterpret_cast<const f32x4*>(p + 4);
-      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t part[3];
-        split3(rr + i < rank ? (i < 4 ? v0[i & 3] : v1[i & 3]) * scale : 0.f, part);
+    for (int i = 0; i < 8; ++i) {
+      uint32_t part[3];
+      split3(rr + i < rank ? (i < 4 ? v0[i & 3] : v1[i & 3]) * scale : 0.f, part);
 #pragma unroll
-        for (int q = 0; q < 3; ++q) w[q][i >> 1] |= part[q] << (16 * (i & 1));
-      }
+      for (int q = 0; q < 3; ++q) w[q][i >> 1] |= part[q] << (16 * (i & 1));
     }
 #pragma unroll
     for (int q = 0; q < 3; ++q)
@@ -442,10 +481,12 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 ? 3 : 2) void k_lora_exp
   u32x4 mask;
 #pragma unroll
   for (int i = 0; i < 4; ++i) mask[i] = 2 * i + 1 < left ? ~0u : 2 * i < left ? 0xFFFFu : 0u;
+  f32x4* turn = reinterpret_cast<f32x4*>(lu + 3 * KS * SUB * 64) + wave * 128;
   __syncthreads();
   for (int o0 = o_first; o0 < n1; o0 += 128) {
     f32x4 cy[SUB][2];
     u32x4 cb[2][KS];
+    if constexpr (!kAheadB) load_b(o0);
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -453,7 +494,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 ? 3 : 2) void k_lora_exp
 #pragma unroll
     for (int j = 0; j < SUB; ++j)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) cy[j][q] = vy[j][q];
+      for (int p = 0; p < 2; ++p) cy[j][p] = vy[j][p];
     load(min(o0 + 128, o_last));   // of the last outputs again, once, where there is no next
 #pragma unroll
     for (int j = 0; j < SUB; ++j) {
@@ -469,11 +510,16 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : KS == 2 ? 3 : 2) void k_lora_exp
               acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(cb[q][s]), u, acc[q], 0, 0, 0);
           }
       }
+      // lane (n, h) has outputs 16 q + 4 h .. + 3 of row n
+      turn[8 * n + (h ^ (n & 7))] = acc[0];
+      turn[8 * n + ((4 + h) ^ (n & 7))] = acc[1];
+      lds_order();
       // rows past the last are outside the buffer: no branch around a store, or every load would be waited for
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, cy[j][q] + acc[q]), ry,
-                                               po[j] + (o0 + 4 * q) * 4, 0, 0);
+      for (int p = 0; p < 2; ++p)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, cy[j][p] + turn[64 * p + 8 * lr + (lc ^ lr)]),
+                                               ry, po[j][p] + o0 * 4, 0, 0);
+      lds_order();
     }
   }
 }
@@ -486,13 +532,13 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
   }
   const LoraJob& last = a.job[a.n_jobs - 1];
   const int g = last.wg_begin + (last.rows + a.n_range - 1) / a.n_range;
-  if (a.M > kLoraScanRows) hipLaunchKernelGGL(k_lora_route, dim3(1), dim3(1024), 0, s, a);
+  if (a.M > kLoraWaveRows) hipLaunchKernelGGL(k_lora_route, dim3(1), dim3(1024), 0, s, a);
   const dim3 gs(a.max_tiles, a.split, z), ge(a.max_tiles, g);
   constexpr size_t kLdsStep = 3 * 64 * sizeof(u32x4);   // u of 16 rows and 32 ranks
   const int ks = (max_rank + 31) / 32;
 #define Q4NX_LORA_EXPAND(KS, SUB)                                                                   \
   do {                                                                                              \
-    const size_t lds = KS * SUB * kLdsStep;                                                         \
+    const size_t lds = KS * SUB * kLdsStep + 4 * 128 * sizeof(f32x4);                               \
     if (lds > 65536)                                                                                \
       (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_lora_expand<KS, SUB>),              \
                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);              \
@@ -500,12 +546,11 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
   } while (0)
 #define Q4NX_LORA_SHRINK(RB, SUB)                                                                   \
   do {                                                                                              \
-    constexpr int W = lora_shrink_waves(SUB);                                                       \
-    const size_t lds = lora_shrink_lds(W, RB + SUB, SUB);                                           \
+    const size_t lds = lora_shrink_lds(RB + SUB, SUB);                                              \
     if (lds > 65536)                                                                                \
-      (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_lora_shrink<W, RB, SUB>),           \
+      (void)hipFuncSetAttribute(reinterpret_cast<const void*>(k_lora_shrink<RB, SUB>),              \
                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);              \
-    hipLaunchKernelGGL((k_lora_shrink<W, RB, SUB>), gs, dim3(64 * W), lds, s, a);                   \
+    hipLaunchKernelGGL((k_lora_shrink<RB, SUB>), gs, dim3(64 * kLoraShrinkWaves), lds, s, a);       \
   } while (0)
 #define Q4NX_LORA(SUB)                                                                              \
   do {                                                                                              \

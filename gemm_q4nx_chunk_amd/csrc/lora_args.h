@@ -11,14 +11,10 @@ constexpr int kLoraMaxRank = 256;
 constexpr int kLoraMaxAdapters = 4096;   // the route kernel counts rows per adapter in LDS
 constexpr int kLoraMaxRows = 4096;       // activation rows of one call
 constexpr int kLoraWaveRows = 64;        // up to here each wave finds its tile's rows itself, 16 at most
-constexpr int kLoraScanRows = 256;       // up to here each workgroup finds its tile's rows itself
-#ifndef Q4NX_LORA_W4
-#define Q4NX_LORA_W4 8
-#endif
-constexpr int lora_shrink_waves(int sub) { return sub == 1 ? 8 : Q4NX_LORA_W4; }
+constexpr int kLoraShrinkWaves = 8;
 constexpr int kLoraStepCols = 64;        // columns of x that a wave multiplies per step
 constexpr int kLoraRankGroup = 64;       // ranks of one shrink workgroup
-constexpr int kLoraMaxSplit = 64;
+constexpr int kLoraMaxSplit = 8;         // parts of u that the expand adds, four loads at a time
 
 struct LoraJob {
   const uint16_t* a;       // adapter e's A [rank][cols] at a + e * a_stride (elements)
@@ -50,15 +46,17 @@ struct LoraArgs {
   const uint16_t* x;       // [M][cols]
   const int32_t* ids;      // [M]
   uint32_t* hdr;           // [0]: bit 0 = an id outside [-1, n_adapters)
-  int32_t* sorted;         // [max_tiles][64] each tile's rows (M > kLoraScanRows)
+  int32_t* sorted;         // [max_tiles][64] each tile's rows (M > kLoraWaveRows)
   LoraTile* tiles;         // [max_tiles]
   int32_t max_tiles;       // grid x
 };
 
-// Tiles of at most 64 rows of one adapter (or of none): whole ones, and at most
-// one short one per adapter.
+// Tiles of rows of one adapter (or of none): whole ones, and at most one short
+// one per adapter.  Up to kLoraWaveRows rows, a workgroup per row instead unless
+// that is twice as many.
 inline int lora_max_tiles(int M, int n_adapters) {
   const int groups = M < n_adapters + 1 ? M : n_adapters + 1;
+  if (M <= kLoraWaveRows) return 2 * (M / 16 + groups) <= M ? M / 16 + groups : M;
   return M / 64 + groups;
 }
 

@@ -1417,9 +1417,18 @@ void lora_shape(const q4nx_lora* const* L, int n, int M, LoraShape& sh) {
   a.split = std::max(1, std::min((steps + per - 1) / per, q4nx::kLoraMaxSplit));
   if (M <= q4nx::kLoraWaveRows) a.split = std::min(a.split, std::max(4, 256 / (M * groups)));
   else a.split = std::max(1, std::min(a.split, 256 / (std::min(a.max_tiles, 2 * tiles) * groups)));
-  // Outputs of a workgroup: 128, or 256 where that still makes 512 workgroups
-  // (4096 x 4096, rank 64: 83 us, 89 with 128; 1000 x 4096: 20.7 with 128, 21.7 with 512).
-  a.n_range = tiles * (rows / 256) >= 512 ? 256 : 128;
+  int max_rank = 0;
+  int64_t blocks = 0;   // of 128 outputs
+  for (int i = 0; i < n; ++i) {
+    max_rank = std::max(max_rank, L[i]->rank);
+    blocks += (L[i]->rows + 127) / 128;
+  }
+  // Outputs of a workgroup, a multiple of 128: as many as make one round of
+  // workgroups at rank 64 and up (three a CU; 4096 x 4096, rank 64: 77 us a call,
+  // 81 with two rounds, 88 with three), where summing u costs most, and two
+  // below (4096 x 14336, rank 32: 122 us, 129 with one).
+  const int64_t slots = max_rank <= 32 || M <= q4nx::kLoraWaveRows ? 2048 : 768;
+  a.n_range = 128 * (int)((a.max_tiles * blocks + slots - 1) / slots);
   while (rows / a.n_range > 32768) a.n_range *= 2;   // grid limit
   int wg = 0;
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };

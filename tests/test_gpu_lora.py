@@ -241,3 +241,40 @@ def test_captured_replayed_and_on_another_stream(M):
     c.dids.copy_(dev_i32(c.ids))
     graph.replay()
     c.check(host(y))
+
+
+def test_outputs_past_two_gigabytes():
+    """Rows beyond the kernels' 31-bit offsets run as pieces of the call, one after the other."""
+    M, K, N, R, E = 1100, 256, 1 << 19, 8, 2
+    print(f"lora M={M} N={N}: y of {M * N * 4 / 2 ** 30:.1f} GiB", flush=True)
+    g = synth.rng("gpu-lora", "large")
+    A = synth.bf16_bits(g.standard_normal((E, R, K)) / np.sqrt(K))
+    B = synth.bf16_bits(g.standard_normal((E, N, R)) / np.sqrt(R))
+    x = synth.bf16_bits(g.standard_normal((M, K)))
+    ids = _ids("random", M, E)
+    ids[0], ids[M - 1] = 7, -1               # an id outside in the first piece only
+    dx, dids, da, db = dev_bf16(x), dev_i32(ids), dev_bf16(A), dev_bf16(B)
+    L = q().lora_table(E, R, N, K, da, db, dev_f32(np.ones(E)))
+    ws = torch.empty(q().lora_ws(L, M), dtype=torch.uint8, device="cuda")
+    y = torch.ones((M, N), device="cuda")
+    q().lora_add(L, dx, dids, M, y, ws)
+    assert int(host(ws[:4].view(torch.int32))[0]) == 1
+    per = (1 << 31) // (4 * N)
+    rows = [0, 1, per - 1, per, per + 1, M - 2, M - 1]
+    cols = np.r_[0:64, N // 2:N // 2 + 64, N - 64:N]
+    got = host(y[rows][:, torch.from_numpy(cols).cuda()])
+    want, mag = oracle.lora_ref(synth.bf16_to_f32(x[rows]), synth.bf16_to_f32(A), synth.bf16_to_f32(B[:, cols]),
+                                np.ones(E), ids[rows], np.ones((len(rows), len(cols))))
+    assert (np.abs(got - want) <= 2.0 ** -23 * ((K + 3 * R + 80) * mag + 1 + np.abs(want))).all()
+    dids.fill_(-1)
+    q().lora_add(L, dx, dids, M, y, ws)
+    assert int(host(ws[:4].view(torch.int32))[0]) == 0
+
+
+@pytest.mark.parametrize("E,kind", [(1, "one"), (2, "each"), (3, "some"), (6, "random"), (15, "each"), (40, "each")])
+@pytest.mark.parametrize("M", [16, 31, 32, 47, 64])
+def test_tiles_of_few_and_of_many_adapters(M, E, kind):
+    """Both ways in which a wave finds its tile, with tiles that fill up and that do not."""
+    c = Case("tiles", M, 256, 64, 8, E, _ids(kind, M, E, seed=M))
+    c.check(c.run())
+    c.check(c.run(in_place=True))

@@ -10,21 +10,28 @@
 // what lies below 2^-24.
 //
 // Two launches.  k_logprob_part: a wave streams a part of a row through
-// registers in chunks of 256 NQ logits, the next chunk's loads in flight, and
-// keeps (m, rest, t = sum e d) against the wave's maximum so far, and the top k
-// so far.  k_logprob_join: one wave a row adds the parts, each by
-// f = exp(m_part - m): rest += (1 + rest_p) f (rest_p alone for one part that
-// has m), t += f (t_p + (1 + rest_p)(m_part - m)).
+// registers in chunks of 256 NQ logits, and keeps (m, rest, t = sum e d) against
+// the wave's maximum so far, and the top k so far.  k_logprob_join: one wave a
+// row adds the parts, each by f = exp(m_part - m): rest += (1 + rest_p) f
+// (rest_p alone for one part that has m), t += f (t_p + (1 + rest_p)(m_part - m)).
 //
 // Top k of a wave: a threshold T that at least k values seen reach, and a
-// gathering space in LDS that holds every value seen above T and, of those
-// equal to T, the first ones.  The first chunk's T comes from the 64 lanes' own
-// maxima: a value that k of them reach.  After that only the values above T
-// are gathered (k / j of chunk j on average, for random logits), by ballots; a
-// full space is cut down to its k largest.  Order among the gathered: count,
-// for each, how many have a larger key.  The key is topk.h's: larger value,
-// then lower index.  Should more values lie above T than the space holds, T is
-// raised by bisection over the order of fp32 first.
+// gathering space in LDS that holds the index of every value seen above T and,
+// of those equal to T, the first ones.  The first chunk's T comes from the 64
+// lanes' own maxima: a value that k of them reach.  After that only the values
+// above T are gathered (k / j of chunk j on average, for random logits): each
+// lane marks its hits in a word, a sum over the lanes below gives it its place.
+// A full space is cut down to its k largest.  At the end the gathered values
+// are read again, as keys (topk.h's: larger value, then lower index), and
+// ordered by counting, for each, how many are larger.  Should more values lie
+// above T than the space holds, T is raised by bisection over the order of
+// fp32 first.
+//
+// Many rows are bound by HBM: 1000 rows of 151936 logits, 608 MB, take 113 us
+// (5.4 TB/s; a large copy reaches 5.2).  64 rows (39 MB, in the Infinity Cache)
+// take 13 us with k = 0 and 17.7 with k = 20: the latency of one chunk a wave,
+// of which the exponentials are a third and the top k a third; one row 7.1 and
+// 9.5 us, two launches of little more than an empty one each.
 #include <algorithm>
 
 #include "logprobs_args.h"
@@ -39,7 +46,6 @@ typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));   // rows 
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr int kGather = 256;   // keys above T that a wave can gather
 constexpr int kRoom = kGather + kLogprobMaxK;   // with those equal to it
-constexpr int kGatherLds = kRoom + 4 + kLogprobMaxK;   // with the padding, and the best of them when cut down
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
@@ -85,11 +91,26 @@ __device__ __forceinline__ float of_ord(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 
+__device__ __forceinline__ float wave_min(float v) { return -wave_max(-v); }
+
+// Sum over the lanes below (row_shr and row_bcast as above), and over all.
+__device__ __forceinline__ int sum_below(int v, int& all) {
+  int s = v;
+  s += __builtin_amdgcn_update_dpp(0, s, 0x111, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x112, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x114, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x118, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x142, 0xA, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x143, 0xC, 0xF, false);
+  all = __builtin_amdgcn_readlane(s, 63);
+  return s - v;
+}
+
 // A bound that at least k lanes' values reach (k <= 64) and, unless values are
-// alike, not many more: bisection over unsigned order between 0, which all
-// reach, and past the largest.
-__device__ __forceinline__ uint32_t reached_by_k(uint32_t v, uint32_t top, int k) {
-  uint32_t lo = 0, hi = top;
+// alike, not many more: bisection over unsigned order between lo, which all
+// reach, and top, the largest.
+__device__ __forceinline__ uint32_t reached_by_k(uint32_t v, uint32_t lo, uint32_t top, int k) {
+  uint32_t hi = top;
   if (__popcll(__ballot(v >= top)) >= k) return top;
   while (hi - lo > 1) {
     const uint32_t mid = lo + (hi - lo) / 2;
@@ -121,78 +142,78 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// How many of the n keys at g (padded with zeros to a multiple of 4) are larger than `key`.
+// How many of the n keys at g (padded with zeros to a multiple of U) are larger than `key`.
+template <int U>
 __device__ __forceinline__ int larger_keys(const uint64_t* g, int n, uint64_t key) {
   int c = 0;
-  for (int j = 0; j < n; j += 4) {
+  for (int j = 0; j < n; j += U) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c += g[j + i] > key ? 1 : 0;
+    for (int i = 0; i < U; ++i) c += g[j + i] > key ? 1 : 0;
   }
   return c;
 }
 
-// The largest min(k, n) of the n keys at g, in decreasing order, to out (not g).
-// One piece of 64 at a time, so that few registers are held beside the chunk's.
-__device__ __forceinline__ void select_k(uint64_t* g, int n, int k, int lane, uint64_t* out) {
-  if (lane < 4) g[n + lane] = 0;
+// A wave's gathering space: the indexes gathered, their keys when they are
+// ordered, and the best of them when the space is cut down.
+struct Gather {
+  int32_t index[kRoom];
+  uint64_t key[kRoom + 8];
+  uint64_t best[kLogprobMaxK];
+};
+
+// The keys of the largest min(k, n) of the n values gathered, in decreasing
+// order, to out (not in g.key).  The values are read again: all at once, and
+// only here.  One piece of 64 at a time, so that few registers are held beside
+// a chunk's.
+template <int U>
+__device__ __forceinline__ void select_k(Gather& g, const float* row, int n, int k, int lane, uint64_t* out) {
+  wave_lds_fence();
+#pragma unroll 1
+  for (int e = lane; e < n; e += 64) g.key[e] = topk_key(row[g.index[e]], g.index[e]);
+  if (lane < U) g.key[n + lane] = 0;
   wave_lds_fence();
 #pragma unroll 1
   for (int e = lane; e - lane < n; e += 64) {
-    const uint64_t mine = e < n ? g[e] : 0;
-    const int at = larger_keys(g, n, mine);
+    const uint64_t mine = e < n ? g.key[e] : 0;
+    const int at = larger_keys<U>(g.key, n, mine);
     if (mine != 0 && at < k) out[at] = mine;
   }
 }
 
-__device__ __forceinline__ uint64_t raw_key(float v, int i) {
-  return ((uint64_t)__float_as_uint(v) << 32) | ~(uint32_t)i;
-}
-
 // The running state of a wave.
 struct TopState {
-  int n;     // gathered keys
+  int n;     // gathered values
   float T;   // at least k values seen reach it; -inf before there are k
 };
 
 // Takes a chunk's values (value q, c of lane l has index i0 + 256 q + c, i0
-// with 4 l in it) into the gathered keys.  qm: maxima of the quads, lm: the
-// lane's, cm: the chunk's.
+// with 4 l in it) into the gathered ones.  lm: the lane's maximum, cm: the
+// chunk's.
 template <int NQ>
-__device__ __forceinline__ void take_chunk(const f32x4 (&v)[NQ], const float (&qm)[NQ], float lm, float cm, int i0,
-                                           int k, int lane, uint64_t* g, TopState& st) {
+__device__ __forceinline__ void take_chunk(const f32x4 (&v)[NQ], float lm, float cm, int i0, const float* row, int k,
+                                           int lane, Gather& g, TopState& st) {
   const bool fresh = st.T == neg_inf();   // fewer than k so far: this chunk's own bound
   float T = st.T;
   if (fresh) {
-    const uint32_t o = k == 1 ? ord_of(cm) : reached_by_k(ord_of(lm), ord_of(cm), k);
+    const uint32_t o = k == 1 ? ord_of(cm) : reached_by_k(ord_of(lm), ord_of(wave_min(lm)), ord_of(cm), k);
     T = o <= ord_of(neg_inf()) ? neg_inf() : of_ord(o);
   }
-  // Gathered as (value bits, ~index) and made into keys afterwards: the few
-  // that are there, not every value.
-  int n;
+  uint32_t hits;   // bit 4 NQ - 1 - (4 q + c): value q, c is above T
+  int at, above;
   for (;;) {
-    n = st.n;
-    int i1 = i0;
-    asm volatile("" : "+v"(i1));   // keeps the indexes of all values from being held through the loop
+    hits = 0;
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      if (__ballot(qm[q] > T) == 0) continue;
+    for (int q = 0; q < NQ; ++q)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint64_t b = __ballot(v[q][c] > T);
-        const int at = n + lanes_below(b, lane);
-        if (v[q][c] > T && at < kGather) g[at] = raw_key(v[q][c], i1 + 256 * q + c);
-        n += __popcll(b);
-      }
-    }
-    if (n <= kGather) break;
+      for (int c = 0; c < 4; ++c) hits = hits + hits + (v[q][c] > T ? 1u : 0u);
+    at = st.n + sum_below(__popc(hits), above);
+    if (st.n + above <= kGather) break;
     if (st.n > k) {   // make room
-      uint64_t* best = g + kRoom + 4;
-      select_k(g, st.n, k, lane, best);
+      select_k<4>(g, row, st.n, k, lane, g.best);
       wave_lds_fence();
-      if (lane < k) g[lane] = best[lane];
-      wave_lds_fence();
+      if (lane < k) g.index[lane] = (int32_t)~(uint32_t)g.best[lane];
       st.n = k;
-      T = fmaxf(T, of_ord((uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(best[k - 1] >> 32))));
+      T = fmaxf(T, of_ord((uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(g.best[k - 1] >> 32))));
       continue;
     }
     // more above T than there is room for: raise it
@@ -208,9 +229,17 @@ __device__ __forceinline__ void take_chunk(const f32x4 (&v)[NQ], const float (&q
     }
     T = of_ord(hi);
   }
+  while (__ballot(hits != 0)) {   // a value of each lane that has one, the first first
+    if (hits != 0) {
+      const int b = 31 - __clz(hits), i = 4 * NQ - 1 - b;
+      g.index[at++] = i0 + 64 * (i & ~3) + (i & 3);
+      hits ^= 1u << b;
+    }
+  }
+  st.n += above;
   // fewer than k of this chunk above its own bound: those equal to it, the lowest indexes first
   if (T != st.T && T > neg_inf()) {
-    int need = k - (n - st.n);
+    int need = k - above;
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       if (need <= 0) continue;
@@ -225,16 +254,13 @@ __device__ __forceinline__ void take_chunk(const f32x4 (&v)[NQ], const float (&q
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         if (v[q][c] == T) {
-          if (before < need) g[n + before] = raw_key(v[q][c], i0 + 256 * q + c);
+          if (before < need) g.index[st.n + before] = i0 + 256 * q + c;
           ++before;
         }
-      n += min(all, need);
+      st.n += min(all, need);
       need -= all;
     }
   }
-  wave_lds_fence();
-  for (int e = st.n + lane; e < n; e += 64) g[e] = topk_key(__uint_as_float((uint32_t)(g[e] >> 32)), ~(uint32_t)g[e]);
-  st.n = n;
   st.T = T;
 }
 
@@ -270,13 +296,10 @@ __device__ __forceinline__ void load_chunk(const float* row, int end, int i0, bo
   }
 }
 
-#ifndef Q4NX_LP_OCC
-#define Q4NX_LP_OCC
-#endif
 template <int NQ>
-__global__ __launch_bounds__(256 Q4NX_LP_OCC) void k_logprob_part(LogprobArgs a) {
+__global__ __launch_bounds__(256) void k_logprob_part(LogprobArgs a) {
   constexpr int kChunk = 256 * NQ;
-  __shared__ uint64_t gath[4][kGatherLds];
+  __shared__ Gather gath[4];
   // the wave's number as a scalar: rows, bounds and branches then are scalar too
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t unit = blockIdx.x * 4 + wave;
@@ -284,7 +307,7 @@ __global__ __launch_bounds__(256 Q4NX_LP_OCC) void k_logprob_part(LogprobArgs a)
   const int m_row = unit / (uint32_t)a.parts, part = unit - (uint32_t)m_row * a.parts;
   const float* row = a.y + (size_t)m_row * a.ldy;
   const int begin = part * a.part_n, end = min(a.n, begin + a.part_n);
-  uint64_t* g = gath[wave];
+  Gather& g = gath[wave];
   TopState st = {0, neg_inf()};
   float m = neg_inf(), rest = 0.f, t = 0.f;   // rest, t: this lane's share, but for the one maximum set apart
   for (int c0 = begin; c0 < end; c0 += kChunk) {
@@ -292,15 +315,12 @@ __global__ __launch_bounds__(256 Q4NX_LP_OCC) void k_logprob_part(LogprobArgs a)
     load_chunk<NQ>(row, end, c0 + 4 * lane, c0 + kChunk <= end, v);
     // NaNs are passed over: a maximum takes the other operand, comparisons are
     // false, and the clamp of d below turns them into nothing.
-    float qm[NQ], lm = neg_inf();
+    float lm = neg_inf();
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      qm[q] = fmaxf(fmaxf(v[q][0], v[q][1]), fmaxf(v[q][2], v[q][3]));
-      lm = fmaxf(lm, qm[q]);
-    }
+    for (int q = 0; q < NQ; ++q) lm = fmaxf(lm, fmaxf(fmaxf(v[q][0], v[q][1]), fmaxf(v[q][2], v[q][3])));
     const float cm = wave_max(lm);
     if (cm == neg_inf()) continue;   // nothing left in this chunk
-    if (a.k > 0 && cm > st.T) take_chunk<NQ>(v, qm, lm, cm, c0 + 4 * lane, a.k, lane, g, st);
+    if (a.k > 0 && cm > st.T) take_chunk<NQ>(v, lm, cm, c0 + 4 * lane, row, a.k, lane, g, st);
     // exp(-200) is 0 in fp32: the clamp changes no sum and keeps -inf and NaN out of e * d
     if (cm >= m) {
       if (cm > m && m != neg_inf()) {   // the old maximum joins the rest
@@ -342,7 +362,7 @@ __global__ __launch_bounds__(256 Q4NX_LP_OCC) void k_logprob_part(LogprobArgs a)
   if (lane == 0) a.stats[unit] = f32x4{m, rest, t, 0.f};
   if (a.k > 0) {
     uint64_t* keys = a.keys + (size_t)unit * a.k;
-    select_k(g, st.n, a.k, lane, keys);
+    select_k<8>(g, row, st.n, a.k, lane, keys);
     if (lane >= st.n && lane < a.k) keys[lane] = 0;
   }
 }
@@ -472,7 +492,7 @@ __global__ __launch_bounds__(64) void k_logprob_join(LogprobArgs a) {
   const size_t o0 = (size_t)m_row * k;
   for (int e0 = 0; e0 < n; e0 += 64) {
     const uint64_t mine = e0 + lane < n ? g[e0 + lane] : 0;
-    const int at = larger_keys(g, n, mine);
+    const int at = larger_keys<4>(g, n, mine);
     if (mine && at < k) {
       a.top_ids[o0 + at] = (int32_t)~(uint32_t)mine;
       if (a.top_logp) a.top_logp[o0 + at] = logp_of(of_ord((uint32_t)(mine >> 32)));

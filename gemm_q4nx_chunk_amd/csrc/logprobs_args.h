@@ -25,19 +25,15 @@ struct LogprobArgs {
 };
 
 constexpr int kLogprobChunk = 2048;    // logits that a wave holds in registers at a time
-#ifndef Q4NX_LP_WAVES
-#define Q4NX_LP_WAVES 16384
-#endif
-#ifndef Q4NX_LP_SMALL
-#define Q4NX_LP_SMALL 2048
-#endif
 
-// Logits of a part.  Few waves: 1024 in one go.  Else whole chunks, as many as
-// leave about 16384 waves.
+// Logits of a part.  Up to 2048 waves of 1024 logits: those, in one go (16 rows
+// of 50001: 10.8 us, 12.8 with 2048 a wave).  Else whole chunks, as many as leave
+// about 16384 waves (1000 rows of 151936: 113 us; with 8192 waves 117, with 4096
+// 118), for a wave's first chunk costs the most.
 inline int logprob_part_n(int n, int M) {
-  if ((int64_t)M * ((n + 1023) / 1024) <= Q4NX_LP_SMALL && n <= kLogprobMaxParts * 1024) return 1024;
+  if ((int64_t)M * ((n + 1023) / 1024) <= 2048 && n <= kLogprobMaxParts * 1024) return 1024;
   const int chunks = (n + kLogprobChunk - 1) / kLogprobChunk;
-  int parts = Q4NX_LP_WAVES / M;
+  int parts = 16384 / M;
   parts = parts < 1 ? 1 : parts > chunks ? chunks : parts;
   parts = parts > kLogprobMaxParts ? kLogprobMaxParts : parts;
   return (chunks + parts - 1) / parts * kLogprobChunk;

@@ -1397,8 +1397,9 @@ void lora_shape(const q4nx_lora* const* L, int n, int M, LoraShape& sh) {
   a.n_adapters = L[0]->n_adapters;
   a.M = M;
   a.cols = L[0]->cols;
-  a.max_tiles = q4nx::lora_max_tiles(M, a.n_adapters);
-  const int tiles = (M + 63) / 64;   // at least
+  a.tile_rows = q4nx::lora_tile_rows(M, a.n_adapters, a.cols);
+  a.max_tiles = q4nx::lora_max_tiles(M, a.n_adapters, a.tile_rows);
+  const int tiles = (M + a.tile_rows - 1) / a.tile_rows;   // at least
   int groups = 0;
   int64_t rows = 0;
   for (int i = 0; i < n; ++i) {
@@ -1427,14 +1428,14 @@ void lora_shape(const q4nx_lora* const* L, int n, int M, LoraShape& sh) {
   // workgroups at rank 64 and up (three a CU; 4096 x 4096, rank 64: 77 us a call,
   // 81 with two rounds, 88 with three), where summing u costs most, and two
   // below (4096 x 14336, rank 32: 122 us, 129 with one).
-  const int64_t slots = max_rank <= 32 || M <= q4nx::kLoraWaveRows ? 2048 : 768;
+  const int64_t slots = max_rank <= 32 || a.tile_rows == 16 ? 2048 : 768;
   a.n_range = 128 * (int)((a.max_tiles * blocks + slots - 1) / slots);
   while (rows / a.n_range > 32768) a.n_range *= 2;   // grid limit
   int wg = 0;
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   size_t o = 256;
   sh.sorted = o;
-  o = up(o + (size_t)a.max_tiles * 64 * 4);
+  o = up(o + (size_t)a.max_tiles * a.tile_rows * 4);
   sh.tiles = o;
   o = up(o + (size_t)a.max_tiles * sizeof(q4nx::LoraTile));
   for (int i = 0; i < n; ++i) {

@@ -106,8 +106,11 @@ __device__ __forceinline__ int sum_below(int v, int& all) {
   return s - v;
 }
 
+// How many may reach a bound that at least k have to reach.
+__host__ __device__ __forceinline__ int reach(int k) { return k + k / 4 + 1; }
+
 // A bound that at least k lanes' values reach (k <= 64) and, unless values are
-// alike, not many more: bisection over unsigned order between lo, which all
+// alike, at most reach(k): bisection over unsigned order between lo, which all
 // reach, and top, the largest.
 __device__ __forceinline__ uint32_t reached_by_k(uint32_t v, uint32_t lo, uint32_t top, int k) {
   uint32_t hi = top;
@@ -118,7 +121,7 @@ __device__ __forceinline__ uint32_t reached_by_k(uint32_t v, uint32_t lo, uint32
     if (c < k) hi = mid;
     else {
       lo = mid;
-      if (c <= k + k / 4 + 1) break;
+      if (c <= reach(k)) break;
     }
   }
   return lo;
@@ -195,8 +198,9 @@ __device__ __forceinline__ void take_chunk(const f32x4 (&v)[NQ], float lm, float
   const bool fresh = st.T == neg_inf();   // fewer than k so far: this chunk's own bound
   float T = st.T;
   if (fresh) {
-    const uint32_t o = k == 1 ? ord_of(cm) : reached_by_k(ord_of(lm), ord_of(wave_min(lm)), ord_of(cm), k);
-    T = o <= ord_of(neg_inf()) ? neg_inf() : of_ord(o);
+    if (k == 1) T = cm;
+    else if (__popcll(__ballot(lm > neg_inf())) > reach(k))   // else T stays below them all
+      T = of_ord(reached_by_k(ord_of(lm), std::max(ord_of(wave_min(lm)), ord_of(neg_inf())), ord_of(cm), k));
   }
   uint32_t hits;   // bit 4 NQ - 1 - (4 q + c): value q, c is above T
   int at, above;
@@ -368,18 +372,20 @@ __global__ __launch_bounds__(256) void k_logprob_part(LogprobArgs a) {
 }
 
 // Joins the parts of a row, one wave a row.  Lane l owns parts l, l + 64, ...
-// (four at most) and loads the first four keys of each of their lists ahead.
-// The row's top k: T, a key that at least k known keys reach, is at most the
-// row's k-th, so the keys of at least T are gathered from the lists (in
-// decreasing order each: a list ends at its first smaller key) and ordered by
-// counting.  The known keys are the lanes' best ones where every lane has a
-// list, else (fewer than 64 parts, of which k may be more than there are) the
-// loaded ones.  At most k + k / 4 + 1 of them reach T: so many lanes' lists whole,
-// or so many keys and what follows the fours among them, bound the room.
-constexpr int kFirst = 4;
+// (four at most).  The row's top k: T, a key that at least k known keys reach,
+// is at most the row's k-th, so the keys of at least T are gathered from the
+// parts' lists and ordered by counting.  The known keys, and what at most is
+// gathered (the host sizes the LDS for it), when reach(k) of them reach T:
+//   up to 512 keys in all: every one, eight a lane; those.
+//   64 parts and more: the lanes' best; the lanes' whole lists.  (A list is in
+//     decreasing order: it ends at its first key below T.)
+//   else: the first four of each list; those, and what follows the fours.
+constexpr int kFirst = 4;    // keys of a list loaded ahead
+constexpr int kAllKeys = 8;  // keys a lane, where all are loaded
 inline int join_room(int parts, int k) {
-  const int reach = k + k / 4 + 1;
-  return parts >= 64 ? std::min(64, reach) * ((parts + 63) / 64) * k : reach + reach / kFirst * std::max(0, k - kFirst);
+  if (parts * k <= 64 * kAllKeys) return std::min(parts * k, reach(k));
+  return parts >= 64 ? std::min(64, reach(k)) * ((parts + 63) / 64) * k
+                     : reach(k) + reach(k) / kFirst * std::max(0, k - kFirst);
 }
 
 __global__ __launch_bounds__(64) void k_logprob_join(LogprobArgs a) {
@@ -390,18 +396,19 @@ __global__ __launch_bounds__(64) void k_logprob_join(LogprobArgs a) {
   // everything whose place is known, in flight at once
   const int tok = lane < a.n_tok ? a.tokens[(size_t)m_row * a.n_tok + lane] : -1;
   f32x4 s[4];
-  uint64_t key[4][kFirst];
+  uint64_t key[4][kFirst];   // all at once: key i of lane l at 64 i + l of the parts' keys; else key j of part l + 64 i
+  const bool all_at_once = a.parts * k <= 64 * kAllKeys;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int p = lane + 64 * i;
     s[i] = f32x4{neg_inf(), 0.f, 0.f, 0.f};
+    if (p < a.parts) s[i] = a.stats[u0 + p];
 #pragma unroll
-    for (int j = 0; j < kFirst; ++j) key[i][j] = 0;
-    if (p < a.parts) {
-      s[i] = a.stats[u0 + p];
-#pragma unroll
-      for (int j = 0; j < kFirst; ++j)
-        if (j < k) key[i][j] = a.keys[(u0 + p) * k + j];
+    for (int j = 0; j < kFirst; ++j) {
+      const int e = 64 * (kFirst * i + j) + lane;
+      key[i][j] = 0;
+      if (all_at_once ? i < kAllKeys / kFirst && e < a.parts * k : p < a.parts && j < k)
+        key[i][j] = a.keys[all_at_once ? u0 * k + e : (u0 + p) * k + j];
     }
   }
   const bool inside = tok >= 0 && tok < a.n;
@@ -442,28 +449,41 @@ __global__ __launch_bounds__(64) void k_logprob_join(LogprobArgs a) {
   if (k == 0) return;
 
   const int lists = (a.parts + 63) / 64;
+  const bool by_lane = !all_at_once && a.parts >= 64;
   uint64_t best = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) best = key[i][0] > best ? key[i][0] : best;
-  const bool by_lane = a.parts >= 64;
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < kFirst; ++j)
+      if (j == 0 || all_at_once) best = key[i][j] > best ? key[i][j] : best;
   const uint64_t top = wave_max_u64(best);
-  uint64_t T = k == 1 ? top : 0;
-  for (uint64_t hi = k == 1 ? 0 : top + 1; hi > T + 1;) {   // fewer than k reach hi
-    const uint64_t mid = T + (hi - T) / 2;
-    int c = __popcll(__ballot((by_lane ? best : key[0][0]) >= mid));
+  auto reached = [&](uint64_t at) {
+    int c = __popcll(__ballot((by_lane ? best : key[0][0]) >= at));
     if (!by_lane) {
 #pragma unroll
-      for (int j = 1; j < kFirst; ++j) c += __popcll(__ballot(key[0][j] >= mid));
+      for (int j = 1; j < kFirst; ++j) c += __popcll(__ballot(key[0][j] >= at));
     }
-    if (c < k) hi = mid;
-    else {
-      T = mid;
-      if (c <= k + k / 4 + 1) break;
+    if (all_at_once) {
+#pragma unroll
+      for (int j = 0; j < kFirst; ++j) c += __popcll(__ballot(key[1][j] >= at));
+    }
+    return c;
+  };
+  uint64_t T = k == 1 ? top : 1;   // 1: every key
+  if (k > 1 && reached(1) > reach(k)) {
+    for (uint64_t hi = top + 1; hi > T + 1;) {   // fewer than k reach hi
+      const uint64_t mid = T + (hi - T) / 2;
+      const int c = reached(mid);
+      if (c < k) hi = mid;
+      else {
+        T = mid;
+        if (c <= reach(k)) break;
+      }
     }
   }
   int n = 0;
   auto add = [&](uint64_t v) {
-    const bool in = v != 0 && v >= T;
+    const bool in = v >= T && v != 0;
     const uint64_t b = __ballot(in);
     const int at = n + lanes_below(b, lane);
     if (in) g[at] = v;
@@ -472,13 +492,13 @@ __global__ __launch_bounds__(64) void k_logprob_join(LogprobArgs a) {
   };
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (i >= lists) continue;
+    if (i >= (all_at_once ? kAllKeys / kFirst : lists)) continue;
     uint64_t b = 0;
 #pragma unroll
     for (int j = 0; j < kFirst; ++j) b = add(key[i][j]);
     const uint64_t* list = a.keys + (u0 + min(lane + 64 * i, a.parts - 1)) * k;
     bool mine = key[i][kFirst - 1] != 0 && key[i][kFirst - 1] >= T;
-    for (int j0 = kFirst; b != 0 && j0 < k; j0 += kFirst) {
+    for (int j0 = kFirst; !all_at_once && b != 0 && j0 < k; j0 += kFirst) {
       uint64_t v[kFirst];
 #pragma unroll
       for (int j = 0; j < kFirst; ++j) v[j] = mine && j0 + j < k ? list[j0 + j] : 0;

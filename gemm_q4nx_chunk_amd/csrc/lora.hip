@@ -9,8 +9,9 @@
 //
 // Launches, on one stream:
 //   route   (more than 64 rows) one workgroup counts the rows of each adapter
-//           and cuts them into tiles of up to 64.  Up to 64 rows every wave of
-//           the other two finds its tile, of up to 16 rows, itself.
+//           and cuts them into tiles of up to 64, or of 16 where few rows share
+//           an adapter.  Up to 64 rows every wave of the other two finds its
+//           tile, of up to 16 rows, itself.
 //   shrink  u = A_e x for a tile, columns split over workgroups and waves,
 //           bf16 matrix cores, fp32 sums: the parts go to the workspace.
 //   expand  sums the parts of u in order, times scale_e, and adds B_e u to the
@@ -51,7 +52,7 @@ __device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirst
 
 // Fills rows[0..cnt) with the tile of workgroup t.  Call with all threads of
 // the workgroup.  SUB: 16-row pieces of a tile.
-//   SUB == 1 (at most 64 rows): every wave finds it by itself, and all write the
+//   up to 64 rows (SUB == 1): every wave finds it by itself, and all write the
 //     same rows: a wave reads what it wrote, no barrier.  With few adapters, so
 //     that few tiles are possible, by walking the adapters in order of their
 //     first rows; else workgroup t is row t's, and has a tile if row t opens one.
@@ -61,7 +62,7 @@ __device__ __forceinline__ Tile find_tile(const LoraArgs& a, int t, int32_t* row
   constexpr int kTile = 16 * SUB;
   const int tid = threadIdx.x, lane = tid & 63;
   Tile tile;
-  if constexpr (SUB > 1) {
+  if (SUB > 1 || a.M > kLoraWaveRows) {
     // everything at once: places past the tile's rows hold no row and are not used
     if (tid < kTile) rows[tid] = a.sorted[kTile * t + tid];
     tile.e = scalar(a.tiles[t].e);
@@ -117,22 +118,35 @@ __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast
 // ---------------------------------------------------------------------------
 // route
 // ---------------------------------------------------------------------------
+// Sum over the lanes up to this one, by DPP: within rows of 16 lanes
+// (row_shr 1, 2, 4, 8), then across them (row_bcast 15 and 31).
+__device__ __forceinline__ int sum_to_here(int s) {
+  s += __builtin_amdgcn_update_dpp(0, s, 0x111, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x112, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x114, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x118, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x142, 0xA, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x143, 0xC, 0xF, false);
+  return s;
+}
+
 // Counting sort of up to 4096 rows by adapter, bin n_adapters for rows without
-// one.  The order of a bin's rows follows the LDS atomics and is not fixed;
-// neither a row's sums nor its place in y depend on it.
+// one: count, prefix sum of the bins' tiles, and every row goes to its place in
+// its tile; a tile's first row writes its record.  The order of a bin's rows
+// follows the LDS atomics and is not fixed; neither a row's sums nor its place
+// in y depend on it.  Bound by its chain of latencies.
 __global__ __launch_bounds__(1024) void k_lora_route(LoraArgs a) {
-  constexpr int kBins = kLoraMaxAdapters + 1, kPer = (kBins + 1023) / 1024;
+  constexpr int kPer = (kLoraMaxAdapters + 1 + 1023) / 1024;   // bins a thread
+  constexpr int kRowsPer = kLoraMaxRows / 1024;
   __shared__ int32_t cnt[kPer * 1024], start[kPer * 1024];
   __shared__ int32_t wsum[16];
   __shared__ uint32_t bad;
   const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6);
-  constexpr int kRowsPer = kLoraMaxRows / 1024;
   int id[kRowsPer];
 #pragma unroll
   for (int i = 0; i < kRowsPer; ++i) id[i] = i * 1024 + tid < a.M ? a.ids[i * 1024 + tid] : -1;
   if (tid == 0) bad = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) cnt[i * 1024 + tid] = 0;
+  for (int e = tid; e <= a.n_adapters; e += 1024) cnt[e] = 0;
   __syncthreads();
   uint32_t wrong = 0;
   int bin[kRowsPer], slot[kRowsPer];
@@ -144,68 +158,60 @@ __global__ __launch_bounds__(1024) void k_lora_route(LoraArgs a) {
     wrong |= row && (id[i] < -1 || id[i] >= a.n_adapters) ? 1u : 0u;
   }
   if (wrong) atomicOr(&bad, 1u);
-  // A prompt's rows come in runs: the first lanes' bins are counted for all
-  // their lanes at once, what is left lane by lane.
+  // A prompt's rows come in runs, and a batch may have few adapters: up to four
+  // of a wave's bins, each for all its lanes at once, while they have several;
+  // what is left lane by lane.
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    uint64_t mine[kRowsPer];
-    int first[kRowsPer];
+  for (int i = 0; i < kRowsPer; ++i) {
+    uint64_t todo = __ballot(bin[i] >= 0), mine[4] = {};
+    if (todo == 0) continue;
+    int first[4] = {};
 #pragma unroll
-    for (int i = 0; i < kRowsPer; ++i) {
-      const uint64_t todo = __ballot(bin[i] >= 0 && slot[i] < 0);
-      mine[i] = 0;
-      first[i] = 0;
-      if (todo == 0) continue;
+    for (int r = 0; r < 4; ++r) {
+      if (todo == 0 || (r > 0 && __popcll(mine[r - 1]) < 4)) continue;
       const int b = __builtin_amdgcn_readlane(bin[i], __builtin_ctzll(todo));
-      mine[i] = __ballot(bin[i] == b && slot[i] < 0);
-      if (lane == 0) first[i] = atomicAdd(&cnt[b], __popcll(mine[i]));
+      mine[r] = __ballot(bin[i] == b) & todo;
+      if (lane == 0) first[r] = atomicAdd(&cnt[b], __popcll(mine[r]));
+      todo &= ~mine[r];
     }
 #pragma unroll
-    for (int i = 0; i < kRowsPer; ++i) {
-      const int f = __builtin_amdgcn_readfirstlane(first[i]);
-      if (mine[i] >> lane & 1) slot[i] = f + __popcll(mine[i] & ((1ull << lane) - 1ull));
+    for (int r = 0; r < 4; ++r) {
+      const int f = __builtin_amdgcn_readfirstlane(first[r]);
+      if (mine[r] >> lane & 1) slot[i] = f + __popcll(mine[r] & ((1ull << lane) - 1ull));
     }
-  }
-#pragma unroll
-  for (int i = 0; i < kRowsPer; ++i)
     if (bin[i] >= 0 && slot[i] < 0) slot[i] = atomicAdd(&cnt[bin[i]], 1);
+  }
   __syncthreads();
   // prefix sum of the tiles over the bins, kPer neighbouring bins a thread
   int c[kPer], tiles = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    c[i] = cnt[tid * kPer + i];
-    tiles += (c[i] + 63) / 64;
+    const int e = tid * kPer + i;
+    c[i] = e <= a.n_adapters ? (cnt[e] + a.tile_rows - 1) / a.tile_rows : 0;
+    tiles += c[i];
   }
-  int it = tiles;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int t = __shfl_up(it, off);
-    if (lane >= off) it += t;
-  }
-  if (lane == 63) wsum[wave] = it;
+  const int to_here = sum_to_here(tiles);
+  if (lane == 63) wsum[wave] = to_here;
   __syncthreads();
-  int t0 = it - tiles;
-#pragma unroll
-  for (int w = 0; w < 16; ++w) t0 += w < wave ? wsum[w] : 0;
-  if (tid == 0) a.hdr[0] = (a.more ? a.hdr[0] : 0u) | bad;
+  const int waves = sum_to_here(lane < 16 ? wsum[lane] : 0);   // lane w: tiles of waves 0 .. w
+  int t0 = to_here - tiles + (wave ? __builtin_amdgcn_readlane(waves, wave - 1) : 0);
+  const int n_tiles = __builtin_amdgcn_readlane(waves, 15);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int e = tid * kPer + i;
-    start[e] = t0;
-    for (int k = 0; k < c[i]; k += 64, ++t0)
-      a.tiles[t0] = {e < a.n_adapters ? e : -1, min(64, c[i] - k)};
+    start[tid * kPer + i] = t0;
+    t0 += c[i];
   }
+  if (tid == 0) a.hdr[0] = (a.more ? a.hdr[0] : 0u) | bad;
+  for (int t = n_tiles + tid; t < a.max_tiles; t += 1024) a.tiles[t] = {-1, 0};
   __syncthreads();
-  if (tid == 1023) start[0] = t0;   // bin 0 starts at tile 0: its place holds the number of tiles
-  __syncthreads();
-  for (int t = start[0] + tid; t < a.max_tiles; t += 1024) a.tiles[t] = {-1, 0};
 #pragma unroll
-  for (int i = 0; i < kRowsPer; ++i)
-    if (bin[i] >= 0) {
-      const int t = (bin[i] > 0 ? start[bin[i]] : 0) + slot[i] / 64;
-      a.sorted[64 * t + slot[i] % 64] = i * 1024 + tid;
-    }
+  for (int i = 0; i < kRowsPer; ++i) {
+    if (bin[i] < 0) continue;
+    const int t = start[bin[i]], in = slot[i] / a.tile_rows, first = in * a.tile_rows;
+    a.sorted[t * a.tile_rows + slot[i]] = i * 1024 + tid;
+    if (slot[i] == first)
+      a.tiles[t + in] = {bin[i] < a.n_adapters ? bin[i] : -1, min(a.tile_rows, cnt[bin[i]] - first)};
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -239,7 +245,7 @@ __global__ __launch_bounds__(64 * kLoraShrinkWaves, SUB == 1 ? 4 : 2) void k_lor
   f32x4(*red)[RB][64] = reinterpret_cast<f32x4(*)[RB][64]>(stage);   // after the loop: B > RB, so it fits
   const int tid = threadIdx.x, lane = tid & 63, wave = scalar(tid >> 6);
   const int n = lane & 15, h = lane >> 4;
-  if (SUB == 1 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && wave == 0) {
+  if (a.M <= kLoraWaveRows && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && wave == 0) {
     const int id = lane < a.M ? a.ids[lane] : -1;
     const uint64_t bad = __ballot(id < -1 || id >= a.n_adapters);
     if (lane == 0) a.hdr[0] = (a.more ? a.hdr[0] : 0u) | (bad ? 1u : 0u);
@@ -562,7 +568,7 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
     else if (ks <= 4) Q4NX_LORA_EXPAND(4, SUB);                                                     \
     else Q4NX_LORA_EXPAND(8, SUB);                                                                  \
   } while (0)
-  if (a.M <= kLoraWaveRows) Q4NX_LORA(1);
+  if (a.tile_rows == 16) Q4NX_LORA(1);
   else Q4NX_LORA(4);
 #undef Q4NX_LORA
 #undef Q4NX_LORA_SHRINK

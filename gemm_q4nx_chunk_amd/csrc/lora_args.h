@@ -40,24 +40,36 @@ struct LoraArgs {
   LoraJob job[kLoraMaxJobs];
   int32_t n_jobs, n_adapters;
   int32_t M, cols;
+  int32_t tile_rows;       // 16 or 64
   int32_t more;            // not the call's first rows: the error bit stays set
   int32_t split;           // parts of the columns in the shrink
   int32_t n_range;         // outputs of one expand workgroup
   const uint16_t* x;       // [M][cols]
   const int32_t* ids;      // [M]
   uint32_t* hdr;           // [0]: bit 0 = an id outside [-1, n_adapters)
-  int32_t* sorted;         // [max_tiles][64] each tile's rows (M > kLoraWaveRows)
+  int32_t* sorted;         // [max_tiles][tile_rows] each tile's rows (M > kLoraWaveRows)
   LoraTile* tiles;         // [max_tiles]
   int32_t max_tiles;       // grid x
 };
 
+// Rows of a tile: 16 where adapters have few rows each (1000 rows of 100
+// adapters, rank 64, 4096 x 4096: 45 us, 62 with 64), or the rows are few and
+// short, so that more workgroups pay more than each adapter read fewer times
+// (512 rows of 4 adapters, rank 64, 4096 x 4096: 23.3 and 25.1 us; 1613 x 2304:
+// 20.6 and 23.3; but 1052 x 11264, rank 16: 29.3 and 26.5).
+inline int lora_tile_rows(int M, int n_adapters, int cols) {
+  const int groups = M < n_adapters + 1 ? M : n_adapters + 1;
+  if (M <= kLoraWaveRows || M <= 32 * groups) return 16;
+  return M <= 2048 && (int64_t)M * cols <= 1 << 22 ? 16 : 64;
+}
+
 // Tiles of rows of one adapter (or of none): whole ones, and at most one short
 // one per adapter.  Up to kLoraWaveRows rows, a workgroup per row instead unless
 // that is twice as many.
-inline int lora_max_tiles(int M, int n_adapters) {
+inline int lora_max_tiles(int M, int n_adapters, int tile_rows) {
   const int groups = M < n_adapters + 1 ? M : n_adapters + 1;
-  if (M <= kLoraWaveRows) return 2 * (M / 16 + groups) <= M ? M / 16 + groups : M;
-  return M / 64 + groups;
+  const int tiles = M / tile_rows + groups;
+  return M <= kLoraWaveRows && 2 * tiles > M ? M : tiles;
 }
 
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s);

@@ -69,7 +69,8 @@ inline int lora_tile_rows(int M, int n_adapters, int cols) {
 inline int lora_max_tiles(int M, int n_adapters, int tile_rows) {
   const int groups = M < n_adapters + 1 ? M : n_adapters + 1;
   const int tiles = M / tile_rows + groups;
-  return M <= kLoraWaveRows && 2 * tiles > M ? M : tiles;
+  if (M <= kLoraWaveRows) return 2 * tiles > M ? M : tiles;
+  return (tiles + 7) / 8 * 8;   // eight at a time, one on each XCD
 }
 
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s);

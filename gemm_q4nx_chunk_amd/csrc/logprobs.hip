@@ -107,7 +107,7 @@ __device__ __forceinline__ int sum_below(int v, int& all) {
 }
 
 // How many may reach a bound that at least k have to reach.
-__host__ __device__ __forceinline__ int reach(int k) { return k + k / 4 + 1; }
+__host__ __device__ __forceinline__ int reach(int k) { return k + k / 4 + 4; }
 
 // A bound that at least k lanes' values reach (k <= 64) and, unless values are
 // alike, at most reach(k): bisection over unsigned order between lo, which all
@@ -376,19 +376,27 @@ __global__ __launch_bounds__(256) void k_logprob_part(LogprobArgs a) {
 // is at most the row's k-th, so the keys of at least T are gathered from the
 // parts' lists and ordered by counting.  The known keys, and what at most is
 // gathered (the host sizes the LDS for it), when reach(k) of them reach T:
-//   up to 512 keys in all: every one, eight a lane; those.
-//   64 parts and more: the lanes' best; the lanes' whole lists.  (A list is in
-//     decreasing order: it ends at its first key below T.)
-//   else: the first four of each list; those, and what follows the fours.
+//   kLanes (64 parts and more): the lanes' best; the lanes' whole lists.  (A
+//     list is in decreasing order: it ends at its first key below T.)
+//   kAll (up to 512 keys): every one, eight a lane; those.
+//   kFours: the first four of each list; those, and what follows the fours.
+enum JoinKeys { kLanes, kAll, kFours };
 constexpr int kFirst = 4;    // keys of a list loaded ahead
 constexpr int kAllKeys = 8;  // keys a lane, where all are loaded
+inline JoinKeys join_keys(int parts, int k) {
+  return parts >= 64 ? kLanes : parts * k <= 64 * kAllKeys ? kAll : kFours;
+}
 inline int join_room(int parts, int k) {
-  if (parts * k <= 64 * kAllKeys) return std::min(parts * k, reach(k));
-  return parts >= 64 ? std::min(64, reach(k)) * ((parts + 63) / 64) * k
-                     : reach(k) + reach(k) / kFirst * std::max(0, k - kFirst);
+  switch (join_keys(parts, k)) {
+    case kAll: return std::min(parts * k, reach(k));
+    case kLanes: return std::min(64, reach(k)) * ((parts + 63) / 64) * k;
+    default: return reach(k) + reach(k) / kFirst * std::max(0, k - kFirst);
+  }
 }
 
+template <JoinKeys KEYS>
 __global__ __launch_bounds__(64) void k_logprob_join(LogprobArgs a) {
+  constexpr bool all_at_once = KEYS == kAll, by_lane = KEYS == kLanes;
   extern __shared__ uint64_t g[];   // join_room keys and 4
   const int m_row = blockIdx.x, lane = threadIdx.x, k = a.k;
   const float* row = a.y + (size_t)m_row * a.ldy;
@@ -397,7 +405,6 @@ __global__ __launch_bounds__(64) void k_logprob_join(LogprobArgs a) {
   const int tok = lane < a.n_tok ? a.tokens[(size_t)m_row * a.n_tok + lane] : -1;
   f32x4 s[4];
   uint64_t key[4][kFirst];   // all at once: key i of lane l at 64 i + l of the parts' keys; else key j of part l + 64 i
-  const bool all_at_once = a.parts * k <= 64 * kAllKeys;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int p = lane + 64 * i;
@@ -405,10 +412,13 @@ __global__ __launch_bounds__(64) void k_logprob_join(LogprobArgs a) {
     if (p < a.parts) s[i] = a.stats[u0 + p];
 #pragma unroll
     for (int j = 0; j < kFirst; ++j) {
-      const int e = 64 * (kFirst * i + j) + lane;
       key[i][j] = 0;
-      if (all_at_once ? i < kAllKeys / kFirst && e < a.parts * k : p < a.parts && j < k)
-        key[i][j] = a.keys[all_at_once ? u0 * k + e : (u0 + p) * k + j];
+      if constexpr (all_at_once) {
+        const int e = 64 * (kFirst * i + j) + lane;
+        if (i < kAllKeys / kFirst && e < a.parts * k) key[i][j] = a.keys[u0 * k + e];
+      } else {
+        if (p < a.parts && j < k) key[i][j] = a.keys[(u0 + p) * k + j];
+      }
     }
   }
   const bool inside = tok >= 0 && tok < a.n;
@@ -449,7 +459,6 @@ __global__ __launch_bounds__(64) void k_logprob_join(LogprobArgs a) {
   if (k == 0) return;
 
   const int lists = (a.parts + 63) / 64;
-  const bool by_lane = !all_at_once && a.parts >= 64;
   uint64_t best = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -457,16 +466,13 @@ __global__ __launch_bounds__(64) void k_logprob_join(LogprobArgs a) {
     for (int j = 0; j < kFirst; ++j)
       if (j == 0 || all_at_once) best = key[i][j] > best ? key[i][j] : best;
   const uint64_t top = wave_max_u64(best);
-  auto reached = [&](uint64_t at) {
-    int c = __popcll(__ballot((by_lane ? best : key[0][0]) >= at));
-    if (!by_lane) {
+  auto reached = [&](uint64_t at) -> int {
+    if constexpr (by_lane) return __popcll(__ballot(best >= at));
+    int c = 0;
 #pragma unroll
-      for (int j = 1; j < kFirst; ++j) c += __popcll(__ballot(key[0][j] >= at));
-    }
-    if (all_at_once) {
+    for (int i = 0; i < (all_at_once ? kAllKeys / kFirst : 1); ++i)
 #pragma unroll
-      for (int j = 0; j < kFirst; ++j) c += __popcll(__ballot(key[1][j] >= at));
-    }
+      for (int j = 0; j < kFirst; ++j) c += __popcll(__ballot(key[i][j] >= at));
     return c;
   };
   uint64_t T = k == 1 ? top : 1;   // 1: every key
@@ -531,7 +537,12 @@ hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_logprob_part<4>), grid, dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((k_logprob_part<kLogprobChunk / 256>), grid, dim3(256), 0, s, a);
-  hipLaunchKernelGGL(k_logprob_join, dim3(a.M), dim3(64), (join_room(a.parts, a.k) + 4) * sizeof(uint64_t), s, a);
+  const size_t lds = (join_room(a.parts, a.k) + 4) * sizeof(uint64_t);
+  switch (join_keys(a.parts, a.k)) {
+    case kAll: hipLaunchKernelGGL((k_logprob_join<kAll>), dim3(a.M), dim3(64), lds, s, a); break;
+    case kLanes: hipLaunchKernelGGL((k_logprob_join<kLanes>), dim3(a.M), dim3(64), lds, s, a); break;
+    case kFours: hipLaunchKernelGGL((k_logprob_join<kFours>), dim3(a.M), dim3(64), lds, s, a); break;
+  }
   return hipGetLastError();
 }
 

@@ -27,11 +27,11 @@
 // above T than the space holds, T is raised by bisection over the order of
 // fp32 first.
 //
-// Many rows are bound by HBM: 1000 rows of 151936 logits, 608 MB, take 113 us
-// (5.4 TB/s; a large copy reaches 5.2).  64 rows (39 MB, in the Infinity Cache)
-// take 13 us with k = 0 and 17.7 with k = 20: the latency of one chunk a wave,
-// of which the exponentials are a third and the top k a third; one row 7.1 and
-// 9.5 us, two launches of little more than an empty one each.
+// Many rows are bound by HBM: 1000 rows of 151936 logits, 608 MB, take 114 us
+// (5.3 TB/s; a large copy reaches 5.2).  64 rows (39 MB, in the Infinity Cache)
+// take 11.9 us a call with k = 0 and 17.8 with k = 20, the latency of one chunk a
+// wave and of the join, and the top k; one row 8.4 us with k = 0 and 9.5 with
+// k = 5, two launches of 5 us each.
 #include <algorithm>
 
 #include "logprobs_args.h"

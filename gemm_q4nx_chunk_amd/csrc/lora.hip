@@ -237,7 +237,7 @@ __global__ __launch_bounds__(1024) void k_lora_route(LoraArgs a) {
 //
 // Measured (4096 rows, 14336 columns, rank 64; 64 rows of 40 adapters, 9728
 // columns): operands straight from memory 75 and 14 us; 64 bytes of a row at a
-// time through LDS 51 and 12.
+// time through LDS 51 and 12; as here 37 and 10.
 inline size_t lora_shrink_lds(int blocks, int sub) {
   return (size_t)kLoraShrinkWaves * blocks * 2048 + 16 * sub * sizeof(int32_t);
 }
@@ -386,7 +386,7 @@ __device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
 // through LDS of the wave's own, so that the base and y move eight lanes to a
 // row, a whole 128-byte line (group c of 4 outputs of row r at slot c ^ (r % 8);
 // 16 rows to 16 lanes instead, as the matrix cores leave them, 47 and 15 us at
-// 4096 x 4096 rank 64 and 1000 x 4096 rank 16).  B and the base of a wave's next
+// 4096 x 4096 rank 64 and 1000 x 4096 rank 16; as here 36 and 9).  B and the base of a wave's next
 // outputs are loaded before the present ones are computed, the first before u
 // is summed.  KS: 32-rank steps of the largest rank.
 template <int KS, int SUB>

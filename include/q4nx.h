@@ -561,11 +561,11 @@ enum { Q4NX_LORA_BATCH_MAX_JOBS = 8, Q4NX_LORA_MAX_M = 4096 };
  *   M    1..Q4NX_LORA_MAX_M
  *   ws   DEVICE workspace of q4nx_lora_ws(L, M) bytes, 256-byte aligned.  Nothing
  *        in it needs initialising; calls that share it must not overlap.
- * Rows of one adapter are found on the device and taken together, up to 64 (16
- * for M <= 64) at a time, so an adapter is read once per tile of rows.  Sums
- * are fp32 in an order fixed by the call's sizes: a row's bits depend neither on
- * the other rows nor on its place.  B_e (A_e x) keeps fp32's precision (A_e x
- * enters the second product as three bf16 parts that hold its 24 bits).
+ * Rows of one adapter are found on the device and taken together, in tiles of up
+ * to 16 or 64 rows, so an adapter is read once per tile.  Sums are fp32 in an
+ * order fixed by the call's sizes: a row's bits depend neither on the other rows
+ * nor on its place.  B_e (A_e x) keeps fp32's precision (A_e x enters the second
+ * product as three bf16 parts that hold its 24 bits).
  * An id below -1 or past the last adapter is never dereferenced: its row is
  * taken as one without an adapter and bit 0 of the uint32 at ws[0] is set
  * (cleared at the start of each call; read it after synchronising).
@@ -600,8 +600,9 @@ size_t q4nx_lora_batched_ws(const q4nx_lora_job* jobs, int n_jobs, int M);
  *   x      DEVICE bf16 [M][D], rounded once to nearest even
  *   M      1..1048576;  D  1..32768, any;  eps >= 0
  * fp32 arrays 4-byte, bf16 arrays 2-byte aligned.  x and r_out must lie apart
- * from each other and from every input, but for r_out in place (E_ARG).  Sums are fp32 in a fixed order;
- * a row whose squares overflow fp32 gives x = 0 (or NaN where s is not finite).
+ * from each other and from every input, but for r_out in place (E_ARG).  Sums
+ * are fp32 in a fixed order; a row whose squares overflow fp32 gives x = 0 (or
+ * NaN where s is not finite).
  */
 int q4nx_add_rmsnorm(const float* y, const float* r, const uint16_t* w, int M, int D, float eps,
                      float* r_out, uint16_t* x, void* stream);

@@ -1382,15 +1382,17 @@ struct LoraShape {
   size_t hdr, sorted, tiles, u[q4nx::kLoraMaxJobs], total;
 };
 
-// Rows of one set of launches: the kernels address x and y by 31-bit offsets,
-// so longer calls are cut, each piece after the other with the same workspace.
+// Most rows of one set of launches: the kernels address x and y by 31-bit
+// offsets, so longer calls are cut, each piece after the other with the same
+// workspace.
 int lora_rows(const q4nx_lora* const* L, int n, int M) {
   int64_t row_bytes = (int64_t)L[0]->cols * 2;
   for (int i = 0; i < n; ++i) row_bytes = std::max(row_bytes, (int64_t)L[i]->rows * 4);
   return (int)std::min((int64_t)M, ((int64_t)1 << 31) / row_bytes);
 }
 
-void lora_shape(const q4nx_lora* const* L, int n, int M, LoraShape& sh) {
+// room: the rows that the workspace is laid out for, at least M.
+void lora_shape(const q4nx_lora* const* L, int n, int M, int room, LoraShape& sh) {
   memset(&sh, 0, sizeof sh);
   q4nx::LoraArgs& a = sh.a;
   a.n_jobs = n;
@@ -1435,14 +1437,14 @@ void lora_shape(const q4nx_lora* const* L, int n, int M, LoraShape& sh) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   size_t o = 256;
   sh.sorted = o;
-  o = up(o + (size_t)a.max_tiles * a.tile_rows * 4);
+  o = up(o + q4nx::lora_places(room, a.n_adapters) * 4);
   sh.tiles = o;
-  o = up(o + (size_t)a.max_tiles * sizeof(q4nx::LoraTile));
+  o = up(o + q4nx::lora_tiles(room, a.n_adapters) * sizeof(q4nx::LoraTile));
   for (int i = 0; i < n; ++i) {
     a.job[i].wg_begin = wg;
     wg += (L[i]->rows + a.n_range - 1) / a.n_range;
     sh.u[i] = o;
-    o = up(o + (size_t)a.split * M * L[i]->rank * 4);
+    o = up(o + q4nx::lora_u_rows(room) * L[i]->rank * 4);
   }
   sh.total = o;
 }
@@ -1490,15 +1492,18 @@ int run_lora(const q4nx_lora_job* jobs, int n, const uint16_t* x, const int32_t*
     L[i] = &j.lora;
   }
   LoraShape sh;
-  const int per = lora_rows(L, n, M);
-  lora_shape(L, n, per, sh);
+  // pieces of one shape, equal but for a last one that is a few rows shorter (and
+  // has more than kLoraWaveRows: a piece may have 512), so that a row's sums do not
+  // depend on its place
+  const int room = lora_rows(L, n, M), pieces = (M + room - 1) / room, per = (M + pieces - 1) / pieces;
+  lora_shape(L, n, per, room, sh);
   if (!ws || ws_bytes < sh.total)
     return fail(Q4NX_E_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", name, ws_bytes, sh.total);
   if (!aligned(ws, 256)) return fail(Q4NX_E_ALIGN, "%s: workspace not 256-byte aligned", name);
   uint8_t* w = static_cast<uint8_t*>(ws);
   for (int m0 = 0; m0 < M; m0 += per) {
-    if (m0) lora_shape(L, n, std::min(per, M - m0), sh);
     q4nx::LoraArgs& a = sh.a;
+    a.M = std::min(per, M - m0);
     a.more = m0 > 0;
     a.x = x + (size_t)m0 * a.cols;
     a.ids = ids + m0;
@@ -1534,7 +1539,8 @@ size_t q4nx_lora_batched_ws(const q4nx_lora_job* jobs, int n_jobs, int M) {
   const q4nx_lora* L[q4nx::kLoraMaxJobs];
   for (int i = 0; i < n_jobs; ++i) L[i] = &jobs[i].lora;
   LoraShape sh;
-  lora_shape(L, n_jobs, lora_rows(L, n_jobs, M), sh);
+  const int room = lora_rows(L, n_jobs, M);
+  lora_shape(L, n_jobs, room, room, sh);
   return sh.total;
 }
 

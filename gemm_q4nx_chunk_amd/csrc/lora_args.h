@@ -73,6 +73,17 @@ inline int lora_max_tiles(int M, int n_adapters, int tile_rows) {
   return (tiles + 7) / 8 * 8;   // eight at a time, one on each XCD
 }
 
+// Room for M rows or fewer, so that none of it shrinks as M grows: rows of u in
+// all its parts (above kLoraWaveRows a split of s > 1 leaves s * M / 64 workgroups
+// at most 256), places in the tiles, and tiles.
+inline size_t lora_u_rows(int M) { return M < 2048 ? (size_t)kLoraMaxSplit * M : 16384; }
+inline size_t lora_places(int M, int n_adapters) {
+  return (size_t)M + 64 * ((size_t)(M < n_adapters + 1 ? M : n_adapters + 1) + 7);
+}
+inline size_t lora_tiles(int M, int n_adapters) {
+  return (size_t)M / 16 + (M < n_adapters + 1 ? M : n_adapters + 1) + 7;
+}
+
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s);
 
 }  // namespace q4nx

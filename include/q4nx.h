@@ -574,7 +574,7 @@ enum { Q4NX_LORA_BATCH_MAX_JOBS = 8, Q4NX_LORA_MAX_M = 4096 };
  */
 int q4nx_lora_add(const q4nx_lora* L, const uint16_t* x, const int32_t* ids, int M, const float* base,
                   float* y, void* ws, size_t ws_bytes, void* stream);
-/* Workspace bytes of q4nx_lora_add (0 = bad descriptor or M). */
+/* Workspace bytes of q4nx_lora_add for M rows or fewer (0 = bad descriptor or M). */
 size_t q4nx_lora_ws(const q4nx_lora* L, int M);
 
 /*

@@ -161,3 +161,15 @@ def test_refusals_are_clean_under_asan_and_ubsan():
                        capture_output=True, text=True, timeout=600)
     out = r.stdout + r.stderr
     assert r.returncode == 0 and "Sanitizer" not in out and "runtime error" not in out, out[-4000:]
+
+
+@pytest.mark.parametrize("E", [1, 3, 40, 400])
+@pytest.mark.parametrize("rank", [8, 64, 256])
+@pytest.mark.parametrize("rows,cols", [(64, 256), (1 << 19, 256), (1 << 19, 4096), (2560, 9728), (4096, 14336), (64, 1 << 20)])
+def test_a_workspace_for_many_rows_holds_fewer(q, E, rank, rows, cols):
+    """A caller keeps one workspace for the largest batch, and a call past 2^31 bytes runs its pieces,
+    the last of them shorter, in the one it was given."""
+    L = q.Lora(E, rank, rows, cols, 4096, 4096, 2 * rank * cols, 2 * rank * rows, 1 << 60, 1 << 60, 4096, None)
+    sizes = [q.lora_ws(L, M) for M in range(1, 4097)]
+    assert sizes[0] > 0
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))

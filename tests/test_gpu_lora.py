@@ -278,3 +278,28 @@ def test_tiles_of_few_and_of_many_adapters(M, E, kind):
     c = Case("tiles", M, 256, 64, 8, E, _ids(kind, M, E, seed=M))
     c.check(c.run())
     c.check(c.run(in_place=True))
+
+
+@pytest.mark.parametrize("M", [1794, 1025])
+def test_uneven_pieces_stay_inside_the_workspace_and_agree(M):
+    """Calls cut at 2^31 bytes of y: nothing past the workspace is written, and a row has the same bits
+    in whichever piece it lies."""
+    K, N, R, E = 4096, 1 << 19, 64, 2
+    print(f"lora M={M} N={N}: y of {M * N * 4 / 2 ** 30:.1f} GiB", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    da = (torch.randn((E, R, K), device="cuda", generator=g) / 64).bfloat16()
+    db = torch.randn((E, N, R), device="cuda", generator=g).bfloat16() / 8
+    L = q().lora_table(E, R, N, K, da, db, dev_f32(np.ones(E)))
+    dx = torch.randn((1, K), device="cuda", generator=g).bfloat16().repeat(M, 1)
+    dids = dev_i32(np.arange(M) % E)
+    size = q().lora_ws(L, M)
+    ws = torch.full((size + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    y = torch.zeros((M, N), device="cuda")
+    q().lora_add(L, dx, dids, M, y, ws[:size])
+    torch.cuda.synchronize()
+    assert bool((ws[size:] == 0x5A).all())
+    assert float(y[0].abs().max()) > 0
+    for m0 in range(0, M, 200):
+        part = y[m0:m0 + 200].view(torch.int32)
+        for m in range(part.shape[0]):
+            assert torch.equal(part[m], y[(m0 + m) % E].view(torch.int32)), m0 + m

@@ -173,3 +173,11 @@ def test_a_workspace_for_many_rows_holds_fewer(q, E, rank, rows, cols):
     sizes = [q.lora_ws(L, M) for M in range(1, 4097)]
     assert sizes[0] > 0
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+@pytest.mark.parametrize("n", [1, 700, 5000, 50001, 151936, 262144, 262145, 1 << 20])
+@pytest.mark.parametrize("k", [0, 1, 32])
+def test_a_logprobs_workspace_for_many_rows_holds_fewer(q, n, k):
+    sizes = [q.token_logprobs_ws(n, M, min(k, n)) for M in [*range(1, 5000), 16383, 16384, 16385, 65535]]
+    assert sizes[0] > 0
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))

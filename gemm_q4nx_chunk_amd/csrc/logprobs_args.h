@@ -1,6 +1,8 @@
 // Device-side arguments of the log-probability kernels (one struct, passed by value).
 #pragma once
 
+#include <algorithm>
+
 #include "q4nx_dev.h"
 
 namespace q4nx {
@@ -39,13 +41,14 @@ inline int logprob_part_n(int n, int M) {
   return (chunks + parts - 1) / parts * kLogprobChunk;
 }
 
-// Workspace: the parts' stats, then their keys.
+// Workspace: the parts' stats, then their keys, laid out for the most parts that
+// M rows or fewer have (logprob_part_n), so that it does not shrink as M grows.
 struct LogprobWsLayout {
   size_t stats, keys, total;
 };
 inline LogprobWsLayout logprob_ws_layout(int n, int M, int k) {
-  const int pn = logprob_part_n(n, M);
-  const size_t units = (size_t)M * ((n + pn - 1) / pn);
+  const int most = std::min((n + 1023) / 1024, kLogprobMaxParts);
+  const size_t units = std::min((size_t)M * most, (size_t)std::max(M, 16384));
   LogprobWsLayout l;
   l.stats = 0;
   l.keys = units * 16;

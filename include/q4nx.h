@@ -628,8 +628,8 @@ int q4nx_add_rmsnorm(const float* y, const float* r, const uint16_t* w, int M, i
  *   entropy  DEVICE fp32 [M] or NULL
  *   k        0..32; top_ids DEVICE int32 [M][k] (NULL when 0), top_logp DEVICE
  *            fp32 [M][k] or NULL
- *   ws       DEVICE workspace of q4nx_token_logprobs_ws(n, M, k) bytes, 256-byte
- *            aligned.  Nothing in it needs initialising; calls that share it
+ *   ws       DEVICE workspace of q4nx_token_logprobs_ws(n, M, k) bytes (enough
+ *            for fewer rows too), 256-byte aligned.  Nothing in it needs initialising; calls that share it
  *            must not overlap.
  * E_ARG also when nothing is asked for.  The largest logit is set apart from
  * the sum, so that the log probability of a likely token, and the entropy of a

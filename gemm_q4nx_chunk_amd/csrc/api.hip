@@ -1606,6 +1606,14 @@ int q4nx_token_logprobs(const float* y, int n, int ldy, int M, const int32_t* to
   if (!aligned(y, 4) || !aligned(tokens, 4) || !aligned(logp, 4) || !aligned(entropy, 4) || !aligned(top_ids, 4) ||
       !aligned(top_logp, 4))
     return fail(Q4NX_E_ALIGN, "token_logprobs: every array must be 4-byte aligned");
+  const struct { const void* p; uint64_t bytes; } part[] = {   // the outputs first
+      {n_tok ? logp : nullptr, (uint64_t)M * n_tok * 4}, {entropy, (uint64_t)M * 4},
+      {k ? top_ids : nullptr, (uint64_t)M * k * 4},      {k ? top_logp : nullptr, (uint64_t)M * k * 4},
+      {y, ((uint64_t)(M - 1) * ldy + n) * 4},            {n_tok ? tokens : nullptr, (uint64_t)M * n_tok * 4}};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 6; ++j)
+      if (part[i].p && part[j].p && overlap(part[i].p, part[i].bytes, part[j].p, part[j].bytes))
+        return fail(Q4NX_E_ARG, "token_logprobs: an output overlaps another array");
   const q4nx::LogprobWsLayout lay = q4nx::logprob_ws_layout(n, M, k);
   if (!ws || ws_bytes < lay.total)
     return fail(Q4NX_E_WORKSPACE, "token_logprobs: workspace of %zu bytes, %zu needed", ws_bytes, lay.total);

@@ -631,9 +631,10 @@ int q4nx_add_rmsnorm(const float* y, const float* r, const uint16_t* w, int M, i
  *   ws       DEVICE workspace of q4nx_token_logprobs_ws(n, M, k) bytes (enough
  *            for fewer rows too), 256-byte aligned.  Nothing in it needs initialising; calls that share it
  *            must not overlap.
- * E_ARG also when nothing is asked for.  The largest logit is set apart from
- * the sum, so that the log probability of a likely token, and the entropy of a
- * sharp distribution, keep their digits.
+ * E_ARG also when nothing is asked for, or an output overlaps another or y or
+ * tokens.  The largest logit is set apart from the sum, so that the log
+ * probability of a likely token, and the entropy of a sharp distribution, keep
+ * their digits.
  */
 size_t q4nx_token_logprobs_ws(int n, int M, int k);
 int q4nx_token_logprobs(const float* y, int n, int ldy, int M, const int32_t* tokens, int n_tok,

@@ -181,3 +181,20 @@ def test_a_logprobs_workspace_for_many_rows_holds_fewer(q, n, k):
     sizes = [q.token_logprobs_ws(n, M, min(k, n)) for M in [*range(1, 5000), 16383, 16384, 16385, 65535]]
     assert sizes[0] > 0
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+def test_logprobs_outputs_lie_apart(q):
+    """An output over the logits, the given tokens or another output is refused."""
+    at = dict(y=0x1000000, tokens=0x2000000, logp=0x3000000, entropy=0x4000000, top_ids=0x5000000, top_logp=0x6000000)
+    M, n, T, k = 4, 1000, 3, 5
+    need = q.token_logprobs_ws(n, M, k)
+    size = dict(y=((M - 1) * 1024 + n) * 4, tokens=M * T * 4, logp=M * T * 4, entropy=M * 4, top_ids=M * k * 4,
+                top_logp=M * k * 4)
+    for out in ("logp", "entropy", "top_ids", "top_logp"):
+        for other in at:
+            if other == out:
+                continue
+            for place in (at[other] + size[other] - 4, at[other] - size[out] + 4):
+                args = dict(at, **{out: place})
+                _expect(q, q.E_ARG, q.token_logprobs, n=n, M=M, ws=WS, n_tok=T, k=k, ldy=1024, stream=0, ws_bytes=need,
+                        **args)

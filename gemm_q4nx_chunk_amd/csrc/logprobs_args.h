@@ -30,7 +30,7 @@ constexpr int kLogprobChunk = 2048;    // logits that a wave holds in registers 
 
 // Logits of a part.  Up to 2048 waves of 1024 logits: those, in one go (16 rows
 // of 50001: 10.8 us, 12.8 with 2048 a wave).  Else whole chunks, as many as leave
-// about 16384 waves (1000 rows of 151936: 113 us; with 8192 waves 117, with 4096
+// about 16384 waves (1000 rows of 151936: 114 us; with 8192 waves 117, with 4096
 // 118), for a wave's first chunk costs the most.
 inline int logprob_part_n(int n, int M) {
   if ((int64_t)M * ((n + 1023) / 1024) <= 2048 && n <= kLogprobMaxParts * 1024) return 1024;

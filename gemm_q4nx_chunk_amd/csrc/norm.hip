@@ -12,6 +12,15 @@
 // in order); each x is rounded once, from fp32, which is what the projections
 // take.
 //
+// A row whose squares leave fp32 (their mean with eps overflows, or lies so low
+// that a square below 2^-126 may count) is summed again from the registers,
+// scaled by a power of two that puts the larger of its maximum and sqrt(eps)
+// just below 1:
+//   x = t / sqrt(mean(t^2) + 4^-e eps) * w,  t = 2^-e s.
+// A square below 2^-126 counts for at most 2^-30 of a mean of 2^-96 and up, so
+// that other rows, with any usual eps all that do not overflow, need no second
+// sum; they are scaled by 1, which changes no bit.
+//
 // Bound by HBM for many rows and by two memory latencies (load, reduce, store)
 // for few.
 #include "q4nx_dev.h"
@@ -28,6 +37,37 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   const f32x2 v = {a, b};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+constexpr float kLowMean = 0x1p-96f;
+
+// Sum (or maximum) of a value over the row's threads, in every one of them.
+template <int WAVES, bool MAX>
+__device__ __forceinline__ float over_row(float v, float* part, int wave, int lane) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    const float o = __shfl_xor(v, off);
+    v = MAX ? fmaxf(v, o) : v + o;
+  }
+  if constexpr (WAVES > 1) {
+    if (lane == 0) part[wave] = v;
+    __syncthreads();
+    v = 0.f;   // maxima are of magnitudes
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) v = MAX ? fmaxf(v, part[i]) : v + part[i];
+  }
+  return v;
+}
+
+// Sum of the squares of pre * s, pre a power of two.
+template <int NV>
+__device__ __forceinline__ float squares(const f32x4 (&s)[NV], float pre) {
+  float sum = 0.f;
+#pragma unroll
+  for (int g = 0; g < NV; ++g)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = fmaf(pre * s[g][i], pre * s[g][i], sum);
+  return sum;
 }
 
 }  // namespace
@@ -47,7 +87,6 @@ __global__ __launch_bounds__(WAVES ? 64 * WAVES : 256) void k_add_rmsnorm(
   const size_t row = (size_t)m * D;
   f32x4 s[NV];
   u32x2 wv[NV];
-  float sum = 0.f;
 #pragma unroll
   for (int g = 0; g < NV; ++g) {
     const int c = 4 * (g * kThreads + t);
@@ -66,27 +105,32 @@ __global__ __launch_bounds__(WAVES ? 64 * WAVES : 256) void k_add_rmsnorm(
         }
     }
   }
+  __shared__ float part[WAVES > 1 ? WAVES : 1];
+  float mean = over_row<WAVES, false>(squares(s, 1.f), part, wave, lane) / (float)D + eps;
+  float pre = 1.f;   // 2^-e
+  if (!(mean >= kLowMean && mean <= __FLT_MAX__)) {   // the same in all of the row's threads
+    if constexpr (WAVES > 1) __syncthreads();         // part is read above
+    float top = 0.f;
 #pragma unroll
-  for (int g = 0; g < NV; ++g)
+    for (int g = 0; g < NV; ++g)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum = fmaf(s[g][i], s[g][i], sum);
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-  if constexpr (WAVES > 1) {
-    __shared__ float part[WAVES];
-    if (lane == 0) part[wave] = sum;
-    __syncthreads();
-    sum = 0.f;
-#pragma unroll
-    for (int v = 0; v < WAVES; ++v) sum += part[v];
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(s[g][i]));
+    top = over_row<WAVES, true>(top, part, wave, lane);
+    // rows of an infinity, of a NaN (the mean is one) and of zeros stay with what they have
+    if (top > 0.f && top <= __FLT_MAX__ && mean == mean) {
+      // 2^126 at most, which takes 2^-149 to 2^-23
+      pre = ldexpf(1.f, -max(__builtin_amdgcn_frexp_expf(fmaxf(top, sqrtf(eps))), -126));
+      if constexpr (WAVES > 1) __syncthreads();
+      mean = over_row<WAVES, false>(squares(s, pre), part, wave, lane) / (float)D + eps * pre * pre;
+    }
   }
-  const float inv = 1.f / sqrtf(sum / (float)D + eps);
+  const float inv = 1.f / sqrtf(mean);
 #pragma unroll
   for (int g = 0; g < NV; ++g) {
     const int c = 4 * (g * kThreads + t);
     const f32x4 v = s[g];
-    const u32x2 o = {bf16_pair(v[0] * inv * bf16lo(wv[g].x), v[1] * inv * bf16hi(wv[g].x)),
-                     bf16_pair(v[2] * inv * bf16lo(wv[g].y), v[3] * inv * bf16hi(wv[g].y))};
+    const u32x2 o = {bf16_pair(v[0] * pre * inv * bf16lo(wv[g].x), v[1] * pre * inv * bf16hi(wv[g].x)),
+                     bf16_pair(v[2] * pre * inv * bf16lo(wv[g].y), v[3] * pre * inv * bf16hi(wv[g].y))};
     if (c + 3 < D) {
       if (r_out) *reinterpret_cast<f32x4u*>(r_out + row + c) = v;
       *reinterpret_cast<u32x2u*>(x + row + c) = o;

@@ -601,8 +601,10 @@ size_t q4nx_lora_batched_ws(const q4nx_lora_job* jobs, int n_jobs, int M);
  *   M      1..1048576;  D  1..32768, any;  eps >= 0
  * fp32 arrays 4-byte, bf16 arrays 2-byte aligned.  x and r_out must lie apart
  * from each other and from every input, but for r_out in place (E_ARG).  Sums
- * are fp32 in a fixed order; a row whose squares overflow fp32 gives x = 0 (or
- * NaN where s is not finite).
+ * are fp32 in a fixed order; a row whose squares overflow fp32, or vanish in it
+ * beside eps, is scaled by a power of two first, so that every finite row has
+ * its x (NaN for a row of zeros without eps).  An infinity in s gives NaN, and
+ * 0 in the rest of its row; a NaN in s gives NaN in all of it.
  */
 int q4nx_add_rmsnorm(const float* y, const float* r, const uint16_t* w, int M, int D, float eps,
                      float* r_out, uint16_t* x, void* stream);

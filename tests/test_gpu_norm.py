@@ -136,3 +136,42 @@ def test_many_rows():
     x = torch.empty((M, D), dtype=torch.int16, device="cuda")
     q().add_rmsnorm(dev_f32(r), dev_bf16(w), M, D, EPS, x, y=dev_f32(y))
     _check_x(host(x), y + r, w, EPS)
+
+
+@pytest.mark.parametrize("D", [4, 100, 256, 300, 700, 1025, 2560, 4097, 9000, 20000])
+@pytest.mark.parametrize("place", ["apart", "in place", "norm only"])
+def test_rows_whose_squares_leave_fp32(D, place):
+    """Finite rows whose squares overflow or vanish in fp32 keep their x, beside rows that do neither, an
+    infinity and a NaN.  Without eps, with one that counts beside the smallest squares, and with the usual
+    one.  The bound is the file's: the rows are scaled by powers of two, and an element that this takes
+    below 2^-126 has |x| < 2^-134 here (|w| < 4, and x is at most sqrt(D) of s over the row's largest)."""
+    scales = [1.0, 2e19, 1e25, 3e37, 1e-20, 1e-25, 1e-37, 1e-40, 1.0, 1.0]
+    M = len(scales)
+    _, r, w = _inputs(M, D, "range")
+    r = (r / np.abs(r).max(axis=1, keepdims=True) * np.array(scales)[:, None]).astype(np.float32)
+    r[2, 1] = 1e-25                               # far below its row
+    r[8, 0], r[9, 2] = np.inf, np.nan
+    y = np.zeros_like(r) if place == "norm only" else (r / 4).astype(np.float32)
+    s = y + r
+    for eps in (0.0, 1e-44, 1e-30, EPS):
+        dr, x = dev_f32(r), torch.full((M, D), -1, dtype=torch.int16, device="cuda")
+        q().add_rmsnorm(dr, dev_bf16(w), M, D, eps, x, y=None if place == "norm only" else dev_f32(y),
+                        r_out=dr if place == "in place" else None)
+        got = host(x)
+        _check_x(got[:8], s[:8], w, float(np.float32(eps)))
+        if place == "in place":
+            np.testing.assert_array_equal(host(dr), s)
+        v = synth.bf16_to_f32(got.view(np.uint16))
+        assert np.isnan(v[8, 0]) and (v[8, 1:] == 0).all() and np.isnan(v[9]).all()
+
+
+@pytest.mark.parametrize("D", [64, 600, 4096])
+def test_rows_of_zeros_with_any_eps(D):
+    """Zeros over the root of eps are zeros, however small eps is; the row beside them keeps its values."""
+    r = np.zeros((3, D), np.float32)
+    r[1] = np.linspace(-1e-24, 1e-24, D, dtype=np.float32)
+    w = synth.bf16_bits(np.ones(D))
+    for eps in (1e-6, 1e-30, 1e-38, 1e-45):
+        x = torch.full((3, D), -1, dtype=torch.int16, device="cuda")
+        q().add_rmsnorm(dev_f32(r), dev_bf16(w), 3, D, eps, x)
+        _check_x(host(x), r, w, float(np.float32(eps)))

@@ -326,6 +326,8 @@ __global__ __launch_bounds__(256) void k_logprob_part(LogprobArgs a) {
     if (cm == neg_inf()) continue;   // nothing left in this chunk
     if (a.k > 0 && cm > st.T) take_chunk<NQ>(v, lm, cm, c0 + 4 * lane, row, a.k, lane, g, st);
     // exp(-200) is 0 in fp32: the clamp changes no sum and keeps -inf and NaN out of e * d
+    float r_c = 0.f, t_c = 0.f;   // this chunk's rest and t: a sum of its own, so that no value passes more
+                                  // additions than a chunk has values in a lane and a part has chunks
     if (cm >= m) {
       if (cm > m && m != neg_inf()) {   // the old maximum joins the rest
         const float d = fmaxf(m - cm, -200.f), f = __builtin_amdgcn_exp2f(d * kLog2e);
@@ -343,11 +345,11 @@ __global__ __launch_bounds__(256) void k_logprob_part(LogprobArgs a) {
           same += __popcll(__ballot(is));
           const float d = fmaxf(v[q][c] - m, -200.f);
           const float e = is ? 0.f : __builtin_amdgcn_exp2f(d * kLog2e);
-          rest += e;
-          t = fmaf(e, d, t);
+          r_c += e;
+          t_c = fmaf(e, d, t_c);
           if (c == 3) __builtin_amdgcn_sched_barrier(0);
         }
-      rest += lane == 0 ? (float)same : 0.f;
+      r_c += lane == 0 ? (float)same : 0.f;
     } else {
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
@@ -355,11 +357,13 @@ __global__ __launch_bounds__(256) void k_logprob_part(LogprobArgs a) {
         for (int c = 0; c < 4; ++c) {
           const float d = fmaxf(v[q][c] - m, -200.f);
           const float e = __builtin_amdgcn_exp2f(d * kLog2e);
-          rest += e;
-          t = fmaf(e, d, t);
+          r_c += e;
+          t_c = fmaf(e, d, t_c);
           if (c == 3) __builtin_amdgcn_sched_barrier(0);
         }
     }
+    rest += r_c;
+    t += t_c;
   }
   rest = wave_sum(rest);
   t = wave_sum(t);

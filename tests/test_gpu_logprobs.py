@@ -264,3 +264,47 @@ def test_waves_that_take_many_chunks(k):
     _check(got, big, n, tokens, k, rows=range(8))
     for name in ("logp", "entropy", "top_ids", "top_logp"):
         np.testing.assert_array_equal(got[name].reshape(M // 8, 8, -1), np.broadcast_to(got[name][:8].reshape(1, 8, -1), (M // 8, 8, got[name][0].size)))
+
+
+def _run_many(rows, M, n, tokens, k):
+    """A call over M rows that repeat the given ones (laid out on the device), with stale outputs; and the
+    least chunks of 2048 logits that some wave took, from the records of parts that a call without
+    alternatives leaves in its workspace: 16 bytes a part, the last 4 of them 0."""
+    y = dev_f32(rows).repeat(M // len(rows), 1)
+    print(f"logprobs M={M} n={n} k={k}", flush=True)
+    out = {"logp": torch.full((M, 1), -7.0, device="cuda"), "entropy": torch.full((M,), -7.0, device="cuda"),
+           "top_ids": torch.full((M, k), -7, dtype=torch.int32, device="cuda"), "top_logp": torch.full((M, k), -7.0, device="cuda")}
+    dt = torch.from_numpy(tokens).cuda().repeat(M // len(rows), 1)
+    size = q().token_logprobs_ws(n, M, k)
+    ws = torch.full((size + 4096,), 0xAB, dtype=torch.uint8, device="cuda")
+    q().token_logprobs(y, n, M, ws, tokens=dt, n_tok=1, k=k, ws_bytes=size, **out)
+    assert bool((ws[size:] == 0xAB).all())
+    got = {name: v.reshape(M // len(rows), len(rows), -1) for name, v in out.items()}
+    for name, v in got.items():     # the same row, the same bits, wherever it lies
+        v = v.view(torch.int32)
+        assert bool((v == v[:1]).all()), name
+    got = {name: host(v[0]) for name, v in got.items()}
+    got["entropy"] = got["entropy"][:, 0]
+    ws.fill_(0xAB)
+    q().token_logprobs(y, n, M, ws, entropy=out["entropy"], ws_bytes=q().token_logprobs_ws(n, M, 0))
+    parts = int((host(ws)[:size // 16 * 16].view(np.int32).reshape(-1, 4)[:, 3] == 0).sum()) // M
+    return got, math.ceil(n / parts / 2048)
+
+
+@pytest.mark.parametrize("n,M", [(65536, 16384), (151936, 16384), (151936, 4096)])
+def test_level_rows_in_a_large_batch(n, M):
+    """Rows whose many logits are alike, so that every addition of a long sum errs the same way, and rows
+    whose maximum rises slowly all along, in batches so large that a wave takes many chunks: the error's
+    bound does not grow with the batch."""
+    g = np.random.default_rng(n)
+    y = np.empty((8, n), np.float32)
+    for i, d in enumerate((-0.76, -2.8, -2.05, -0.58, -5.3)):
+        y[i] = d
+        y[i, 7 * i] = 0.0
+    y[5] = np.arange(n, dtype=np.float32) * np.float32(1e-4)
+    y[6] = np.arange(n, dtype=np.float32) * np.float32(1e-6)
+    y[7] = -1.37 + 1e-3 * g.standard_normal(n)
+    tokens = np.full((8, 1), n - 3, np.int32)
+    got, chunks = _run_many(y, M, n, tokens, 2)
+    assert chunks >= 4
+    _check(got, y, n, tokens, 2)

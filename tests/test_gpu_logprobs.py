@@ -308,3 +308,34 @@ def test_level_rows_in_a_large_batch(n, M):
     got, chunks = _run_many(y, M, n, tokens, 2)
     assert chunks >= 4
     _check(got, y, n, tokens, 2)
+
+
+@pytest.mark.parametrize("k", [1, 20, 32])
+@pytest.mark.parametrize("n,M", [(20001, 8192), (30001, 16384)])
+def test_waves_that_take_five_chunks_and_more(n, M, k):
+    """A threshold carried over many chunks, a gathering space that fills up and is cut down again and
+    again, a maximum that rises many times, and a first bound only after chunks that are masked whole."""
+    g = np.random.default_rng(n + k)
+    y = (2 * g.standard_normal((16, n))).astype(np.float32)
+    y[1].sort()
+    y[2] = np.sort(y[2])[::-1]
+    y[3] = 1.25
+    y[4, :9000] = -np.inf
+    y[5, ::2] = np.arange(0, n, 2) / 1000
+    y[6] = np.floor(np.arange(n) / 300)
+    y[7, :] = np.finfo(np.float32).min
+    y[7, n - 5:] = 3
+    y[8] = np.round(2 * y[8]) / 2                        # ties everywhere
+    y[9] = y[9] / 4 + np.arange(n) / 4000                # more above the threshold in every chunk
+    y[10, :n - 3000] = np.nan
+    y[11] = np.where(g.random(n) < 0.999, -np.inf, y[11])   # fewer than k a chunk, for several chunks
+    y[12] = np.repeat(np.arange(n // 100 + 1), 100)[:n] % 37
+    y[13, :] = -np.inf
+    y[13, n - 7] = y[13, 5] = -4.0
+    y[14, 2048 * 3:] += 60                               # one rise, late
+    y[15, ::1024] = np.inf
+    tokens = g.integers(0, n, (16, 1)).astype(np.int32)
+    tokens[:3, 0] = n - 1
+    got, chunks = _run_many(y, M, n, tokens, k)
+    assert chunks >= 5
+    _check(got, y, n, tokens, k)

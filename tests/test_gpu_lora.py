@@ -303,3 +303,175 @@ def test_uneven_pieces_stay_inside_the_workspace_and_agree(M):
         part = y[m0:m0 + 200].view(torch.int32)
         for m in range(part.shape[0]):
             assert torch.equal(part[m], y[(m0 + m) % E].view(torch.int32)), m0 + m
+
+
+class Many(Case):
+    """A case of many rows: the reference of a whole adapter's rows at once (the same sums as
+    oracle.lora_ref, which forms them row by row)."""
+
+    def ref(self):
+        x = synth.bf16_to_f32(self.x).astype(np.float64)
+        y, mag = self.base.astype(np.float64), np.zeros(self.base.shape)
+        for e in np.unique(self.ids[(self.ids >= 0) & (self.ids < self.E)]):
+            mine = self.ids == e
+            r = self.R if self.ranks is None else min(max(int(self.ranks[e]), 0), self.R)
+            a, b = self.A[e, :r].astype(np.float64), self.B[e, :, :r].astype(np.float64)
+            s = float(self.scale[e])
+            y[mine] += s * (x[mine] @ a.T @ b.T)
+            mag[mine] = abs(s) * (np.abs(x[mine]) @ np.abs(a).T @ np.abs(b).T)
+        return y, mag
+
+    def tiles(self, ws):
+        """(adapter, rows) of each tile that the last call made, from its workspace: the tiles follow the
+        header and the places of the rows.  Records past the tiles keep the workspace's stale bytes."""
+        groups = min(self.M, self.E + 1)
+        at = (256 + 4 * (self.M + 64 * (groups + 7)) + 255) // 256 * 256
+        rec = host(ws)[at:at + 8 * (self.M // 16 + groups + 7)].view(np.int32).reshape(-1, 2)
+        rec = rec[(rec[:, 1] > 0) & (rec[:, 0] >= -1)]
+        assert rec[:, 1].sum() == self.M
+        want = np.where((self.ids >= 0) & (self.ids < self.E), self.ids, -1)
+        for e in np.unique(want):
+            assert rec[rec[:, 0] == e, 1].sum() == (want == e).sum()
+        return rec
+
+    def run_tiles(self, in_place=False):
+        """run(), and the most rows of a tile; nothing past the workspace may change."""
+        n = q().lora_ws(self.table, self.M)
+        ws = torch.full((n + 4096,), 0xAB, dtype=torch.uint8, device="cuda")
+        y = self.run(in_place, ws)
+        assert (host(ws[n:]) == 0xAB).all()
+        return y, int(self.tiles(ws)[:, 1].max())
+
+
+def test_the_reference_of_many_rows():
+    c = Many("many", 40, 256, 64, 16, 3, _ids("some", 40, 3), ranks=[16, 0, 5])
+    for a, b in zip(c.ref(), Case.ref(c)):
+        np.testing.assert_allclose(a, b, rtol=1e-12, atol=1e-13)
+
+
+@pytest.mark.parametrize("M,K,E,kind,R", [
+    (2049, 256, 3, "random", 8), (2080, 256, 3, "random", 16), (3000, 256, 5, "some", 32), (4096, 256, 1, "one", 64),
+    (4095, 256, 7, "runs", 128), (2100, 512, 4, "random", 200), (2500, 256, 6, "random", 256), (513, 9728, 2, "random", 64),
+    (700, 9728, 3, "runs", 16), (1100, 9728, 4, "some", 72)])
+def test_tiles_of_64_rows(M, K, E, kind, R):
+    """Enough rows an adapter that tiles hold up to 64: every rank variant, pieces of 16 that are full, in
+    part and not at all."""
+    c = Many("tile64", M, K, 160, R, E, _ids(kind, M, E))
+    y, rows = c.run_tiles()
+    assert 48 < rows <= 64
+    c.check(y)
+    z, _ = c.run_tiles(in_place=True)
+    np.testing.assert_array_equal(y.view(np.int32), z.view(np.int32))
+    assert c.flag == 0
+
+
+@pytest.mark.parametrize("R", [72, 256])
+def test_tiles_of_64_rows_with_ranks_of_each_adapter(R):
+    M, E = 2600, 12
+    ranks = [0, 1, 7, 8, 9, 31, 33, 63, 64, 65, 71, R]
+    c = Many("tile64 mixed", M, 256, 96, R, E, _ids("some", M, E), ranks, pad=24, garbage=True)
+    y, rows = c.run_tiles()
+    assert 48 < rows <= 64
+    c.check(y)
+
+
+def test_tiles_of_64_rows_ids_outside():
+    M, E = 2200, 4
+    ids = _ids("random", M, E)
+    ids[[0, 3, 2199]] = [4, -2, -2 ** 31]
+    ids[1000:1070] = 2 ** 31 - 1
+    c = Many("tile64 outside", M, 256, 64, 8, E, ids)
+    y, rows = c.run_tiles()
+    assert rows == 64 and c.flag == 1
+    c.check(y)
+
+
+@pytest.mark.parametrize("M,R", [(2300, 32), (4096, 256)])
+def test_tiles_of_64_rows_a_rows_bits_depend_on_its_own_inputs_only(M, R):
+    c = Many("tile64 bits", M, 256, 96, R, 6, _ids("random", M, 6))
+    y0, rows = c.run_tiles()
+    assert 48 < rows <= 64
+    c.check(y0)
+    np.testing.assert_array_equal(c.run().view(np.int32), y0.view(np.int32))
+    p = np.random.default_rng(3).permutation(M)
+    c.dx, c.dids, c.dbase = dev_bf16(c.x[p]), dev_i32(c.ids[p]), dev_f32(c.base[p])
+    np.testing.assert_array_equal(c.run().view(np.int32), y0[p].view(np.int32))
+    ids = (c.ids + 1) % 6
+    ids[7] = c.ids[7]
+    c.dx, c.dids, c.dbase = dev_bf16(c.x), dev_i32(ids), dev_f32(c.base)
+    np.testing.assert_array_equal(c.run()[7].view(np.int32), y0[7].view(np.int32))
+
+
+@pytest.mark.parametrize("ranks", [(16, 40, 128), (8, 256, 64)])
+def test_tiles_of_64_rows_batched(ranks):
+    M = 2300
+    ids = _ids("some", M, 5)
+    cs = [Many(f"tile64 qkv{i}", M, 256, n, r, 5, ids) for i, (n, r) in enumerate(zip((256, 64, 96), ranks))]
+    for c in cs[1:]:
+        c.x, c.dx = cs[0].x, cs[0].dx
+    ys = [torch.full((M, c.N), float("nan"), device="cuda") for c in cs]
+    jobs = q().lora_jobs([(c.table, c.dbase, y) for c, y in zip(cs, ys)])
+    n = q().lora_batched_ws(jobs, M)
+    ws = torch.full((n + 4096,), 0xAB, dtype=torch.uint8, device="cuda")
+    print(f"lora batched M={M}", flush=True)
+    q().lora_add_batched(jobs, cs[0].dx, cs[0].dids, M, ws)
+    assert 48 < int(cs[0].tiles(ws)[:, 1].max()) <= 64 and (host(ws[n:]) == 0xAB).all()
+    for c, y in zip(cs, ys):
+        c.check(host(y))
+
+
+def test_tiles_of_64_rows_captured_and_replayed():
+    M = 2300
+    c = Many("tile64 graph", M, 256, 128, 72, 4, _ids("random", M, 4))
+    eager, rows = c.run_tiles()
+    assert 48 < rows <= 64
+    c.check(eager)
+    ws = torch.full((q().lora_ws(c.table, M),), 0xAB, dtype=torch.uint8, device="cuda")
+    y = torch.empty((M, c.N), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q().lora_add(c.table, c.dx, c.dids, M, y, ws, base=c.dbase)
+    for i in range(3):
+        y.fill_(float("nan"))
+        ws.fill_(i)
+        graph.replay()
+        np.testing.assert_array_equal(host(y).view(np.int32), eager.view(np.int32))
+
+
+@pytest.mark.parametrize("M,E,kind", [(4096, 1500, "random"), (4096, 4096, "each"), (4096, 4096, "random"), (4095, 1023, "some"),
+                                      (4096, 1024, "each"), (1100, 4096, "random"), (65, 4096, "some"), (3000, 130, "runs")])
+def test_route_of_many_adapters(M, E, kind):
+    """The route at its most rows and adapters: every row in one tile of its adapter, once."""
+    c = Many("route", M, 256, 32, 8, E, _ids(kind, M, E))
+    y, _ = c.run_tiles()
+    c.check(y)
+    assert c.flag == 0
+
+
+@pytest.mark.parametrize("M,K,N", [(1100, 256, 1 << 19), (1100, 1 << 20, 32)])
+def test_the_border_of_pieces(M, K, N):
+    """Calls cut at 2^31 bytes of y, and of x: the rows on both sides of every border."""
+    R, E = 8, 2
+    print(f"lora M={M} K={K} N={N}: x of {M * K / 2 ** 29:.1f} GiB, y of {M * N / 2 ** 28:.1f} GiB", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    dx = torch.randn((M, K), device="cuda", generator=g, dtype=torch.bfloat16)
+    da = torch.randn((E, R, K), device="cuda", generator=g, dtype=torch.bfloat16) / K ** 0.5
+    db = torch.randn((E, N, R), device="cuda", generator=g, dtype=torch.bfloat16)
+    ids = _ids("random", M, E)
+    ids[[0, M - 1]] = [7, -1]
+    L = q().lora_table(E, R, N, K, da, db, dev_f32(np.array([1.0, 0.5])))
+    ws = torch.empty(q().lora_ws(L, M), dtype=torch.uint8, device="cuda")
+    y = torch.ones((M, N), device="cuda")
+    q().lora_add(L, dx, dev_i32(ids), M, y, ws)
+    assert int(host(ws[:4].view(torch.int32))[0]) == 1
+    at_most = (1 << 31) // max(2 * K, 4 * N)
+    pieces = -(-M // at_most)
+    per = -(-M // pieces)
+    assert pieces == 2
+    rows = sorted({r for b in range(0, M + 1, per) for r in range(b - 2, b + 3) if 0 <= r < M} | {M - 2, M - 1})
+    cols = np.arange(N) if N < 256 else np.r_[0:64, N // 2:N // 2 + 64, N - 64:N]
+    tc = torch.from_numpy(cols).cuda()
+    got = host(y[rows][:, tc])
+    want, mag = oracle.lora_ref(host(dx[rows].float()), host(da.float()), host(db[:, tc].float()), np.array([1.0, 0.5]),
+                                ids[rows], np.ones((len(rows), len(cols))))
+    assert (np.abs(got - want) <= 2.0 ** -23 * ((K + 3 * R + 80) * mag + 1 + np.abs(want))).all()

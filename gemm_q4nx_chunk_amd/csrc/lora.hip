@@ -363,20 +363,18 @@ __global__ __launch_bounds__(64 * kLoraShrinkWaves, SUB == 1 ? 4 : 2) void k_lor
 // expand
 // ---------------------------------------------------------------------------
 // The three bf16 parts of u: its sign and exponent with 8 bits of the mantissa
-// each (truncation leaves every remainder exact); infinities and NaNs whole in
-// the first.
+// each (truncation leaves every remainder exact).  Where u ends before its last
+// part, the last one that it has is halved into the rest, which is exact too: a
+// part of 0 would make NaN of an infinite weight of B, where u times it is
+// infinite.  Infinities and NaNs, whose remainder is NaN, become all three parts.
 __device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
-  const uint32_t b = __float_as_uint(v);
-  if ((b & 0x7F800000u) == 0x7F800000u) {
-    p[0] = v != v ? 0x7FC0u : b >> 16;
-    p[1] = p[2] = 0;
-    return;
-  }
-  p[0] = b >> 16;
-  const float r1 = v - __uint_as_float(b & 0xFFFF0000u);
-  const uint32_t b1 = __float_as_uint(r1);
-  p[1] = b1 >> 16;
-  p[2] = __float_as_uint(r1 - __uint_as_float(b1 & 0xFFFF0000u)) >> 16;
+  float p0 = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u), r = v - p0;
+  if (!(fabsf(r) > 0.f)) p0 = r = 0.5f * v;
+  float p1 = __uint_as_float(__float_as_uint(r) & 0xFFFF0000u), p2 = r - p1;
+  if (!(fabsf(p2) > 0.f)) p1 = p2 = 0.5f * r;
+  p[0] = __float_as_uint(p0) >> 16;
+  p[1] = __float_as_uint(p1) >> 16;
+  p[2] = __float_as_uint(p2) >> 16;
 }
 
 // Workgroup (t, g): tile t, outputs n0 .. n0 + n_range of one job.  u of the

@@ -475,3 +475,51 @@ def test_the_border_of_pieces(M, K, N):
     want, mag = oracle.lora_ref(host(dx[rows].float()), host(da.float()), host(db[:, tc].float()), np.array([1.0, 0.5]),
                                 ids[rows], np.ones((len(rows), len(cols))))
     assert (np.abs(got - want) <= 2.0 ** -23 * ((K + 3 * R + 80) * mag + 1 + np.abs(want))).all()
+
+
+@pytest.mark.parametrize("M,E,R", [(1, 1, 8), (7, 2, 16), (64, 3, 72), (100, 3, 40), (300, 2, 256), (2100, 3, 24), (2100, 3, 256)])
+def test_infinite_weights(M, E, R):
+    """Where a weight of B is infinite the output is what the formula gives: infinite of the product's sign,
+    NaN where infinities of both signs or 0 and an infinity meet, or where B holds NaN; the other outputs
+    keep their values.  At most ranks u is two activations' sum times a power of two, a few bits long, so
+    that its lower parts are 0."""
+    c = Many("inf weights", M, 256, 96, R, E, _ids("random", M, E))
+    g = np.random.default_rng(R)
+    short = g.random(R) < 0.7
+    short[0] = True
+    c.A[:, short] = 0.0
+    c.A[:, short, 0] = 1.0
+    c.A[:, :, 5] = 1.0
+    c.scale = (2.0 ** (np.arange(E) % 3 - 1)).astype(np.float32)
+    x = synth.bf16_to_f32(c.x)
+    x[g.random(M) < 0.5] = 1.0
+    if M > 3:
+        x[1] = 0.0
+        x[3, 5] = np.inf
+    c.x = (x.view(np.uint32) >> 16).astype(np.uint16)     # bf16 values as they are
+    b = c.B
+    b[:, 0, 0], b[:, 1, 0] = np.inf, -np.inf
+    b[:, 2, 0], b[:, 2, R - 1] = np.inf, -np.inf
+    b[:, 3, R - 1] = np.nan
+    b[0, 95, R // 2] = np.inf
+    c.dx = dev_bf16(c.x)
+    c.table = q().lora_table(E, R, 96, 256, dev_bf16(synth.bf16_bits(c.A)),
+                             dev_bf16((b.view(np.uint32) >> 16).astype(np.uint16)), dev_f32(c.scale))
+    want, mag = c.base.astype(np.float64), np.zeros(c.base.shape)
+    with np.errstate(invalid="ignore"):
+        for e in range(E):
+            mine = c.ids == e
+            a, s, v = c.A[e].astype(np.float64), float(c.scale[e]), x[mine].astype(np.float64)
+            u, u_mag = (v[:, None] * a).sum(-1), (np.abs(v)[:, None] * np.abs(a)).sum(-1)
+            for r in range(R):
+                want[mine] += s * u[:, r, None] * b[e, :, r]
+                mag[mine] += s * u_mag[:, r, None] * np.abs(b[e, :, r])
+    y = c.run()
+    np.testing.assert_array_equal(np.isnan(y), np.isnan(want))
+    wild = np.isinf(want)
+    assert wild.any()
+    np.testing.assert_array_equal(y[wild], want[wild])
+    fine = np.isfinite(want)
+    with np.errstate(invalid="ignore"):
+        tol = 2.0 ** -23 * ((c.K + 3 * c.R + 80) * mag + np.abs(c.base) + np.abs(want))
+        assert (np.abs(y - want)[fine] <= tol[fine]).all()

@@ -1376,6 +1376,14 @@ int check_lora(const q4nx_lora* L, const char* name) {
   return Q4NX_OK;
 }
 
+// Whether [p, p + n) shares a byte with what a call reads of a checked table.
+bool overlaps_table(const q4nx_lora& L, const void* p, uint64_t n) {
+  const uint64_t others = (uint64_t)L.n_adapters - 1, e = (uint64_t)L.n_adapters * 4;
+  return overlap(p, n, L.a, others * L.a_stride + (uint64_t)L.rank * L.cols * 2) ||
+         overlap(p, n, L.b, others * L.b_stride + (uint64_t)L.rank * L.rows * 2) || overlap(p, n, L.scale, e) ||
+         (L.ranks && overlap(p, n, L.ranks, e));
+}
+
 // Launch shape and workspace layout of a call over checked tables.
 struct LoraShape {
   q4nx::LoraArgs a;
@@ -1486,6 +1494,8 @@ int run_lora(const q4nx_lora_job* jobs, int n, const uint16_t* x, const int32_t*
       const uint64_t kb = (uint64_t)M * jobs[k].lora.rows * 4;
       if (k != i && (overlap(j.y, bytes, jobs[k].y, kb) || overlap(j.y, bytes, jobs[k].base, kb)))
         return fail(Q4NX_E_ARG, "%s: y of job %d overlaps y or base of job %d", name, i, k);
+      if (overlaps_table(jobs[k].lora, j.y, bytes))
+        return fail(Q4NX_E_ARG, "%s: y of job %d overlaps an arena, the scales or the ranks of job %d", name, i, k);
     }
     if (overlap(j.y, bytes, x, (uint64_t)M * j.lora.cols * 2) || overlap(j.y, bytes, ids, (uint64_t)M * 4))
       return fail(Q4NX_E_ARG, "%s: y of job %d overlaps x or ids", name, i);

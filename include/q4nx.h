@@ -557,7 +557,9 @@ enum { Q4NX_LORA_BATCH_MAX_JOBS = 8, Q4NX_LORA_MAX_M = 4096 };
  *   x    DEVICE bf16 [M][cols], row-major, 16-byte aligned: what the projection read
  *   ids  DEVICE int32 [M], in any order
  *   base, y  4-byte aligned; every row of y is written (in place, rows without
- *        an adapter are left as they are); y and base may not overlap in part
+ *        an adapter are left as they are); y and base may not overlap in part, and
+ *        y lies apart from every other input, the arenas with what lies between
+ *        their adapters among them (E_ARG)
  *   M    1..Q4NX_LORA_MAX_M
  *   ws   DEVICE workspace of q4nx_lora_ws(L, M) bytes, 256-byte aligned.  Nothing
  *        in it needs initialising; calls that share it must not overlap.
@@ -585,7 +587,7 @@ size_t q4nx_lora_ws(const q4nx_lora* L, int M);
  * (q|k|v, gate|up), in as many launches as one.
  *   jobs  HOST array of n_jobs (1..Q4NX_LORA_BATCH_MAX_JOBS), with the cols and
  *         n_adapters of jobs[0] (E_SHAPE otherwise); rank and rows may differ.
- *         Each y must lie apart from every other job's y and base.
+ *         Each y must lie apart from every other job's y, base and table.
  */
 int q4nx_lora_add_batched(const q4nx_lora_job* jobs, int n_jobs, const uint16_t* x, const int32_t* ids,
                           int M, void* ws, size_t ws_bytes, void* stream);

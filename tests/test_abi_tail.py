@@ -198,3 +198,38 @@ def test_logprobs_outputs_lie_apart(q):
                 args = dict(at, **{out: place})
                 _expect(q, q.E_ARG, q.token_logprobs, n=n, M=M, ws=WS, n_tok=T, k=k, ldy=1024, stream=0, ws_bytes=need,
                         **args)
+
+
+def test_lora_outputs_lie_apart_from_the_tables(q):
+    """A y over an arena, the scales or the ranks, of its own job or another, is refused."""
+    E, R, K = 4, 16, 512
+    pad = 64
+
+    def table(base, N):
+        return q.lora_table(n_adapters=E, rank=R, rows=N, cols=K, a=base, b=base + 0x100000, scale=base + 0x200000,
+                            ranks=base + 0x300000, a_stride=R * K * 2 + pad, b_stride=R * N * 2 + pad,
+                            a_bytes=1 << 19, b_bytes=1 << 19)
+    M, N = 3, 64
+    size = M * N * 4
+    t = [table(0x10000000 * (i + 2), N) for i in range(2)]
+    parts = [(0, (E - 1) * (R * K * 2 + pad) + R * K * 2), (0x100000, (E - 1) * (R * N * 2 + pad) + R * N * 2),
+             (0x200000, E * 4), (0x300000, E * 4)]
+    apart = 0x600000
+
+    def call(y0, y1=None, base=None):
+        jobs = [(t[0], base, y0)] + ([(t[1], None, y1)] if y1 else [])
+        q.lora_add_batched(jobs, 0x400000, 0x500000, M, WS, stream=0, ws_bytes=1)   # the workspace is checked last
+    _expect(q, q.E_WORKSPACE, call, apart, apart + size)
+    for at, n in parts:
+        for table_at in (0x20000000, 0x30000000):
+            lo = table_at + at
+            for y in (lo - size + 4, lo, lo + n - 4):
+                _expect(q, q.E_ARG, call, apart, y)
+                _expect(q, q.E_ARG, call, y, apart)
+                if table_at == 0x20000000:
+                    _expect(q, q.E_ARG, call, y)
+                    _expect(q, q.E_ARG, call, y, base=0x700000)
+            for y in (lo - size, lo + n):
+                _expect(q, q.E_WORKSPACE, call, apart, y)
+    # a base over a table is read only
+    _expect(q, q.E_WORKSPACE, call, apart, base=0x20000000)

@@ -1510,6 +1510,13 @@ int run_lora(const q4nx_lora_job* jobs, int n, const uint16_t* x, const int32_t*
   if (!ws || ws_bytes < sh.total)
     return fail(Q4NX_E_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", name, ws_bytes, sh.total);
   if (!aligned(ws, 256)) return fail(Q4NX_E_ALIGN, "%s: workspace not 256-byte aligned", name);
+  bool over = overlap(ws, sh.total, x, (uint64_t)M * L[0]->cols * 2) || overlap(ws, sh.total, ids, (uint64_t)M * 4);
+  for (int i = 0; i < n; ++i) {
+    const uint64_t bytes = (uint64_t)M * L[i]->rows * 4;
+    over |= overlap(ws, sh.total, jobs[i].y, bytes) || overlap(ws, sh.total, jobs[i].base, bytes) ||
+            overlaps_table(*L[i], ws, sh.total);
+  }
+  if (over) return fail(Q4NX_E_ARG, "%s: the workspace overlaps an input or output", name);
   uint8_t* w = static_cast<uint8_t*>(ws);
   for (int m0 = 0; m0 < M; m0 += per) {
     q4nx::LoraArgs& a = sh.a;
@@ -1628,6 +1635,9 @@ int q4nx_token_logprobs(const float* y, int n, int ldy, int M, const int32_t* to
   if (!ws || ws_bytes < lay.total)
     return fail(Q4NX_E_WORKSPACE, "token_logprobs: workspace of %zu bytes, %zu needed", ws_bytes, lay.total);
   if (!aligned(ws, 256)) return fail(Q4NX_E_ALIGN, "token_logprobs: workspace not 256-byte aligned");
+  for (const auto& p : part)
+    if (p.p && overlap(ws, lay.total, p.p, p.bytes))
+      return fail(Q4NX_E_ARG, "token_logprobs: the workspace overlaps an input or output");
   q4nx::LogprobArgs a;
   memset(&a, 0, sizeof a);
   a.y = y;

@@ -561,8 +561,9 @@ enum { Q4NX_LORA_BATCH_MAX_JOBS = 8, Q4NX_LORA_MAX_M = 4096 };
  *        y lies apart from every other input, the arenas with what lies between
  *        their adapters among them (E_ARG)
  *   M    1..Q4NX_LORA_MAX_M
- *   ws   DEVICE workspace of q4nx_lora_ws(L, M) bytes, 256-byte aligned.  Nothing
- *        in it needs initialising; calls that share it must not overlap.
+ *   ws   DEVICE workspace of q4nx_lora_ws(L, M) bytes, 256-byte aligned, apart from
+ *        every input and output (E_ARG).  Nothing in it needs initialising; calls
+ *        that share it must not overlap.
  * Rows of one adapter are found on the device and taken together, in tiles of up
  * to 16 or 64 rows, so an adapter is read once per tile.  Sums are fp32 in an
  * order fixed by the call's sizes: a row's bits depend neither on the other rows
@@ -636,10 +637,10 @@ int q4nx_add_rmsnorm(const float* y, const float* r, const uint16_t* w, int M, i
  *   k        0..32; top_ids DEVICE int32 [M][k] (NULL when 0), top_logp DEVICE
  *            fp32 [M][k] or NULL
  *   ws       DEVICE workspace of q4nx_token_logprobs_ws(n, M, k) bytes (enough
- *            for fewer rows too), 256-byte aligned.  Nothing in it needs initialising; calls that share it
- *            must not overlap.
- * E_ARG also when nothing is asked for, or an output overlaps another or y or
- * tokens.  The largest logit is set apart from the sum, so that the log
+ *            for fewer rows too), 256-byte aligned.  Nothing in it needs
+ *            initialising; calls that share it must not overlap.
+ * E_ARG also when nothing is asked for, or an output or the workspace overlaps
+ * another array.  The largest logit is set apart from the sum, so that the log
  * probability of a likely token, and the entropy of a sharp distribution, keep
  * their digits.
  */

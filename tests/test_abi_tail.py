@@ -233,3 +233,24 @@ def test_lora_outputs_lie_apart_from_the_tables(q):
                 _expect(q, q.E_WORKSPACE, call, apart, y)
     # a base over a table is read only
     _expect(q, q.E_WORKSPACE, call, apart, base=0x20000000)
+
+
+def test_workspaces_lie_apart(q):
+    """A workspace over an input or output is refused: where it begins in one, and where its last needed
+    bytes reach one."""
+    M, T, k, n = 4, 3, 5, 1000
+    at = dict(y=0x1000000, tokens=0x2000000, logp=0x3000000, entropy=0x4000000, top_ids=0x5000000, top_logp=0x6000000)
+    need = q.token_logprobs_ws(n, M, k)
+    assert need % 256 == 0
+    for name in at:
+        for ws in (at[name], at[name] - need + 256):
+            _expect(q, q.E_ARG, q.token_logprobs, n=n, M=M, ws=ws, n_tok=T, k=k, ldy=1024, stream=0, ws_bytes=1 << 22, **at)
+            assert "workspace" in q.last_error()
+    L = _table(q, ranks=0x800000)
+    need = q.lora_ws(L, M)
+    assert need % 256 == 0
+    at = dict(a=0x100000, b=0x200000, scale=0x300000, ranks=0x800000, x=0x400000, ids=0x500000, y=0x600000, base=0x700000)
+    for place in at.values():
+        for ws in (place, place - need + 256):
+            _expect(q, q.E_ARG, _add, q, L, M=M, base=at["base"], ws=ws, ws_bytes=1 << 22)
+            assert "workspace" in q.last_error()

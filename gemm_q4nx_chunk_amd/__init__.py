@@ -512,13 +512,18 @@ def token_logprobs_ws(n: int, M: int, k: int = 0) -> int:
     return int(_lib.q4nx_token_logprobs_ws(n, M, k))
 
 
-def token_logprobs(y, n: int, M: int, ws, tokens=None, n_tok: int = 0, logp=None, entropy=None, k: int = 0,
-                   top_ids=None, top_logp=None, ldy: int | None = None, stream=None,
+def token_logprobs(y, n: int, M: int, ws, tokens=None, n_tok: int | None = None, logp=None, entropy=None,
+                   k: int | None = None, top_ids=None, top_logp=None, ldy: int | None = None, stream=None,
                    ws_bytes: int | None = None) -> None:
     """Of each row of logits y[m][:n]: logp[M, n_tok] of tokens[M, n_tok] (int32), entropy[M], and
-    the k likeliest tokens top_ids[M, k] (int32, best first) with top_logp[M, k]."""
-    _check(_lib.q4nx_token_logprobs(_ptr(y), n, n if ldy is None else ldy, M, _ptr(tokens), n_tok, _ptr(logp),
-                                    _ptr(entropy), k, _ptr(top_ids), _ptr(top_logp), _ptr(ws),
+    the k likeliest tokens top_ids[M, k] (int32, best first) with top_logp[M, k].  n_tok and k are
+    given wherever their arrays are."""
+    if n_tok is None and (tokens is not None or logp is not None):
+        raise Q4nxError(E_ARG, "token_logprobs: tokens or logp without n_tok")
+    if k is None and (top_ids is not None or top_logp is not None):
+        raise Q4nxError(E_ARG, "token_logprobs: top_ids or top_logp without k")
+    _check(_lib.q4nx_token_logprobs(_ptr(y), n, n if ldy is None else ldy, M, _ptr(tokens), n_tok or 0, _ptr(logp),
+                                    _ptr(entropy), k or 0, _ptr(top_ids), _ptr(top_logp), _ptr(ws),
                                     _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
 
 

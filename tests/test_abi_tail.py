@@ -254,3 +254,21 @@ def test_workspaces_lie_apart(q):
         for ws in (place, place - need + 256):
             _expect(q, q.E_ARG, _add, q, L, M=M, base=at["base"], ws=ws, ws_bytes=1 << 22)
             assert "workspace" in q.last_error()
+
+
+def test_logprobs_arrays_without_their_count(q):
+    """Arrays that would be left unwritten without a word, because their count was left out, are refused;
+    a count of 0 may stand beside them."""
+    def call(**arrays):
+        args = dict(entropy=0x400000, ws=WS, ws_bytes=1, stream=0)
+        args.update(arrays)
+        q.token_logprobs(0x100000, 5000, 2, **args)
+    _expect(q, q.E_WORKSPACE, call)
+    for arrays in (dict(tokens=0x200000, logp=0x300000), dict(tokens=0x200000), dict(logp=0x300000)):
+        _expect(q, q.E_ARG, call, **arrays)
+        _expect(q, q.E_ARG, call, k=3, top_ids=0x500000, **arrays)
+        _expect(q, q.E_WORKSPACE, call, n_tok=0, **arrays)
+    for arrays in (dict(top_ids=0x500000, top_logp=0x600000), dict(top_ids=0x500000), dict(top_logp=0x600000)):
+        _expect(q, q.E_ARG, call, **arrays)
+        _expect(q, q.E_WORKSPACE, call, k=0, **arrays)
+    _expect(q, q.E_WORKSPACE, call, n_tok=1, tokens=0x200000, logp=0x300000, k=2, top_ids=0x500000)

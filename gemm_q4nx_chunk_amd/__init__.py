@@ -195,8 +195,10 @@ def _nbytes(t) -> int:
 def _stream(stream) -> int:
     if stream is None:
         import torch
-        # the current stream's handle, without building a Stream object (2.9 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # the current stream's handle without building a Stream object (2.9 us a call), where this
+        # torch has the function, which its public interface does not promise
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

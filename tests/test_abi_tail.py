@@ -272,3 +272,18 @@ def test_logprobs_arrays_without_their_count(q):
         _expect(q, q.E_ARG, call, **arrays)
         _expect(q, q.E_WORKSPACE, call, k=0, **arrays)
     _expect(q, q.E_WORKSPACE, call, n_tok=1, tokens=0x200000, logp=0x300000, k=2, top_ids=0x500000)
+
+
+def test_the_current_stream_by_either_way(q, monkeypatch):
+    """Calls take the current stream of the current device, also with a torch that lacks the shorter way."""
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        cuda_stream = 0x1234
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0x1000 + device, raising=False)
+    assert q._stream(None) == 0x1003
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert q._stream(None) == 0x1234
+    assert q._stream(7) == 7 and q._stream(Stream) == 0x1234

@@ -1602,7 +1602,8 @@ int q4nx_add_rmsnorm(const float* y, const float* r, const uint16_t* w, int M, i
 }
 
 size_t q4nx_token_logprobs_ws(int n, int M, int k) {
-  if (n < 1 || n > q4nx::kLogprobMaxN || M < 1 || M > 65535 || k < 0 || k > q4nx::kLogprobMaxK) return 0;
+  if (n < 1 || n > q4nx::kLogprobMaxN || M < 1 || M > 65535 || k < 0 || k > q4nx::kLogprobMaxK || k > n)
+    return 0;
   return q4nx::logprob_ws_layout(n, M, k).total;
 }
 

@@ -634,8 +634,8 @@ int q4nx_add_rmsnorm(const float* y, const float* r, const uint16_t* w, int M, i
  *   tokens   DEVICE int32 [M][n_tok], logp DEVICE fp32 [M][n_tok]; n_tok 0..64
  *            (both may be NULL when 0)
  *   entropy  DEVICE fp32 [M] or NULL
- *   k        0..32; top_ids DEVICE int32 [M][k] (NULL when 0), top_logp DEVICE
- *            fp32 [M][k] or NULL
+ *   k        0..min(32, n); top_ids DEVICE int32 [M][k] (NULL when 0), top_logp
+ *            DEVICE fp32 [M][k] or NULL
  *   ws       DEVICE workspace of q4nx_token_logprobs_ws(n, M, k) bytes (enough
  *            for fewer rows too), 256-byte aligned.  Nothing in it needs
  *            initialising; calls that share it must not overlap.

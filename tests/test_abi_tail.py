@@ -287,3 +287,12 @@ def test_the_current_stream_by_either_way(q, monkeypatch):
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
     assert q._stream(None) == 0x1234
     assert q._stream(7) == 7 and q._stream(Stream) == 0x1234
+
+
+@pytest.mark.parametrize("n", [1, 5, 31])
+def test_no_more_alternatives_than_logits(q, n):
+    """The workspace's size and the call agree on the largest k."""
+    assert q.token_logprobs_ws(n, 3, n) > 0 and q.token_logprobs_ws(n, 3, n + 1) == 0
+    args = dict(y=0x100000, n=n, M=3, ws=WS, ws_bytes=1, top_ids=0x500000, stream=0)
+    _expect(q, q.E_WORKSPACE, q.token_logprobs, k=n, **args)
+    _expect(q, q.E_ARG, q.token_logprobs, k=n + 1, **args)

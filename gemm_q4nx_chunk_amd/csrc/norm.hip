@@ -19,7 +19,7 @@
 //   x = t / sqrt(mean(t^2) + 4^-e eps) * w,  t = 2^-e s.
 // A square below 2^-126 counts for at most 2^-30 of a mean of 2^-96 and up, so
 // that other rows, with any usual eps all that do not overflow, need no second
-// sum; they are scaled by 1, which changes no bit.
+// sum.
 //
 // Bound by HBM for many rows and by two memory latencies (load, reduce, store)
 // for few.
@@ -106,11 +106,31 @@ __global__ __launch_bounds__(WAVES ? 64 * WAVES : 256) void k_add_rmsnorm(
     }
   }
   __shared__ float part[WAVES > 1 ? WAVES : 1];
-  float mean = over_row<WAVES, false>(squares(s, 1.f), part, wave, lane) / (float)D + eps;
-  float pre = 1.f;   // 2^-e
-  if (!(mean >= kLowMean && mean <= __FLT_MAX__)) {   // the same in all of the row's threads
-    if constexpr (WAVES > 1) __syncthreads();         // part is read above
-    float top = 0.f;
+  const float mean = over_row<WAVES, false>(squares(s, 1.f), part, wave, lane) / (float)D + eps;
+  float inv = 1.f / sqrtf(mean);
+  auto write = [&](float pre) {
+#pragma unroll
+    for (int g = 0; g < NV; ++g) {
+      const int c = 4 * (g * kThreads + t);
+      const f32x4 v = s[g];
+      const u32x2 o = {bf16_pair(v[0] * pre * inv * bf16lo(wv[g].x), v[1] * pre * inv * bf16hi(wv[g].x)),
+                       bf16_pair(v[2] * pre * inv * bf16lo(wv[g].y), v[3] * pre * inv * bf16hi(wv[g].y))};
+      if (c + 3 < D) {
+        if (r_out) *reinterpret_cast<f32x4u*>(r_out + row + c) = v;
+        *reinterpret_cast<u32x2u*>(x + row + c) = o;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c + i < D) {
+            if (r_out) r_out[row + c + i] = v[i];
+            x[row + c + i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
+          }
+      }
+    }
+  };
+  if (__builtin_expect(!(mean >= kLowMean && mean <= __FLT_MAX__), 0)) {   // the same in all of the row's threads
+    if constexpr (WAVES > 1) __syncthreads();                               // part is read above
+    float top = 0.f, pre = 1.f;                                             // pre: 2^-e
 #pragma unroll
     for (int g = 0; g < NV; ++g)
 #pragma unroll
@@ -121,28 +141,12 @@ __global__ __launch_bounds__(WAVES ? 64 * WAVES : 256) void k_add_rmsnorm(
       // 2^126 at most, which takes 2^-149 to 2^-23
       pre = ldexpf(1.f, -max(__builtin_amdgcn_frexp_expf(fmaxf(top, sqrtf(eps))), -126));
       if constexpr (WAVES > 1) __syncthreads();
-      mean = over_row<WAVES, false>(squares(s, pre), part, wave, lane) / (float)D + eps * pre * pre;
+      inv = 1.f / sqrtf(over_row<WAVES, false>(squares(s, pre), part, wave, lane) / (float)D + eps * pre * pre);
     }
+    write(pre);
+    return;
   }
-  const float inv = 1.f / sqrtf(mean);
-#pragma unroll
-  for (int g = 0; g < NV; ++g) {
-    const int c = 4 * (g * kThreads + t);
-    const f32x4 v = s[g];
-    const u32x2 o = {bf16_pair(v[0] * pre * inv * bf16lo(wv[g].x), v[1] * pre * inv * bf16hi(wv[g].x)),
-                     bf16_pair(v[2] * pre * inv * bf16lo(wv[g].y), v[3] * pre * inv * bf16hi(wv[g].y))};
-    if (c + 3 < D) {
-      if (r_out) *reinterpret_cast<f32x4u*>(r_out + row + c) = v;
-      *reinterpret_cast<u32x2u*>(x + row + c) = o;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c + i < D) {
-          if (r_out) r_out[row + c + i] = v[i];
-          x[row + c + i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
-        }
-    }
-  }
+  write(1.f);
 }
 
 hipError_t launch_add_rmsnorm(const float* y, const float* r, const uint16_t* w, int M, int D, float eps,

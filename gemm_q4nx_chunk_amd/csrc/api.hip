@@ -1419,10 +1419,13 @@ void lora_shape(const q4nx_lora* const* L, int n, int M, int room, LoraShape& sh
   }
   // Parts of the columns.  Each part is a row of u that the expand reads again
   // for each of its ranges, so no more than give a wave two steps, than fill
-  // the GPU, or than the expand loads at once.  Up to 64 rows, with an adapter
-  // each: 64 rows of 9728 columns, rank 64, 17.6 us with 4 parts, 19.6 with 8,
-  // 22.9 with 10; 32 rows of 14336 columns 19.7, 18.9, 22.1.  More rows: 4096 of
-  // 14336 columns, rank 64, 91 us with 3 parts, 104 with 7.
+  // the GPU, or than the expand loads at once.  Up to 64 rows as if each had an
+  // adapter of its own, as measured: 64 rows of 9728 columns, rank 64, 17.6 us
+  // with 4 parts, 19.6 with 8, 22.9 with 10; 32 rows of 14336 columns 19.7, 18.9,
+  // 22.1.  Rows that share adapters get the same parts, and leave more of the GPU
+  // empty (64 rows of 9728 columns, rank 64, of one adapter 12.9 us, of three
+  // 13.5); more parts were not measured for them.  More rows: 4096 of 14336
+  // columns, rank 64, 91 us with 3 parts, 104 with 7.
   const int steps = a.cols / q4nx::kLoraStepCols;
   const int per = q4nx::kLoraShrinkWaves * 2;
   a.split = std::max(1, std::min((steps + per - 1) / per, q4nx::kLoraMaxSplit));

@@ -19,19 +19,23 @@
 // gathering space in LDS that holds the index of every value seen above T and,
 // of those equal to T, the first ones.  The first chunk's T comes from the 64
 // lanes' own maxima: a value that k of them reach.  After that only the values
-// above T are gathered (k / j of chunk j on average, for random logits): each
-// lane marks its hits in a word, a sum over the lanes below gives it its place.
-// A full space is cut down to its k largest.  At the end the gathered values
+// above T are gathered (of random logits about as many in every chunk as in the
+// first, for T stays until the space is full): each lane marks its hits in a
+// word, a sum over the lanes below gives it its place.  A full space is cut down
+// to its k largest, and T raised to the least of them.  At the end the gathered values
 // are read again, as keys (topk.h's: larger value, then lower index), and
 // ordered by counting, for each, how many are larger.  Should more values lie
 // above T than the space holds, T is raised by bisection over the order of
 // fp32 first.
 //
-// Many rows are bound by HBM: 1000 rows of 151936 logits, 608 MB, take 114 us
-// (5.3 TB/s; a large copy reaches 5.2).  64 rows (39 MB, in the Infinity Cache)
-// take 11.9 us a call with k = 0 and 17.8 with k = 20, the latency of one chunk a
-// wave and of the join, and the top k; one row 8.4 us with k = 0 and 9.5 with
-// k = 5, two launches of 5 us each.
+// Many rows are bound by HBM with k <= 1: 1000 rows of 151936 logits, 608 MB, take
+// 114 us (5.3 TB/s), 4096 rows 429 us (5.8); a large copy, which writes too,
+// reaches 5.2, this library's longest weight streams 6.0 to 6.3.  Their top k
+// costs more: 1000 rows 148 us with k = 20 and 170 with k = 32, 828 and 937 MB
+// fetched instead of 616, for the gathered values are read again; 4096 rows 508
+// with k = 20.  64 rows (39 MB, in the Infinity Cache) take 11.9 us a call with
+// k = 0 and 17.7 with k = 20, the latency of one chunk a wave and of the join, and
+// the top k; one row 9.4 us with k = 5, its two kernels 5.0 and 4.8.
 #include <algorithm>
 
 #include "logprobs_args.h"

@@ -237,7 +237,7 @@ __global__ __launch_bounds__(1024) void k_lora_route(LoraArgs a) {
 //
 // Measured (4096 rows, 14336 columns, rank 64; 64 rows of 40 adapters, 9728
 // columns): operands straight from memory 75 and 14 us; 64 bytes of a row at a
-// time through LDS 51 and 12; as here 37 and 10.
+// time through LDS 51 and 12; as here 37 and 11.
 inline size_t lora_shrink_lds(int blocks, int sub) {
   return (size_t)kLoraShrinkWaves * blocks * 2048 + 16 * sub * sizeof(int32_t);
 }

@@ -56,7 +56,12 @@ struct LoraArgs {
 // adapters, rank 64, 4096 x 4096: 45 us, 62 with 64), or the rows are few and
 // short, so that more workgroups pay more than each adapter read fewer times
 // (512 rows of 4 adapters, rank 64, 4096 x 4096: 23.3 and 25.1 us; 1613 x 2304:
-// 20.6 and 23.3; but 1052 x 11264, rank 16: 29.3 and 26.5).
+// 20.6 and 23.3; but 1052 x 11264, rank 16: 29.3 and 26.5).  Where the rows stop
+// being few depends on the rank and the outputs as well, and 2^22 elements of x
+// are on the low side of it: 1024 rows of 4 adapters, 4096 outputs, ranks 16 and
+// 64, take 18.3 and 24.5 us with 16 at 5120 columns (21.1 and 28.5 with 64), 19.6
+// and 27.0 at 9728 (22.1 and 30.4); 2048 rows 23.4 and 32.8 at 2560 columns (26.7
+// and 33.8), 27.7 and 41.6 at 4096 (27.5 and 37.7).
 inline int lora_tile_rows(int M, int n_adapters, int cols) {
   const int groups = M < n_adapters + 1 ? M : n_adapters + 1;
   if (M <= kLoraWaveRows || M <= 32 * groups) return 16;

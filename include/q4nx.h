@@ -569,9 +569,10 @@ enum { Q4NX_LORA_BATCH_MAX_JOBS = 8, Q4NX_LORA_MAX_M = 4096 };
  * order fixed by the call's sizes: a row's bits depend neither on the other rows
  * nor on its place.  B_e (A_e x) keeps fp32's precision (A_e x enters the second
  * product as three bf16 parts that hold its 24 bits).
- * Infinities and NaNs of x, A, B and the scale come out as the formula has them:
- * an infinite weight of B gives an infinity, or NaN where it meets 0 or one of
- * the other sign (scale_e A_e x below 2^-100 may count as 0 there).
+ * The scale multiplies A_e x, in fp32.  Infinities and NaNs of x, A and B come
+ * out as the formula has them: an infinite weight of B gives an infinity, or NaN
+ * where it meets 0 or an infinity of the other sign (scale_e A_e x below 2^-100
+ * may count as 0 there).
  * An id below -1 or past the last adapter is never dereferenced: its row is
  * taken as one without an adapter and bit 0 of the uint32 at ws[0] is set
  * (cleared at the start of each call; read it after synchronising).

@@ -78,6 +78,35 @@ class LoraJob(ctypes.Structure):
     _fields_ = [("lora", Lora), ("base", ctypes.c_void_p), ("y", ctypes.c_void_p)]
 
 
+class KvCache(ctypes.Structure):
+    """q4nx_kv_cache: a paged cache of keys and values (see include/q4nx.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("kv_heads", "head_dim", "page_tokens", "n_pages", "type")] + [
+        (n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + [
+        (n, ctypes.c_int64) for n in ("k_bytes", "v_bytes", "k_scale_bytes", "v_scale_bytes")]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("ld", ctypes.c_int64), ("heads", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("inv_freq", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p)]
+
+
+class AttnBatch(ctypes.Structure):
+    """q4nx_attn_batch: the sequences of one attention call (see include/q4nx.h)."""
+    _fields_ = [("n_seq", ctypes.c_int32), ("max_q", ctypes.c_int32), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p), ("pages_ld", ctypes.c_int32),
+                ("prefix_len", ctypes.c_int32), ("prefix_pages", ctypes.c_void_p)]
+
+
+class Linear(ctypes.Structure):
+    """q4nx_linear: the sequences and heads of one linear attention call (see include/q4nx.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("k_heads", "v_heads", "dk", "dv", "n_seq", "max_q", "n_slots")] + [
+        (n, ctypes.c_void_p) for n in ("q_start", "slots", "fresh")]
+
+
 class ChunkLayout(ctypes.Structure):
     """q4nx_chunk_layout: where a q4_1 / Q4_K chunk keeps each field (see include/q4nx.h)."""
     _fields_ = [(n, ctypes.c_int32) for n in (
@@ -133,6 +162,17 @@ _lib.q4nx_add_rmsnorm.argtypes = [_P, _P, _P, _I, _I, ctypes.c_float, _P, _P, _P
 _lib.q4nx_token_logprobs_ws.argtypes = [_I, _I, _I]
 _lib.q4nx_token_logprobs_ws.restype = ctypes.c_size_t
 _lib.q4nx_token_logprobs.argtypes = [_P, _I, _I, _I, _P, _I, _P, _P, _I, _P, _P, _P, ctypes.c_size_t, _P]
+_lib.q4nx_kv_append.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(Rope), ctypes.POINTER(Heads), _P,
+                                ctypes.POINTER(Heads), ctypes.POINTER(Heads), _P, _I, _P, _P]
+_lib.q4nx_attention.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(AttnBatch), _P, _I, _I, ctypes.c_float, _P, _P,
+                                _P, ctypes.c_size_t, _P, _P]
+_lib.q4nx_attention_ws.argtypes = [ctypes.POINTER(KvCache), ctypes.POINTER(AttnBatch), _I, _I]
+_lib.q4nx_attention_ws.restype = ctypes.c_size_t
+_L = ctypes.c_int64
+_lib.q4nx_linear_attn.argtypes = [ctypes.POINTER(Linear), _P, _L, _P, _L, _P, _L, _P, _L, _I, ctypes.c_float, _P, _P,
+                                  _P, _P, ctypes.c_size_t, _P, _P]
+_lib.q4nx_linear_attn_ws.argtypes = [ctypes.POINTER(Linear), _I]
+_lib.q4nx_linear_attn_ws.restype = ctypes.c_size_t
 _lib.q4nx_plan_create.argtypes = [ctypes.POINTER(GemvJob), ctypes.POINTER(ctypes.c_int32), _I, _I,
                                   ctypes.POINTER(ctypes.c_void_p)]
 _lib.q4nx_plan_run.argtypes = [_P, _P]
@@ -149,7 +189,7 @@ for _f in ("q4nx_weight_check", "q4nx_gemv", "q4nx_gemv_batched", "q4nx_gemm_blo
            "q4nx_plan_run", "q4nx_plan_errors", "q4nx_gemm_exchange_mode", "q4nx_gemv_topk",
            "q4nx_chunk_layout_default", "q4nx_chunk_layout_check", "q4nx_relayout", "q4nx_plan_set_mode",
            "q4nx_gemm_block_noalloc", "q4nx_lora_add", "q4nx_lora_add_batched", "q4nx_add_rmsnorm",
-           "q4nx_token_logprobs"):
+           "q4nx_token_logprobs", "q4nx_kv_append", "q4nx_attention", "q4nx_linear_attn"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 
@@ -527,6 +567,128 @@ def token_logprobs(y, n: int, M: int, ws, tokens=None, n_tok: int | None = None,
     _check(_lib.q4nx_token_logprobs(_ptr(y), n, n if ldy is None else ldy, M, _ptr(tokens), n_tok or 0, _ptr(logp),
                                     _ptr(entropy), k or 0, _ptr(top_ids), _ptr(top_logp), _ptr(ws),
                                     _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
+
+
+KV_BF16, KV_INT8 = 0, 1
+_F32, _BF16 = 0, 1
+
+
+def kv_cache(kv_heads: int, head_dim: int, page_tokens: int, n_pages: int, k, v, k_scale=None, v_scale=None,
+             k_bytes: int | None = None, v_bytes: int | None = None, k_scale_bytes: int | None = None,
+             v_scale_bytes: int | None = None) -> KvCache:
+    """A paged cache over device memory (layout: include/q4nx.h): k and v of n_pages * kv_heads * page_tokens *
+    head_dim bf16 values, or int8 codes beside k_scale and v_scale, fp32 [n_pages][kv_heads][page_tokens]."""
+    c = KvCache(kv_heads, head_dim, page_tokens, n_pages, KV_BF16 if k_scale is None and v_scale is None else KV_INT8,
+                _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _nbytes(k) if k_bytes is None else k_bytes,
+                _nbytes(v) if v_bytes is None else v_bytes, _nbytes(k_scale) if k_scale_bytes is None else k_scale_bytes,
+                _nbytes(v_scale) if v_scale_bytes is None else v_scale_bytes)
+    c._owners = (k, v, k_scale, v_scale)
+    return c
+
+
+def rope(inv_freq, pos, dim: int, interleaved: bool = False) -> Rope:
+    """Rotation of the first dim dimensions by pos[m] * inv_freq[i] (fp32 [dim/2], int32 [M]), in pairs (i, i + dim/2) or
+    (2i, 2i + 1)."""
+    r = Rope(dim, 1 if interleaved else 0, _ptr(inv_freq), _ptr(pos))
+    r._owners = (inv_freq, pos)
+    return r
+
+
+def heads(t, n: int, head_dim: int, ld: int | None = None, bf16: bool | None = None) -> Heads:
+    """M rows of n heads: fp32, or bf16 (bf16 or int16 tensors), rows ld elements apart (a tensor's first stride)."""
+    if isinstance(t, int):
+        return Heads(t, n * head_dim if ld is None else ld, n, _BF16 if bf16 else _F32)
+    if t.element_size() not in (2, 4):
+        raise Q4nxError(E_ARG, f"heads of type {t.dtype}: fp32 or bf16 are taken")
+    if t.dim() < 2:
+        step = n * head_dim
+    else:
+        if t.stride(-1) != 1 or (t.dim() == 3 and t.stride(1) != head_dim):
+            raise Q4nxError(E_SHAPE, "heads: the columns of a row must be contiguous")
+        step = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), n * head_dim)
+    h = Heads(t.data_ptr(), step if ld is None else ld, n, (t.element_size() == 2) if bf16 is None else bf16)
+    h._owner = t
+    return h
+
+
+def kv_append(cache: KvCache, k, v, slots, M: int, rope: Rope | None = None, q=None, q_heads: int | None = None,
+              q_out=None, flags=None, stream=None) -> None:
+    """k and v (tensors of kv_heads heads a row, or what heads() made) to the cache's slots[M], k turned by rope; q turned
+    into q_out (bf16 [M][q_heads][head_dim])."""
+    D, n = cache.head_dim, cache.kv_heads
+    if q is not None and q_heads is None and not isinstance(q, Heads):
+        raise Q4nxError(E_ARG, "kv_append: q without q_heads")
+    qh, kh, vh = (t if t is None or isinstance(t, Heads) else heads(t, c, D) for t, c in ((q, q_heads), (k, n), (v, n)))
+    ref = lambda s: None if s is None else ctypes.byref(s)  # noqa: E731
+    _check(_lib.q4nx_kv_append(ctypes.byref(cache), ref(rope), ref(qh), _ptr(q_out), ref(kh), ref(vh), _ptr(slots), M,
+                               _ptr(flags), _stream(stream)))
+
+
+def attn_batch(q_start, kv_len, pages, max_q: int, prefix_len: int = 0, prefix_pages=None, n_seq: int | None = None,
+               pages_ld: int | None = None) -> AttnBatch:
+    """The sequences of an attention call: q_start int32 [n_seq + 1], kv_len int32 [n_seq], pages int32 [n_seq][pages_ld],
+    at most max_q rows a sequence, behind a prefix of prefix_len tokens in prefix_pages."""
+    b = AttnBatch(kv_len.numel() if n_seq is None else n_seq, max_q, _ptr(q_start), _ptr(kv_len), _ptr(pages),
+                  pages.shape[1] if pages_ld is None else pages_ld, prefix_len, _ptr(prefix_pages))
+    b._owners = (q_start, kv_len, pages, prefix_pages)
+    return b
+
+
+def attention_ws(cache: KvCache, batch: AttnBatch, q_heads: int, M: int) -> int:
+    """Workspace bytes of attention (0 = bad arguments)."""
+    return int(_lib.q4nx_attention_ws(ctypes.byref(cache), ctypes.byref(batch), q_heads, M))
+
+
+def attention(cache: KvCache, batch: AttnBatch, q, q_heads: int, M: int, scale: float, out, ws, lse=None, flags=None,
+              stream=None, ws_bytes: int | None = None) -> None:
+    """out[M, q_heads, head_dim] (bf16) = softmax(scale q k^T) v over the prefix and each sequence's cached tokens, causal;
+    lse[M, q_heads] the logarithm of the sums."""
+    _check(_lib.q4nx_attention(ctypes.byref(cache), ctypes.byref(batch), _ptr(q), q_heads, M, scale, _ptr(out), _ptr(lse),
+                               _ptr(ws), _nbytes(ws) if ws_bytes is None else ws_bytes, _ptr(flags), _stream(stream)))
+
+
+def linear_attn_seqs(q_start, slots, max_q: int, fresh=None, n_seq: int | None = None) -> Linear:
+    """The sequences of a linear attention call: q_start int32 [n_seq + 1], slots int32 [n_seq] (each one's state, -1:
+    none), fresh int32 [n_seq] (not 0: begin with zeros) or None."""
+    s = Linear(n_seq=slots.numel() if n_seq is None else n_seq, max_q=max_q, q_start=_ptr(q_start), slots=_ptr(slots),
+               fresh=_ptr(fresh))
+    s._owners = (q_start, slots, fresh)
+    return s
+
+
+def _linear(seqs: Linear, k_heads: int, v_heads: int, dk: int, dv: int, n_slots: int) -> Linear:
+    return Linear(k_heads, v_heads, dk, dv, seqs.n_seq, seqs.max_q, n_slots, seqs.q_start, seqs.slots, seqs.fresh)
+
+
+def linear_attn_ws(seqs: Linear, k_heads: int, v_heads: int, dk: int, dv: int, M: int) -> int:
+    """Workspace bytes of linear_attn (0 = bad arguments)."""
+    return int(_lib.q4nx_linear_attn_ws(ctypes.byref(_linear(seqs, k_heads, v_heads, dk, dv, 1)), M))
+
+
+def linear_attn(seqs: Linear, q, k, v, decay, k_heads: int, v_heads: int, dk: int, dv: int, M: int, scale: float, state,
+                out, ws, state_out=None, flags=None, stream=None, n_slots: int | None = None, q_ld: int | None = None,
+                k_ld: int | None = None, v_ld: int | None = None, decay_ld: int | None = None,
+                ws_bytes: int | None = None) -> None:
+    """S = exp(decay) S + k v^T, out[M, v_heads, dv] (fp32) = scale q^T S, row by row of each sequence, from state[n_slots,
+    v_heads, dk, dv] (fp32) into state_out (None: state itself).  Row strides come from tensors of two or three dimensions;
+    a decay of one dimension is every token's."""
+    def step(t, ld, columns, width):
+        if ld is not None:
+            return ld
+        if isinstance(t, int) or t.dim() < 2:
+            return columns
+        if t.stride(-1) != 1 or (t.dim() == 3 and t.stride(1) != width):
+            raise Q4nxError(E_SHAPE, "linear_attn: the columns of a row must be contiguous")
+        return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), columns)
+    if decay_ld is None:
+        decay_ld = 0 if not isinstance(decay, int) and decay.dim() == 1 else step(decay, None, v_heads, 1)
+    if n_slots is None:
+        n_slots = state.numel() // (v_heads * dk * dv)
+    L = _linear(seqs, k_heads, v_heads, dk, dv, n_slots)
+    _check(_lib.q4nx_linear_attn(ctypes.byref(L), _ptr(q), step(q, q_ld, k_heads * dk, dk), _ptr(k),
+                                 step(k, k_ld, k_heads * dk, dk), _ptr(v), step(v, v_ld, v_heads * dv, dv), _ptr(decay),
+                                 decay_ld, M, scale, _ptr(state), _ptr(state if state_out is None else state_out), _ptr(out),
+                                 _ptr(ws), _nbytes(ws) if ws_bytes is None else ws_bytes, _ptr(flags), _stream(stream)))
 
 
 def unpack(w: Weight, codes, meta0, meta1=None, row_meta=None, stream=None) -> None:

@@ -19,6 +19,7 @@
 
 #include "../../include/q4nx.h"
 #include "gemm_args.h"
+#include "kv_args.h"
 #include "logprobs_args.h"
 #include "lora_args.h"
 #include "moe_args.h"
@@ -28,6 +29,7 @@
 
 static_assert(Q4NX_GEMM_BATCH_MAX_JOBS == q4nx::kGemmMaxJobs, "GEMM job table size");
 static_assert(Q4NX_LORA_BATCH_MAX_JOBS == q4nx::kLoraMaxJobs, "adapter job table size");
+static_assert(Q4NX_ATTN_MAX_SEQ == q4nx::kAttnMaxSeq, "sequences of one attention call");
 static_assert(Q4NX_LORA_MAX_M == q4nx::kLoraMaxRows, "adapter rows of one call");
 
 namespace {
@@ -1661,6 +1663,351 @@ int q4nx_token_logprobs(const float* y, int n, int ldy, int M, const int32_t* to
   a.stats = reinterpret_cast<q4nx::f32x4*>(wsb + lay.stats);
   a.keys = reinterpret_cast<uint64_t*>(wsb + lay.keys);
   return hip_status(q4nx::launch_token_logprobs(a, static_cast<hipStream_t>(stream)), "token_logprobs launch");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// the cache, attention, linear attention
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_cache(const q4nx_kv_cache* c, const char* name, bool pointers) {
+  if (!c) return fail(Q4NX_E_ARG, "%s: null cache", name);
+  if (c->kv_heads < 1 || c->kv_heads > 256) return fail(Q4NX_E_ARG, "%s: kv_heads = %d outside 1..256", name, c->kv_heads);
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return fail(Q4NX_E_SHAPE, "%s: head_dim = %d is not 64, 128 or 256", name, c->head_dim);
+  if (c->page_tokens < 16 || c->page_tokens > 1024 || (c->page_tokens & (c->page_tokens - 1)))
+    return fail(Q4NX_E_SHAPE, "%s: page_tokens = %d is not a power of two in 16..1024", name, c->page_tokens);
+  if (c->n_pages < 1 || (int64_t)c->n_pages * c->page_tokens > INT32_MAX)
+    return fail(Q4NX_E_ARG, "%s: n_pages = %d (1 at least, 2^31 - 1 tokens at most)", name, c->n_pages);
+  if (c->type != Q4NX_KV_BF16 && c->type != Q4NX_KV_INT8)
+    return fail(Q4NX_E_ARG, "%s: cache type %d is not bf16 or int8", name, c->type);
+  if (!pointers) return Q4NX_OK;
+  const bool i8 = c->type == Q4NX_KV_INT8;
+  if (!c->k || !c->v) return fail(Q4NX_E_ARG, "%s: null k or v pages", name);
+  if (i8 != (c->k_scale != nullptr) || i8 != (c->v_scale != nullptr))
+    return fail(Q4NX_E_ARG, "%s: an int8 cache has k_scale and v_scale, a bf16 cache neither", name);
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
+    return fail(Q4NX_E_ALIGN, "%s: pages and scales must be 16-byte aligned", name);
+  const int64_t tokens = (int64_t)c->n_pages * c->page_tokens * c->kv_heads;
+  const int64_t need = tokens * c->head_dim * (i8 ? 1 : 2);
+  if (c->k_bytes < need || c->v_bytes < need)
+    return fail(Q4NX_E_SHORT, "%s: pages of %lld and %lld bytes, %lld needed", name, (long long)c->k_bytes,
+                (long long)c->v_bytes, (long long)need);
+  if (i8 && (c->k_scale_bytes < tokens * 4 || c->v_scale_bytes < tokens * 4))
+    return fail(Q4NX_E_SHORT, "%s: scales of %lld and %lld bytes, %lld needed", name, (long long)c->k_scale_bytes,
+                (long long)c->v_scale_bytes, (long long)tokens * 4);
+  return Q4NX_OK;
+}
+
+struct Span { const void* p; uint64_t bytes; };
+
+bool overlap(const Span& x, const Span& y) { return x.p && y.p && x.bytes && y.bytes && overlap(x.p, x.bytes, y.p, y.bytes); }
+
+// Whether two of the first `outs` of the spans, or one of them and another, share a byte.
+template <size_t N>
+bool outputs_overlap(const Span (&part)[N], size_t outs) {
+  for (size_t i = 0; i < outs; ++i)
+    for (size_t j = i + 1; j < N; ++j)
+      if (overlap(part[i], part[j])) return true;
+  return false;
+}
+
+// The four arrays of a checked cache.
+void cache_spans(const q4nx_kv_cache* c, Span* s) {
+  const uint64_t tokens = (uint64_t)c->n_pages * c->page_tokens * c->kv_heads;
+  const uint64_t bytes = tokens * c->head_dim * (c->type == Q4NX_KV_INT8 ? 1 : 2);
+  s[0] = {c->k, bytes};
+  s[1] = {c->v, bytes};
+  s[2] = {c->k_scale, tokens * 4};
+  s[3] = {c->v_scale, tokens * 4};
+}
+
+q4nx::KvCache device_cache(const q4nx_kv_cache* c) {
+  q4nx::KvCache d;
+  d.k = c->k;
+  d.v = c->v;
+  d.ks = c->k_scale;
+  d.vs = c->v_scale;
+  d.heads = c->kv_heads;
+  d.dim = c->head_dim;
+  d.page_shift = __builtin_ctz((unsigned)c->page_tokens);
+  d.n_pages = c->n_pages;
+  return d;
+}
+
+int check_heads(const q4nx_heads* h, const char* name, int dim, int heads) {
+  if (!h || !h->p) return fail(Q4NX_E_ARG, "kv_append: null %s", name);
+  if (h->type != Q4NX_F32 && h->type != Q4NX_BF16) return fail(Q4NX_E_ARG, "kv_append: type %d of %s", h->type, name);
+  if (heads && h->heads != heads) return fail(Q4NX_E_SHAPE, "kv_append: %s has %d heads, the cache %d", name, h->heads, heads);
+  if (h->heads < 1 || (int64_t)h->heads * dim > 16384)
+    return fail(Q4NX_E_SHAPE, "kv_append: %d heads of %s (1 at least, 16384 columns at most)", h->heads, name);
+  if (h->ld < (int64_t)h->heads * dim || h->ld > (int64_t)1 << 40)
+    return fail(Q4NX_E_SHAPE, "kv_append: ld %lld of %s below its %d columns, or too large", (long long)h->ld, name, h->heads * dim);
+  if (!aligned(h->p, h->type == Q4NX_F32 ? 4 : 2)) return fail(Q4NX_E_ALIGN, "kv_append: %s is not aligned to its element", name);
+  return Q4NX_OK;
+}
+
+Span heads_span(const q4nx_heads* h, int dim, int M) {
+  if (!h) return {nullptr, 0};
+  return {h->p, ((uint64_t)(M - 1) * h->ld + (uint64_t)h->heads * dim) * (h->type == Q4NX_F32 ? 4 : 2)};
+}
+
+q4nx::HeadRows device_heads(const q4nx_heads* h) {
+  if (!h) return {nullptr, 0, 0, 0};
+  return {h->p, h->ld, h->heads, h->type == Q4NX_BF16};
+}
+
+// How one q4nx_attention runs: the kernels of its sequences and, where several
+// sequences share a prefix, of the prefix; and where their parts lie.
+struct AttnShape {
+  q4nx::AttnParts own, pre;   // pre.rows = 0: the prefix comes with each sequence's own keys
+  int own_grid, pre_grid;
+  size_t own_plan, own_o, own_ml, pre_plan, pre_o, pre_ml, total;
+};
+
+void attn_shape(const q4nx_kv_cache* c, const q4nx_attn_batch* b, int q_heads, int M, AttnShape& sh) {
+  memset(&sh, 0, sizeof sh);
+  const int KH = c->kv_heads, group = q_heads / KH;
+  const int64_t rows = (int64_t)M * group;
+  const bool apart = b->prefix_len > 0 && b->n_seq > 1;
+  auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+  size_t o = 0;
+  auto place = [&](q4nx::AttnParts& p, int set, int& grid, size_t& plan, size_t& po, size_t& ml) {
+    p.set = set;
+    p.rows = 16;
+    p.target = 2048;
+    const int64_t parts = q4nx::attn_max_parts(set, b->n_seq, rows, KH, p.rows, p.target);
+    grid = (int)std::min<int64_t>(parts, 1024);
+    plan = o;
+    o = up(o + (2 + 2 * (size_t)q4nx::attn_entries(set, b->n_seq)) * 4);
+    po = o;
+    o = up(o + (size_t)parts * p.rows * c->head_dim * 4);
+    ml = o;
+    o = up(o + (size_t)parts * p.rows * 8);
+  };
+  place(sh.own, apart ? q4nx::ATTN_OWN : q4nx::ATTN_ALL, sh.own_grid, sh.own_plan, sh.own_o, sh.own_ml);
+  if (apart) place(sh.pre, q4nx::ATTN_PREFIX, sh.pre_grid, sh.pre_plan, sh.pre_o, sh.pre_ml);
+  sh.total = o;
+}
+
+int check_attn(const q4nx_kv_cache* c, const q4nx_attn_batch* b, int q_heads, int M, bool pointers) {
+  const int st = check_cache(c, "attention", pointers);
+  if (st) return st;
+  if (!b) return fail(Q4NX_E_ARG, "attention: null batch");
+  if (b->n_seq < 1 || b->n_seq > Q4NX_ATTN_MAX_SEQ)
+    return fail(Q4NX_E_ARG, "attention: n_seq = %d outside 1..%d", b->n_seq, (int)Q4NX_ATTN_MAX_SEQ);
+  if (M < 1 || M > Q4NX_ATTN_MAX_M) return fail(Q4NX_E_ARG, "attention: M = %d outside 1..%d", M, (int)Q4NX_ATTN_MAX_M);
+  if (b->max_q < 1 || b->max_q > Q4NX_ATTN_MAX_M) return fail(Q4NX_E_ARG, "attention: max_q = %d", b->max_q);
+  if (q_heads < 1 || q_heads % c->kv_heads || (int64_t)q_heads * c->head_dim > 16384)
+    return fail(Q4NX_E_SHAPE, "attention: %d query heads over %d of %d columns (a multiple, 16384 columns at most)",
+                q_heads, c->kv_heads, c->head_dim);
+  if (b->pages_ld < 1) return fail(Q4NX_E_ARG, "attention: pages_ld = %d", b->pages_ld);
+  if (b->prefix_len < 0 || (int64_t)b->prefix_len + (int64_t)b->pages_ld * c->page_tokens > INT32_MAX - 1024)
+    return fail(Q4NX_E_ARG, "attention: a prefix of %d tokens before %d pages (2^31 - 1024 tokens at most)", b->prefix_len,
+                b->pages_ld);
+  return Q4NX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int q4nx_kv_append(const q4nx_kv_cache* cache, const q4nx_rope* rope, const q4nx_heads* q, uint16_t* q_out,
+                   const q4nx_heads* k, const q4nx_heads* v, const int32_t* slots, int M, uint32_t* flags,
+                   void* stream) {
+  int st = check_cache(cache, "kv_append", true);
+  if (st) return st;
+  const int D = cache->head_dim;
+  if (M < 1 || M > Q4NX_KV_MAX_M) return fail(Q4NX_E_ARG, "kv_append: M = %d outside 1..%d", M, (int)Q4NX_KV_MAX_M);
+  if (q && !q->p) q = nullptr;
+  if ((q != nullptr) != (q_out != nullptr)) return fail(Q4NX_E_ARG, "kv_append: q without q_out, or q_out without q");
+  if (q && (st = check_heads(q, "q", D, 0))) return st;
+  if ((st = check_heads(k, "k", D, cache->kv_heads)) || (st = check_heads(v, "v", D, cache->kv_heads))) return st;
+  if (!slots) return fail(Q4NX_E_ARG, "kv_append: null slots");
+  if (!aligned(slots, 4) || !aligned(flags, 4) || !aligned(q_out, 16))
+    return fail(Q4NX_E_ALIGN, "kv_append: slots and flags must be 4-byte, q_out 16-byte aligned");
+  if (rope) {
+    if (!rope->inv_freq || !rope->pos) return fail(Q4NX_E_ARG, "kv_append: null inv_freq or pos");
+    if (rope->dim < 16 || rope->dim % 16 || rope->dim > D)
+      return fail(Q4NX_E_SHAPE, "kv_append: rope over %d dimensions is not a multiple of 16 in 16..%d", rope->dim, D);
+    if (!aligned(rope->inv_freq, 4) || !aligned(rope->pos, 4))
+      return fail(Q4NX_E_ALIGN, "kv_append: inv_freq and pos must be 4-byte aligned");
+  }
+  Span part[13] = {{q_out, q ? (uint64_t)M * q->heads * D * 2 : 0}};
+  cache_spans(cache, part + 1);
+  part[5] = {flags, 4};
+  part[6] = heads_span(q, D, M);
+  part[7] = heads_span(k, D, M);
+  part[8] = heads_span(v, D, M);
+  part[9] = {slots, (uint64_t)M * 4};
+  if (rope) {
+    part[10] = {rope->pos, (uint64_t)M * 4};
+    part[11] = {rope->inv_freq, (uint64_t)rope->dim * 2};
+  }
+  if (outputs_overlap(part, 6)) return fail(Q4NX_E_ARG, "kv_append: q_out, the cache or flags overlap another array");
+  q4nx::AppendArgs a;
+  memset(&a, 0, sizeof a);
+  a.c = device_cache(cache);
+  a.q = device_heads(q);
+  a.k = device_heads(k);
+  a.v = device_heads(v);
+  a.q_out = q_out;
+  a.slots = slots;
+  a.flags = flags;
+  a.M = M;
+  if (rope) {
+    a.inv_freq = rope->inv_freq;
+    a.pos = rope->pos;
+    a.rot = rope->dim;
+    a.interleaved = rope->interleaved != 0;
+  }
+  // about a thousand workgroups: up to eight tokens each where there are many,
+  // one token's heads over several where there are few
+  a.tile = std::max(1, std::min(q4nx::kAppendTile, M / 512));
+  const int tiles = (M + a.tile - 1) / a.tile, heads = a.q.heads + 2 * a.c.heads;
+  const int head_parts = std::min((a.tile * heads * D / 8 + 255) / 256, std::max(1, 1024 / tiles));
+  return hip_status(q4nx::launch_kv_append(a, head_parts, static_cast<hipStream_t>(stream)), "kv_append launch");
+}
+
+size_t q4nx_attention_ws(const q4nx_kv_cache* cache, const q4nx_attn_batch* batch, int q_heads, int M) {
+  if (check_attn(cache, batch, q_heads, M, false)) return 0;
+  AttnShape sh;
+  attn_shape(cache, batch, q_heads, M, sh);
+  return sh.total;
+}
+
+int q4nx_attention(const q4nx_kv_cache* cache, const q4nx_attn_batch* batch, const uint16_t* q, int q_heads, int M,
+                   float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes, uint32_t* flags, void* stream) {
+  const int st = check_attn(cache, batch, q_heads, M, true);
+  if (st) return st;
+  const q4nx_attn_batch& b = *batch;
+  if (!q || !out) return fail(Q4NX_E_ARG, "attention: null q or out");
+  if (!b.q_start || !b.kv_len || !b.pages || (b.prefix_len && !b.prefix_pages))
+    return fail(Q4NX_E_ARG, "attention: null q_start, kv_len, pages or prefix_pages");
+  if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return fail(Q4NX_E_ARG, "attention: scale = %g is not finite", scale);
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(flags, 4) || !aligned(b.q_start, 4) ||
+      !aligned(b.kv_len, 4) || !aligned(b.pages, 4) || !aligned(b.prefix_pages, 4))
+    return fail(Q4NX_E_ALIGN, "attention: q and out must be 16-byte, every other array 4-byte aligned");
+  const uint64_t bytes = (uint64_t)M * q_heads * cache->head_dim * 2;
+  AttnShape sh;
+  attn_shape(cache, batch, q_heads, M, sh);
+  if (!ws || ws_bytes < sh.total)
+    return fail(Q4NX_E_WORKSPACE, "attention: workspace of %zu bytes, %zu needed", ws_bytes, sh.total);
+  if (!aligned(ws, 256)) return fail(Q4NX_E_ALIGN, "attention: workspace not 256-byte aligned");
+  Span part[13] = {{out, bytes}, {lse, (uint64_t)M * q_heads * 4}, {ws, sh.total}, {flags, 4}, {q, bytes}};
+  part[5] = {b.q_start, ((uint64_t)b.n_seq + 1) * 4};
+  part[6] = {b.kv_len, (uint64_t)b.n_seq * 4};
+  part[7] = {b.pages, (uint64_t)b.n_seq * b.pages_ld * 4};
+  part[8] = {b.prefix_len ? b.prefix_pages : nullptr, ((uint64_t)b.prefix_len + cache->page_tokens - 1) / cache->page_tokens * 4};
+  cache_spans(cache, part + 9);
+  if (outputs_overlap(part, 4))
+    return fail(Q4NX_E_ARG, "attention: out, lse, the workspace or flags overlap another array");
+  q4nx::AttnArgs a;
+  memset(&a, 0, sizeof a);
+  a.c = device_cache(cache);
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.q_start = b.q_start;
+  a.kv_len = b.kv_len;
+  a.pages = b.pages;
+  a.prefix_pages = b.prefix_pages;
+  a.flags = flags;
+  a.n_seq = b.n_seq;
+  a.M = M;
+  a.q_heads = q_heads;
+  a.group = q_heads / cache->kv_heads;
+  a.pages_ld = b.pages_ld;
+  a.prefix_len = b.prefix_len;
+  a.scale = scale * 1.4426950408889634f;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  auto at = [&](q4nx::AttnParts& p, size_t plan, size_t o, size_t ml) {
+    p.plan = reinterpret_cast<int32_t*>(w + plan);
+    p.o = reinterpret_cast<float*>(w + o);
+    p.ml = reinterpret_cast<float*>(w + ml);
+  };
+  at(sh.own, sh.own_plan, sh.own_o, sh.own_ml);
+  if (sh.pre.rows) at(sh.pre, sh.pre_plan, sh.pre_o, sh.pre_ml);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = q4nx::launch_attn_few(a, sh.own, sh.own_grid, s);
+  if (e == hipSuccess && sh.pre.rows) e = q4nx::launch_attn_few(a, sh.pre, sh.pre_grid, s);
+  if (e == hipSuccess) e = q4nx::launch_attn_join(a, sh.own, sh.pre, s);
+  return hip_status(e, "attention launch");
+}
+
+size_t q4nx_linear_attn_ws(const q4nx_linear* L, int M) {
+  if (!L || M < 1 || M > Q4NX_ATTN_MAX_M) return 0;
+  return 256;
+}
+
+int q4nx_linear_attn(const q4nx_linear* L, const uint16_t* q, int64_t q_ld, const uint16_t* k, int64_t k_ld,
+                     const uint16_t* v, int64_t v_ld, const float* decay, int64_t decay_ld, int M, float scale,
+                     const float* state, float* state_out, float* out, void* ws, size_t ws_bytes, uint32_t* flags,
+                     void* stream) {
+  if (!L) return fail(Q4NX_E_ARG, "linear_attn: null descriptor");
+  if (!q || !k || !v || !decay || !state || !state_out || !out) return fail(Q4NX_E_ARG, "linear_attn: null array");
+  if (!L->q_start || !L->slots) return fail(Q4NX_E_ARG, "linear_attn: null q_start or slots");
+  if (L->n_seq < 1 || L->n_seq > Q4NX_ATTN_MAX_SEQ || L->max_q < 1 || L->max_q > Q4NX_ATTN_MAX_M || L->n_slots < 1 ||
+      L->n_slots > (1 << 20))
+    return fail(Q4NX_E_ARG, "linear_attn: n_seq = %d, max_q = %d, n_slots = %d (1..%d, 1..%d, 1..1048576)", L->n_seq, L->max_q,
+                L->n_slots, (int)Q4NX_ATTN_MAX_SEQ, (int)Q4NX_ATTN_MAX_M);
+  if (M < 1 || M > Q4NX_ATTN_MAX_M) return fail(Q4NX_E_ARG, "linear_attn: M = %d outside 1..%d", M, (int)Q4NX_ATTN_MAX_M);
+  if (L->k_heads < 1 || L->k_heads > 256 || L->v_heads < 1 || L->v_heads > 1024 || L->v_heads % L->k_heads)
+    return fail(Q4NX_E_SHAPE, "linear_attn: %d key and %d value heads (1..256, a multiple of them up to 1024)", L->k_heads,
+                L->v_heads);
+  if ((L->dk != 64 && L->dk != 128) || (L->dv != 64 && L->dv != 128))
+    return fail(Q4NX_E_SHAPE, "linear_attn: dk = %d, dv = %d are not 64 or 128 each", L->dk, L->dv);
+  const int64_t kc = (int64_t)L->k_heads * L->dk, vc = (int64_t)L->v_heads * L->dv, most = (int64_t)1 << 40;
+  if (q_ld < kc || k_ld < kc || v_ld < vc || q_ld > most || k_ld > most || v_ld > most)
+    return fail(Q4NX_E_SHAPE, "linear_attn: row strides %lld, %lld, %lld below %lld, %lld, %lld columns, or too large",
+                (long long)q_ld, (long long)k_ld, (long long)v_ld, (long long)kc, (long long)kc, (long long)vc);
+  if (decay_ld != 0 && (decay_ld < L->v_heads || decay_ld > most))
+    return fail(Q4NX_E_SHAPE, "linear_attn: decay_ld %lld is neither 0 nor at least %d", (long long)decay_ld, L->v_heads);
+  if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return fail(Q4NX_E_ARG, "linear_attn: scale = %g is not finite", scale);
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || q_ld % 8 || k_ld % 8 || v_ld % 8 || !aligned(state, 16) ||
+      !aligned(state_out, 16) || !aligned(out, 16))
+    return fail(Q4NX_E_ALIGN, "linear_attn: q, k, v, the states and out must be 16-byte aligned, strides multiples of 8");
+  if (!aligned(decay, 4) || !aligned(L->q_start, 4) || !aligned(L->slots, 4) || !aligned(L->fresh, 4) || !aligned(flags, 4))
+    return fail(Q4NX_E_ALIGN, "linear_attn: decay, q_start, slots, fresh and flags must be 4-byte aligned");
+  const size_t need = q4nx_linear_attn_ws(L, M);
+  if (!ws || ws_bytes < need) return fail(Q4NX_E_WORKSPACE, "linear_attn: workspace of %zu bytes, %zu needed", ws_bytes, need);
+  if (!aligned(ws, 256)) return fail(Q4NX_E_ALIGN, "linear_attn: workspace not 256-byte aligned");
+  const uint64_t sb = (uint64_t)L->n_slots * L->v_heads * L->dk * L->dv * 4, r = (uint64_t)M - 1;
+  const Span part[] = {{out, (uint64_t)M * vc * 4}, {state_out, sb}, {ws, need}, {flags, 4},
+                       {state_out == state ? nullptr : state, sb}, {q, (r * q_ld + kc) * 2}, {k, (r * k_ld + kc) * 2},
+                       {v, (r * v_ld + vc) * 2}, {decay, (r * decay_ld + L->v_heads) * 4},
+                       {L->q_start, ((uint64_t)L->n_seq + 1) * 4}, {L->slots, (uint64_t)L->n_seq * 4},
+                       {L->fresh, (uint64_t)L->n_seq * 4}};
+  if (outputs_overlap(part, 4))
+    return fail(Q4NX_E_ARG, "linear_attn: out, state_out, the workspace or flags overlap another array");
+  q4nx::LinearArgs a;
+  memset(&a, 0, sizeof a);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_ld = q_ld;
+  a.k_ld = k_ld;
+  a.v_ld = v_ld;
+  a.decay = decay;
+  a.decay_ld = decay_ld;
+  a.state = state;
+  a.state_out = state_out;
+  a.out = out;
+  a.q_start = L->q_start;
+  a.slots = L->slots;
+  a.fresh = L->fresh;
+  a.flags = flags;
+  a.k_heads = L->k_heads;
+  a.v_heads = L->v_heads;
+  a.dk = L->dk;
+  a.dv = L->dv;
+  a.n_seq = L->n_seq;
+  a.n_slots = L->n_slots;
+  a.M = M;
+  a.scale = scale;
+  return hip_status(q4nx::launch_linear_rows(a, static_cast<hipStream_t>(stream)), "linear_attn launch");
 }
 
 int q4nx_decode(const q4nx_weight* w, float* out, void* stream) {

@@ -1,0 +1,321 @@
+// Attention over the paged cache, and the join of its parts.
+//
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(z_j - max z),  z_j = scale log2(e) q.k_j
+//
+// Both products run transposed, S^T = K Q^T and O^T = V^T P^T, on matrix
+// instructions of 16 x 16: a lane then holds scores of one row only (its
+// column), so that the running maximum and the rescaling need no exchange but
+// one over the four lanes of a column, and P^T is already in the order in which
+// the second product takes it.  Which key stands in which line of S^T is free:
+// lines are dealt so that a lane's eight scores belong to eight neighbouring
+// tokens, which is what one 16-byte piece of the cache's values holds.  So K and
+// V go from memory to the matrix cores as they lie, in whole lines.
+#include <algorithm>
+
+#include "attn_core.h"
+
+namespace q4nx {
+
+namespace {
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Eight elements of the cache.
+template <bool I8>
+__device__ __forceinline__ bf16x8 cache8(const void* p, size_t at) {
+  if constexpr (I8) return bf16x8_of_codes(*reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(p) + at));
+  else return *reinterpret_cast<const bf16x8*>(static_cast<const uint16_t*>(p) + at);
+}
+
+// Four dimensions of a row and head, from d.  A sum of 0 is that of a row that
+// sees nothing (any other has its largest term, 1, or a NaN).
+__device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, int D, int d, f32x4 o, float m, float l) {
+  const bool none = l == 0.f;
+  const float inv = none ? 0.f : 1.f / l;
+  uint32_t w[2];
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    bf16x2 v;
+    v[0] = (__bf16)(o[2 * n] * inv);
+    v[1] = (__bf16)(o[2 * n + 1] * inv);
+    w[n] = __builtin_bit_cast(uint32_t, v);
+  }
+  *reinterpret_cast<u32x2*>(a.out + row * D + d) = u32x2{w[0], w[1]};
+  if (a.lse && d == 0) a.lse[row] = none ? kNegInf : m * 0.6931471805599453f + logf(l);
+}
+
+}  // namespace
+
+// Few rows (up to 16 a tile): a sequence's one row, or a window's, with the
+// query heads of one key head.  The workgroup's four waves take 32 keys each of
+// a unit of 128, with maxima, sums and outputs of their own that are joined at
+// the end, so that a unit's K and V are read once, straight into registers.
+// Bound by memory.
+template <int D, bool I8>
+__global__ __launch_bounds__(256) void k_attn_few(AttnArgs a, AttnParts p) {
+  constexpr int kRows = 16, NS = D / 32, NJ = D / 16, kLd = D + 4;
+  __shared__ AttnPlan plan;
+  __shared__ float s_m[4][kRows], s_l[4][kRows];
+  extern __shared__ __align__(16) float s_o[];   // [4][kRows][kLd]
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c = lane & 15, g = lane >> 4;
+  const int total = attn_plan(a, p, plan), entries = p.set == ATTN_PREFIX ? 1 : a.n_seq;
+  const int KH = a.c.heads;
+  for (int idx = blockIdx.x; idx < total * KH; idx += gridDim.x) {
+    const int head = idx % KH, it = idx / KH;
+    const int e = attn_find(plan, entries, it);
+    const AttnEntry x = attn_entry(a, plan.start, p.set, kRows, e);
+    const int split = max(1, (x.units + plan.per - 1) / plan.per), local = it - plan.first[e];
+    const int part = local % split, rt = local / split;
+    // the lane's row
+    const int r = min(rt * kRows + c, x.rows - 1), r_last = min(rt * kRows + kRows, x.rows) - 1;
+    const int i = r / a.group, h = head * a.group + r % a.group;
+    auto seen = [&](int row) { return min(max(x.causal + row / a.group + 1, 0), x.own); };
+    const int lim_own = seen(r), lim_first = seen(rt * kRows), lim_last = seen(r_last);
+    const int pre_units = attn_units(x.pre), units = pre_units + attn_units(lim_last);
+    const int per = (units + split - 1) / split, u0 = part * per, u1 = min(units, u0 + per);
+    bf16x8 qf[NS];
+    const uint16_t* qp = a.q + ((size_t)(x.row0 + i) * a.q_heads + h) * D + 8 * g;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) qf[s] = *reinterpret_cast<const bf16x8*>(qp + 32 * s);
+
+    f32x4 acc[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m_run = kNegInf, l_run = 0.f;
+    const int32_t* own_pages = p.set == ATTN_PREFIX ? nullptr : a.pages + (size_t)e * a.pages_ld;
+    for (int u = u0; u < u1; ++u) {
+      const bool pre = u < pre_units;
+      const int key0 = (pre ? u : u - pre_units) * kAttnUnit + 32 * wave;
+      const int have = pre ? x.pre : lim_last;   // keys from here on are no row's
+      if (key0 >= have) continue;
+      const int32_t* table = pre ? a.prefix_pages : own_pages;
+      const int ps = a.c.page_shift;
+      // the 16 tokens of each half: their page, and the lane's 8 keys' half
+      size_t at0, at1;
+      const bool ok0 = attn_page(a.c, a.flags, table[key0 >> ps], head, at0);
+      bool ok1 = false;   // a half of no keys reads what is there of the first one's page
+      if (key0 + 16 >= have) at1 = at0;
+      else ok1 = attn_page(a.c, a.flags, table[(key0 + 16) >> ps], head, at1);
+      const int t0 = key0 & ((1 << ps) - 1), t1 = (key0 + 16) & ((1 << ps) - 1);
+      // keys: line c of block b holds token 8 (c / 4) + 4 b + c % 4, in half c / 8
+      const size_t kb = (c & 8 ? at1 + (size_t)t1 * D : at0 + (size_t)t0 * D) + g * 128 +
+                        ((8 * (c >> 2) + (c & 3)) & 15) * 8;
+      const size_t vb = (g & 2 ? at1 + (size_t)t1 * D : at0 + (size_t)t0 * D) +
+                        (size_t)(g & 1) * 8 * D + c * 8;
+      f32x4 st[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+      bf16x8 vf[NJ];
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          st[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cache8<I8>(a.c.k, kb + s * 512 + b * 32), qf[s], st[b], 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) vf[j] = cache8<I8>(a.c.v, vb + j * 128);
+      float z[8], vs[8];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) z[n] = st[n >> 2][n & 3] * a.scale;
+      if constexpr (I8) {
+        const size_t sb = (g & 2 ? at1 / D + t1 : at0 / D + t0) + (g & 1) * 8;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          z[n] *= a.c.ks[sb + n];
+          vs[n] = a.c.vs[sb + n];
+        }
+      }
+      const int mine = key0 + 8 * g;   // the lane's first key
+      const bool ok = g & 2 ? ok1 : ok0;
+      if (key0 + 32 > (pre ? x.pre : lim_first) || !ok0 || !ok1) {
+        const int lim = ok ? (pre ? x.pre : lim_own) - mine : 0, there = ok ? have - mine : 0;
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+          if (n >= lim) z[n] = kNegInf;
+        if constexpr (!I8) {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) vf[j] = keep_first(vf[j], there);
+          // an infinity or NaN that only some of the rows see is kept out of the product, which has a 0
+          // for the others, and added to those rows
+          if (!pre && lim_first < lim_last) {
+            bool any = false;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) any |= drop_nonfinite(vf[j]);
+            if (__ballot(any)) {
+              for (int n = 0; n < 32 && key0 + n < have; ++n) {
+                const bool half = n & 16;
+                if (!(half ? ok1 : ok0)) continue;
+                const uint16_t* vp = static_cast<const uint16_t*>(a.c.v) + (half ? at1 : at0);
+                const int tok = half ? t1 + (n & 15) : t0 + n;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                  for (int d = 0; d < 4; ++d) {
+                    const float v = bf16lo(vp[v_place(D, tok, 16 * j + 4 * g + d)]);
+                    if (!(fabsf(v) <= __FLT_MAX__) && key0 + n < lim_own) acc[j][d] += v;
+                  }
+              }
+            }
+          }
+        }
+      }
+      float top = z[0];
+#pragma unroll
+      for (int n = 1; n < 8; ++n) top = fmaxf(top, z[n]);
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float m_new = fmaxf(m_run, top), base = m_new == kNegInf ? 0.f : m_new;
+      const float alpha = __builtin_amdgcn_exp2f(m_run - base);
+      m_run = m_new;
+      float pr[8], sum = 0.f;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        pr[n] = __builtin_amdgcn_exp2f(z[n] - base);
+        sum += pr[n];
+        if constexpr (I8) pr[n] = z[n] == kNegInf ? 0.f : pr[n] * vs[n];
+      }
+      l_run = l_run * alpha + sum;
+      const bf16x8 pf = bf16x8_of(pr);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        acc[j] *= alpha;
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[j], pf, acc[j], 0, 0, 0);
+      }
+    }
+    // the four waves' parts become one
+    l_run += __shfl_xor(l_run, 16);
+    l_run += __shfl_xor(l_run, 32);
+    __syncthreads();   // the item before has been read
+    if (g == 0) s_m[wave][c] = m_run;
+    __syncthreads();
+    float m_all = s_m[0][c];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) m_all = fmaxf(m_all, s_m[w][c]);
+    const float f = m_all == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m_run - m_all);
+    if (g == 0) s_l[wave][c] = l_run * f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      *reinterpret_cast<f32x4*>(&s_o[(wave * kRows + c) * kLd + 16 * j + 4 * g]) = acc[j] * f;
+    __syncthreads();
+    const bool whole = split == 1 && p.set == ATTN_ALL;
+    const size_t slot = (size_t)it * KH + head;
+    for (int q4 = tid; q4 < kRows * (D / 4); q4 += 256) {
+      const int row = q4 / (D / 4), d = 4 * (q4 % (D / 4)), rr = rt * kRows + row;
+      if (rr >= x.rows) continue;
+      f32x4 o = *reinterpret_cast<const f32x4*>(&s_o[row * kLd + d]);
+      float l = s_l[0][row], m = s_m[0][row];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) {
+        o += *reinterpret_cast<const f32x4*>(&s_o[(w * kRows + row) * kLd + d]);
+        l += s_l[w][row];
+        m = fmaxf(m, s_m[w][row]);
+      }
+      if (whole) {
+        const int qrow = x.row0 + rr / a.group, qh = head * a.group + rr % a.group;
+        write_row(a, ((size_t)qrow * a.q_heads + qh), D, d, o, m, l);
+      } else {
+        *reinterpret_cast<f32x4*>(p.o + (slot * kRows + row) * D + d) = o;
+        if (d == 0) {
+          p.ml[(slot * kRows + row) * 2] = m;
+          p.ml[(slot * kRows + row) * 2 + 1] = l;
+        }
+      }
+    }
+  }
+}
+
+// The parts of one row and head, joined in order.  32 * D / 128 lanes have four
+// dimensions each; the rest of the workgroup shares the parts.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, AttnParts own, AttnParts pre) {
+  constexpr int L = D / 4, kGroups = 256 / L;
+  __shared__ float s_o[kGroups][D + 4];
+  __shared__ float s_l[kGroups];
+  const int m = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+  // the row's sequence; starts that fall count as the largest before them
+  int seq = -1, begin = 0, row0 = 0;
+  {
+    int up = 0, before = 0;
+    for (int b = 0; b <= a.n_seq; b += 64) {
+      const int e = b + lane;
+      int v = e <= a.n_seq ? min(max(a.q_start[e], 0), a.M) : 0;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(v, off);
+        if (lane >= off) v = max(v, o);
+      }
+      v = max(v, up);
+      if (b == 0) row0 = __shfl(v, 0);
+      const uint64_t at = __ballot(e <= a.n_seq && v <= m);
+      const int n = __popcll(at);
+      if (n) begin = __shfl(v, n - 1);
+      before += n;
+      up = __shfl(v, 63);
+      if (b + 63 <= a.n_seq && n < 64) break;
+    }
+    seq = before - 1;
+  }
+  if (seq < 0 || seq >= a.n_seq) return;   // no sequence's row
+  const int i = m - begin, KH = a.c.heads;
+  const int split = own.plan[2 + 2 * seq + 1], first = own.plan[2 + 2 * seq];
+  const int pre_split = pre.rows ? pre.plan[3] : 0;
+  if (!pre.rows && split == 1) return;     // written by its only part
+  const int grp = tid / L, d = 4 * (tid % L);
+  for (int h = blockIdx.y; h < a.q_heads; h += gridDim.y) {
+    const int head = h / a.group, r = i * a.group + h % a.group, rt = r / own.rows;
+    const size_t slot0 = ((size_t)(first + rt * split) * KH + head) * own.rows + r % own.rows, step = (size_t)KH * own.rows;
+    const int rp = (m - row0) * a.group + h % a.group;
+    const size_t pslot0 = pre.rows ? ((size_t)(rp / pre.rows * pre_split) * KH + head) * pre.rows + rp % pre.rows : 0;
+    const size_t pstep = (size_t)KH * pre.rows;
+    float top = kNegInf;
+    for (int s = lane; s < split + pre_split; s += 64)
+      top = fmaxf(top, s < pre_split ? pre.ml[2 * (pslot0 + s * pstep)] : own.ml[2 * (slot0 + (s - pre_split) * step)]);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    float l = 0.f;
+    const float base = top == kNegInf ? 0.f : top;
+    for (int s = grp; s < split + pre_split; s += kGroups) {
+      const bool is_pre = s < pre_split;
+      const size_t slot = is_pre ? pslot0 + s * pstep : slot0 + (s - pre_split) * step;
+      const float* ml = (is_pre ? pre.ml : own.ml) + 2 * slot;
+      const float f = __builtin_amdgcn_exp2f(ml[0] - base);
+      l += f * ml[1];
+      o += f * *reinterpret_cast<const f32x4*>((is_pre ? pre.o : own.o) + slot * D + d);
+    }
+    __syncthreads();
+    *reinterpret_cast<f32x4*>(&s_o[grp][d]) = o;
+    if (d == 0) s_l[grp] = l;
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+      for (int w = 1; w < kGroups; ++w) {
+        o += *reinterpret_cast<const f32x4*>(&s_o[w][d]);
+        l += s_l[w];
+      }
+      write_row(a, (size_t)m * a.q_heads + h, D, d, o, top, l);
+    }
+  }
+}
+
+hipError_t launch_attn_few(const AttnArgs& a, const AttnParts& p, int grid, hipStream_t s) {
+  const bool i8 = a.c.ks != nullptr;
+#define Q4NX_FEW(D)                                                                                              \
+  if (i8) hipLaunchKernelGGL((k_attn_few<D, true>), dim3(grid), dim3(256), 4 * 16 * (D + 4) * 4, s, a, p);       \
+  else hipLaunchKernelGGL((k_attn_few<D, false>), dim3(grid), dim3(256), 4 * 16 * (D + 4) * 4, s, a, p)
+  if (a.c.dim == 64) { Q4NX_FEW(64); }
+  else if (a.c.dim == 128) { Q4NX_FEW(128); }
+  else { Q4NX_FEW(256); }
+#undef Q4NX_FEW
+  return hipGetLastError();
+}
+
+hipError_t launch_attn_join(const AttnArgs& a, const AttnParts& own, const AttnParts& prefix, hipStream_t s) {
+  // many rows fill the GPU by themselves, and most of them have one part
+  const dim3 grid(a.M, a.M >= 1024 ? 1 : std::min(a.q_heads, 1024 / a.M + 1));
+  if (a.c.dim == 64) hipLaunchKernelGGL(k_attn_join<64>, grid, dim3(256), 0, s, a, own, prefix);
+  else if (a.c.dim == 128) hipLaunchKernelGGL(k_attn_join<128>, grid, dim3(256), 0, s, a, own, prefix);
+  else hipLaunchKernelGGL(k_attn_join<256>, grid, dim3(256), 0, s, a, own, prefix);
+  return hipGetLastError();
+}
+
+}  // namespace q4nx

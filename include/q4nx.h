@@ -651,6 +651,175 @@ int q4nx_token_logprobs(const float* y, int n, int ldy, int M, const int32_t* to
                         size_t ws_bytes, void* stream);
 
 /*
+ * A paged cache of keys and values (onw technical notes, "compiler fixes": the
+ * engine's paged 8-bit cache with its online-softmax combine).  The pages are
+ * the caller's, of any order; page p and head h hold page_tokens tokens
+ *   k  [n_pages][kv_heads][page_tokens/16][head_dim/8][16][8]
+ *   v  [n_pages][kv_heads][page_tokens/8][head_dim][8]
+ * (last index fastest; token and dimension indexes split as shown), the order
+ * in which the matrix cores take their operands, so that attention reads pages
+ * in whole lines and rearranges nothing.
+ */
+enum { Q4NX_KV_BF16 = 0, Q4NX_KV_INT8 = 1 };
+typedef struct q4nx_kv_cache {
+  int32_t kv_heads;     /* 1..256 */
+  int32_t head_dim;     /* 64, 128 or 256 */
+  int32_t page_tokens;  /* a power of two, 16..1024 */
+  int32_t n_pages;      /* at least 1; n_pages * page_tokens at most 2^31 - 1 */
+  int32_t type;         /* Q4NX_KV_BF16, or Q4NX_KV_INT8: value = code * scale, codes -127..127 */
+  void* k;              /* DEVICE, 16-byte aligned */
+  void* v;              /* DEVICE, 16-byte aligned */
+  float* k_scale;       /* DEVICE fp32 [n_pages][kv_heads][page_tokens], 16-byte aligned; INT8 only */
+  float* v_scale;       /* the same for v (both NULL for bf16) */
+  int64_t k_bytes, v_bytes;               /* bytes available in k and v */
+  int64_t k_scale_bytes, v_scale_bytes;   /* and in the scales (INT8) */
+} q4nx_kv_cache;
+
+/* Heads of M rows: row m at p + m*ld elements, head after head. */
+enum { Q4NX_F32 = 0, Q4NX_BF16 = 1 };
+typedef struct q4nx_heads {
+  const void* p;        /* DEVICE, aligned to its element */
+  int64_t ld;           /* elements between rows, at least heads * head_dim */
+  int32_t heads;
+  int32_t type;         /* Q4NX_F32 (what a projection wrote) or Q4NX_BF16 (what a norm wrote) */
+} q4nx_heads;
+
+/* Rotation by position: pair i < dim/2 turns by pos * inv_freq[i]. */
+typedef struct q4nx_rope {
+  int32_t dim;             /* leading dimensions that turn: a multiple of 16, 16..head_dim */
+  int32_t interleaved;     /* 0: pair (i, i + dim/2); 1: pair (2i, 2i + 1) */
+  const float* inv_freq;   /* DEVICE fp32 [dim/2] */
+  const int32_t* pos;      /* DEVICE int32 [M], any value */
+} q4nx_rope;
+
+enum { Q4NX_KV_MAX_M = 16384 };   /* most rows of one q4nx_kv_append */
+
+/*
+ * The step from the q, k and v projections to attention: q and k turned by
+ * their positions, q rounded to bf16 for q4nx_attention, k and v stored in the
+ * cache, for M tokens:
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = pos[m] * inv_freq[i]
+ * The angle is formed and reduced in fp64, so that positions of any size keep
+ * their digits.  bf16 values are rounded once, from fp32.  INT8 values are
+ * formed in fp64 and cached as scale = fp32(max |x| / 127), code =
+ * round(x / scale), half to even, per token and head; a head of zeros has scale
+ * 0, and one with an infinity or NaN an infinite or NaN scale with codes 0.
+ *   q      heads * head_dim columns, or NULL (with q_out NULL): only k and v
+ *   q_out  DEVICE bf16 [M][q heads][head_dim], 16-byte aligned; every row is written
+ *   k, v   kv_heads heads each
+ *   rope   or NULL: nothing turns
+ *   slots  DEVICE int32 [M]: page * page_tokens + offset of each row's token, in
+ *          any order, or -1: the row is not cached (padding).  Of rows with one
+ *          slot the last is stored.  A slot below -1 or past the last page is
+ *          never written: its row is not cached, and bit 0 of *flags is set.
+ *   M      1..Q4NX_KV_MAX_M
+ *   flags  DEVICE uint32 or NULL; the call only sets bits, the caller clears them
+ * q_out and the cache must lie apart from the inputs and each other (E_ARG).
+ */
+int q4nx_kv_append(const q4nx_kv_cache* cache, const q4nx_rope* rope, const q4nx_heads* q, uint16_t* q_out,
+                   const q4nx_heads* k, const q4nx_heads* v, const int32_t* slots, int M, uint32_t* flags,
+                   void* stream);
+
+/* The sequences of one q4nx_attention. */
+typedef struct q4nx_attn_batch {
+  int32_t n_seq;                /* 1..1024 */
+  int32_t max_q;                /* rows that a sequence has at most; only the choice of kernels goes by it */
+  const int32_t* q_start;       /* DEVICE int32 [n_seq + 1]: sequence s has rows q_start[s] .. q_start[s+1]-1 */
+  const int32_t* kv_len;        /* DEVICE int32 [n_seq]: its cached tokens, the rows' own among them, without
+                                   the prefix */
+  const int32_t* pages;         /* DEVICE int32 [n_seq][pages_ld]: its pages in order */
+  int32_t pages_ld;             /* at least 1 */
+  int32_t prefix_len;           /* tokens that every sequence begins with, 0: none */
+  const int32_t* prefix_pages;  /* DEVICE int32 [ceil(prefix_len / page_tokens)] */
+} q4nx_attn_batch;
+
+enum { Q4NX_ATTN_MAX_SEQ = 1024, Q4NX_ATTN_MAX_M = 65536 };
+
+/*
+ * Attention over the cache for a batch that shares a prefix (onw technical
+ * notes, "compiler fixes": attention over a paged cache whose parts are joined
+ * by their maxima and sums).  Row i of a sequence with n rows and L cached
+ * tokens sees the whole prefix and its sequence's first L - n + i + 1 tokens:
+ *   out = sum_j p_j v_j,  p = softmax_j(scale * q.k_j),  lse = log sum_j exp(scale * q.k_j)
+ * Query head h reads key head h / (q_heads / kv_heads).
+ *   q     DEVICE bf16 [M][q_heads][head_dim], 16-byte aligned
+ *   out   DEVICE bf16 of the same shape, 16-byte aligned
+ *   lse   DEVICE fp32 [M][q_heads], or NULL
+ *   M     rows of q, out and lse, 1..Q4NX_ATTN_MAX_M.  Rows behind the last sequence, and
+ *         rows before the first, are left as they were.
+ *   scale finite
+ *   ws    DEVICE workspace of q4nx_attention_ws bytes for these arguments, 256-byte
+ *         aligned.  Nothing in it needs initialising; calls that share it must not overlap.
+ *   flags DEVICE uint32 or NULL; the call only sets bits, the caller clears them
+ * One token, windows of a few and whole prompts go through the same call; where
+ * several sequences have few rows each, the prefix is read once for all.
+ * A row that sees no key, or only keys with a score of -Inf, has out 0 and lse
+ * -Inf.  What lies past a sequence's tokens, in its last page or in its table,
+ * may hold anything, infinities and NaNs among it; so may tokens that a row does
+ * not see.  A page number outside the cache is never followed: its tokens count
+ * as unseen, and bit 0 of *flags is set.  A kv_len outside 0..pages_ld *
+ * page_tokens, and rows of q_start that fall or leave 0..M, are clamped, and
+ * bit 1 is set.
+ * Scores, maxima, sums and outputs are fp32; the softmax's numerators enter the
+ * second product in bf16, the sum of them does not.  Parts of a long row are
+ * joined in a fixed order; how rows are cut into parts goes by the whole batch's
+ * lengths, so that a row's last bits may differ between batches.
+ * E_SHAPE: q_heads no multiple of kv_heads, or more than 16384 columns of q.
+ */
+int q4nx_attention(const q4nx_kv_cache* cache, const q4nx_attn_batch* batch, const uint16_t* q, int q_heads,
+                   int M, float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes, uint32_t* flags,
+                   void* stream);
+/* Workspace bytes of q4nx_attention (0 = bad arguments); the descriptors' DEVICE pointers
+   are not looked at, and n_seq, max_q, prefix_len and M count. */
+size_t q4nx_attention_ws(const q4nx_kv_cache* cache, const q4nx_attn_batch* batch, int q_heads, int M);
+
+/* The sequences and heads of one q4nx_linear_attn. */
+typedef struct q4nx_linear {
+  int32_t k_heads;          /* heads of q and k, 1..256 */
+  int32_t v_heads;          /* heads of v, the decay and the state: a multiple of k_heads, at most 1024 */
+  int32_t dk, dv;           /* 64 or 128 each */
+  int32_t n_seq;            /* 1..1024 */
+  int32_t max_q;            /* rows that a sequence has at most; only the choice of kernels goes by it */
+  int32_t n_slots;          /* states */
+  const int32_t* q_start;   /* DEVICE int32 [n_seq + 1] */
+  const int32_t* slots;     /* DEVICE int32 [n_seq]: a sequence's state, or -1: none is read or kept */
+  const int32_t* fresh;     /* DEVICE int32 [n_seq] or NULL: not 0: begin with zeros instead of the state */
+} q4nx_linear;
+
+/*
+ * Linear attention with a decay for each head (Strata article, the recurrent
+ * mixer's states and their checkpoints): for each value head, with its state S
+ * [dk][dv] in fp32,
+ *   S_t = exp(decay_t) S_{t-1} + k_t v_t^T,   out_t = scale * q_t^T S_t
+ * over the rows of each sequence in order.  Value head h reads q and k of head
+ * h / (v_heads / k_heads).
+ *   q, k   DEVICE bf16, row m at q + m*q_ld, k + m*k_ld: [k_heads][dk]; 16-byte aligned, strides a
+ *          multiple of 8 elements
+ *   v      DEVICE bf16, row m at v + m*v_ld: [v_heads][dv], likewise
+ *   decay  DEVICE fp32, row m at decay + m*decay_ld: [v_heads], decay_ld at least v_heads, or 0:
+ *          the same for every token.  Natural logarithms, of 0 at most (-Inf forgets all); a larger
+ *          one, or NaN, is taken as 0, and bit 1 of *flags is set.
+ *   state      DEVICE fp32 [n_slots][v_heads][dk][dv], 16-byte aligned: what the sequences begin with
+ *   state_out  the same shape: receives what they end with; state itself, or apart from it (a
+ *              checkpoint to go back to).  Slots of no sequence, or of one without rows, are left as they were.
+ *   out    DEVICE fp32 [M][v_heads][dv], 16-byte aligned; rows of no sequence are left as they were
+ *   M      1..Q4NX_ATTN_MAX_M rows
+ *   ws     DEVICE workspace of q4nx_linear_attn_ws(L, M) bytes, 256-byte aligned.  Nothing in
+ *          it needs initialising; calls that share it must not overlap.
+ *   flags  DEVICE uint32 or NULL; the call only sets bits, the caller clears them
+ * Few rows run as the recurrence, prompts in chunks of 64 rows whose products go
+ * to the matrix cores with every operand's 24 bits: states and sums are fp32.
+ * A slot outside -1..n_slots-1, or one that an earlier sequence with rows has, is
+ * taken as -1 and sets bit 0.  Rows of q_start that fall or leave 0..M are
+ * clamped, and bit 2 is set.
+ */
+int q4nx_linear_attn(const q4nx_linear* L, const uint16_t* q, int64_t q_ld, const uint16_t* k, int64_t k_ld,
+                     const uint16_t* v, int64_t v_ld, const float* decay, int64_t decay_ld, int M, float scale,
+                     const float* state, float* state_out, float* out, void* ws, size_t ws_bytes,
+                     uint32_t* flags, void* stream);
+size_t q4nx_linear_attn_ws(const q4nx_linear* L, int M);
+
+/*
  * Test surface of the decoders (NPU engine page, "Q4NX chunks": the decoders
  * of all three kinds are checked bit for bit).  Writes the fields of every
  * chunk in logical [rows][cols] order:

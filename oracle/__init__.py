@@ -15,6 +15,8 @@ the HIP kernels.  It is plain, slow and written to be checked by eye:
   bound;
 * ``tail``    -- low-rank adapters beside a projection, the residual RMS norm
   and log probabilities over logits, from their definitions;
+* ``mixing``  -- rotation and the paged cache's layout, attention behind a shared
+  prefix, and linear attention with decay, row by row;
 * ``gguf``    -- GGUF Q4_0 / Q4_1 / Q4_K blocks decoded from their own
   definition, and the q4_1 fields the GGUF -> q4_1 conversion must give.
 
@@ -37,6 +39,8 @@ from .ref import (gemv_ref, check_tol, tol_ratio, silu, swiglu, moe_layer_ref, m
                   repack_q4k_to_q41, repack_bound, router_topk, router_logits_ref, head_topk)
 from .gguf import (GGUF_Q4_0, GGUF_Q4_1, GGUF_Q4_K, gguf_bytes, gguf_fields, gguf_dequant,
                    gguf_to_q41, gguf_to_q41_bound)
+from .mixing import (attention_batch_ref, attention_ref, linear_attn_ref, pack_k, pack_v, rope_ref, unpack_k,
+                     unpack_v)
 from .tail import add_rmsnorm_ref, lora_ref, token_logprobs_ref
 
 __all__ = [
@@ -46,5 +50,6 @@ __all__ = [
     "moe_layer_ref", "moe_combine_ref", "repack_q4k_to_q41", "repack_bound", "router_topk",
     "router_logits_ref", "head_topk", "GGUF_Q4_0", "GGUF_Q4_1", "GGUF_Q4_K", "gguf_bytes", "gguf_fields",
     "gguf_dequant", "gguf_to_q41", "gguf_to_q41_bound",
+    "attention_ref", "attention_batch_ref", "linear_attn_ref", "rope_ref", "pack_k", "pack_v", "unpack_k", "unpack_v",
     "lora_ref", "add_rmsnorm_ref", "token_logprobs_ref",
 ]

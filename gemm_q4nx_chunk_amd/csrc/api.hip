@@ -1771,15 +1771,15 @@ void attn_shape(const q4nx_kv_cache* c, const q4nx_attn_batch* b, int q_heads, i
   memset(&sh, 0, sizeof sh);
   const int KH = c->kv_heads, group = q_heads / KH;
   const int64_t rows = (int64_t)M * group;
-  const bool apart = b->prefix_len > 0 && b->n_seq > 1;
+  const bool apart = b->prefix_len > 0 && b->n_seq > 1 && (int64_t)b->max_q * group < 128;
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   size_t o = 0;
-  auto place = [&](q4nx::AttnParts& p, int set, int& grid, size_t& plan, size_t& po, size_t& ml) {
+  auto place = [&](q4nx::AttnParts& p, int set, bool many, int& grid, size_t& plan, size_t& po, size_t& ml) {
     p.set = set;
-    p.rows = 16;
-    p.target = 2048;
+    p.rows = many ? 128 : 16;
+    p.target = many ? 512 : 2048;
     const int64_t parts = q4nx::attn_max_parts(set, b->n_seq, rows, KH, p.rows, p.target);
-    grid = (int)std::min<int64_t>(parts, 1024);
+    grid = (int)std::min<int64_t>(parts, many ? 1 << 20 : 1024);
     plan = o;
     o = up(o + (2 + 2 * (size_t)q4nx::attn_entries(set, b->n_seq)) * 4);
     po = o;
@@ -1787,8 +1787,8 @@ void attn_shape(const q4nx_kv_cache* c, const q4nx_attn_batch* b, int q_heads, i
     ml = o;
     o = up(o + (size_t)parts * p.rows * 8);
   };
-  place(sh.own, apart ? q4nx::ATTN_OWN : q4nx::ATTN_ALL, sh.own_grid, sh.own_plan, sh.own_o, sh.own_ml);
-  if (apart) place(sh.pre, q4nx::ATTN_PREFIX, sh.pre_grid, sh.pre_plan, sh.pre_o, sh.pre_ml);
+  place(sh.own, apart ? q4nx::ATTN_OWN : q4nx::ATTN_ALL, (int64_t)b->max_q * group > 16, sh.own_grid, sh.own_plan, sh.own_o, sh.own_ml);
+  if (apart) place(sh.pre, q4nx::ATTN_PREFIX, rows > 16, sh.pre_grid, sh.pre_plan, sh.pre_o, sh.pre_ml);
   sh.total = o;
 }
 
@@ -1931,8 +1931,11 @@ int q4nx_attention(const q4nx_kv_cache* cache, const q4nx_attn_batch* batch, con
   at(sh.own, sh.own_plan, sh.own_o, sh.own_ml);
   if (sh.pre.rows) at(sh.pre, sh.pre_plan, sh.pre_o, sh.pre_ml);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = q4nx::launch_attn_few(a, sh.own, sh.own_grid, s);
-  if (e == hipSuccess && sh.pre.rows) e = q4nx::launch_attn_few(a, sh.pre, sh.pre_grid, s);
+  auto launch = [&](const q4nx::AttnParts& p, int grid) {
+    return p.rows == 128 ? q4nx::launch_attn_many(a, p, grid, s) : q4nx::launch_attn_few(a, p, grid, s);
+  };
+  hipError_t e = launch(sh.own, sh.own_grid);
+  if (e == hipSuccess && sh.pre.rows) e = launch(sh.pre, sh.pre_grid);
   if (e == hipSuccess) e = q4nx::launch_attn_join(a, sh.own, sh.pre, s);
   return hip_status(e, "attention launch");
 }

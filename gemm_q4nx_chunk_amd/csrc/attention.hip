@@ -29,6 +29,28 @@ __device__ __forceinline__ bf16x8 cache8(const void* p, size_t at) {
   else return *reinterpret_cast<const bf16x8*>(static_cast<const uint16_t*>(p) + at);
 }
 
+// N products of which each takes an operand from LDS: read(n) gives it, mul(n, v)
+// uses it.  Four operands are read while the four before them are used; the
+// scheduler, left alone, reads each right before its product and waits.
+template <int N, typename Read, typename Mul>
+__device__ __forceinline__ void fed(Read read, Mul mul) {
+  static_assert(N % 4 == 0, "groups of four");
+  bf16x8 v[2][4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) v[0][n] = read(n);
+#pragma unroll
+  for (int g = 0; g < N / 4; ++g) {
+    if (g + 1 < N / 4) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) v[(g + 1) & 1][n] = read(4 * g + 4 + n);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) mul(4 * g + n, v[g & 1][n]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
 // Four dimensions of a row and head, from d.  A sum of 0 is that of a row that
 // sees nothing (any other has its largest term, 1, or a NaN).
 __device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, int D, int d, f32x4 o, float m, float l) {
@@ -223,6 +245,280 @@ __global__ __launch_bounds__(256) void k_attn_few(AttnArgs a, AttnParts p) {
   }
 }
 
+// Many rows (128 a tile): prompts, and the shared prefix of a batch.  Each wave
+// has 32 rows, in matrix instructions of 32 x 32; the four share a tile of KT
+// keys that goes from memory straight to LDS, in the order in which it lies,
+// while the tile before it is worked on.  Lines of S^T are dealt as above, so
+// that a lane's scores of 16 keys are eight neighbouring tokens': P never
+// leaves its registers.
+//
+// The maximum that scores are taken against is raised only when a row's grows
+// by 2^8: numerators up to 2^8 lose nothing in bf16 or in the fp32 sums, and the
+// outputs are rescaled a few times a row instead of once a tile.
+template <int D, bool I8, int KT>
+__global__ __launch_bounds__(256, 2) void k_attn_many(AttnArgs a, AttnParts p) {
+  constexpr int kRows = 128, NQ = D / 16, NB = KT / 32, NO = D / 32, kBlocks = KT / 16, kTiles = kAttnUnit / KT;
+  constexpr int kTile = KT * D;   // elements of K or V
+  __shared__ AttnPlan plan;
+  __shared__ __align__(16) int32_t s_valid[2][4];     // tokens that count of each 16
+  __shared__ __align__(16) float s_ks[I8 ? 2 : 1][I8 ? KT : 4], s_vs[I8 ? 2 : 1][I8 ? KT : 4];
+  extern __shared__ __align__(16) uint16_t s_kv[];    // [2][K | V]
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c = lane & 31, hh = lane >> 5;
+  const int total = attn_plan(a, p, plan), entries = p.set == ATTN_PREFIX ? 1 : a.n_seq;
+  const int KH = a.c.heads, ps = a.c.page_shift;
+  // -Inf of a key that is not seen stays -Inf under any scale
+  const float scale = a.scale == 0.f ? 1e-45f : fabsf(a.scale);
+  const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+  // where the lane's operands lie in a tile
+  const int line = 16 * ((c >> 3) >> 1) + 8 * ((c >> 2) & 1) + 4 * ((c >> 3) & 1) + (c & 3);
+  const int k_at = (line >> 4) * 16 * D + hh * 128 + (line & 15) * 8, v_at = hh * 8 * D + c * 8;
+  for (int idx = blockIdx.x; idx < total * KH; idx += gridDim.x) {
+    const int head = idx % KH, nth = idx / KH;
+    const int e = attn_find(plan, entries, nth);
+    const AttnEntry x = attn_entry(a, plan.start, p.set, kRows, e);
+    const int split = max(1, (x.units + plan.per - 1) / plan.per);
+    const int local = x.tiles * split - 1 - (nth - plan.first[e]);   // the last tiles see most keys: first
+    const int part = local % split, rt = local / split, it = plan.first[e] + local;
+    const int r0 = rt * kRows + 32 * wave;
+    const bool has_rows = r0 < x.rows;
+    const int r = min(r0 + c, x.rows - 1);
+    const int i = r / a.group, h = head * a.group + r % a.group;
+    auto seen = [&](int row) { return min(max(x.causal + row / a.group + 1, 0), x.own); };
+    const int lim_own = seen(r), lim_first = seen(min(r0, x.rows - 1)), lim_wave = seen(min(r0 + 31, x.rows - 1));
+    const int lim_last = seen(min(rt * kRows + kRows, x.rows) - 1);
+    const int pre_units = attn_units(x.pre), units = pre_units + attn_units(lim_last);
+    const int per = (units + split - 1) / split, u0 = part * per, u1 = min(units, u0 + per);
+    // tiles: [0, pre_end) of the prefix, [own_begin, own_end) of the sequence's own
+    const int pre_end = (x.pre + KT - 1) / KT, own_begin = pre_units * kTiles, own_end = own_begin + (lim_last + KT - 1) / KT;
+    const int t_end = min(u1 * kTiles, own_end);
+    auto skip = [&](int t) { return t >= pre_end && t < own_begin ? own_begin : t; };
+    const int32_t* own_pages = p.set == ATTN_PREFIX ? nullptr : a.pages + (size_t)e * a.pages_ld;
+
+    bf16x8 qf[NQ];
+    const uint16_t* qp = a.q + ((size_t)(x.row0 + i) * a.q_heads + h) * D + 8 * hh;
+#pragma unroll
+    for (int s = 0; s < NQ; ++s) {
+      u32x4 w = *reinterpret_cast<const u32x4*>(qp + 16 * s);
+      w ^= u32x4{flip, flip, flip, flip};
+      qf[s] = __builtin_bit_cast(bf16x8, w);
+    }
+    f32x16 acc[NO];
+#pragma unroll
+    for (int o = 0; o < NO; ++o)
+#pragma unroll
+      for (int n = 0; n < 16; ++n) acc[o][n] = 0.f;
+    float m_run = kNegInf, l_run = 0.f;
+
+    // A tile's loading: wave w has 16-token block w of K and of V (two blocks: the upper two waves V).
+    // 8-bit tiles go through registers, 16 bytes of codes at a time, and become bf16 on the way.
+    constexpr int kRaw = I8 ? KT * D / 16 / 256 : 1;
+    u32x4 raw_k[kRaw], raw_v[kRaw];
+    float raw_scale = 0.f;
+    const int my_block = kBlocks == 4 ? wave : wave & 1;
+    auto page_of = [&](int t, int blk) {   // 0 where nothing is to be loaded
+      const bool pre = t < own_begin;
+      const int key = (pre ? t : t - own_begin) * KT + 16 * blk, have = pre ? x.pre : lim_last;
+      return t < t_end && key < have ? (pre ? a.prefix_pages : own_pages)[key >> ps] : 0;
+    };
+    auto issue = [&](int t, int buf, int page) {
+      const bool pre = t < own_begin;
+      const int key0 = (pre ? t : t - own_begin) * KT, have = pre ? x.pre : lim_last;
+      if constexpr (I8) {
+#pragma unroll
+        for (int n = 0; n < kRaw; ++n) {
+          const int at = tid + 256 * n, blk = at / D;
+          const int key = key0 + 16 * blk;
+          const int pg = key < have ? (pre ? a.prefix_pages : own_pages)[key >> ps] : 0;
+          const size_t base = kv_page(a.c, (uint32_t)pg < (uint32_t)a.c.n_pages ? pg : 0, head) + (size_t)(key & ((1 << ps) - 1)) * D + (at % D) * 16;
+          raw_k[n] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.c.k) + base);
+          raw_v[n] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.c.v) + base);
+        }
+        if (tid < 2 * KT) {
+          const int tok = tid % KT, key = key0 + tok;
+          const int pg = key < have ? (pre ? a.prefix_pages : own_pages)[key >> ps] : 0;
+          const bool ok = (uint32_t)pg < (uint32_t)a.c.n_pages;
+          if (!ok) set_flag(a.flags, kFlagIndex);
+          raw_scale = (tid < KT ? a.c.ks : a.c.vs)[((((size_t)(ok ? pg : 0) * KH + head) << ps)) + (key & ((1 << ps) - 1))];
+          if (tid < KT && (tok & 15) == 0) s_valid[buf][tok >> 4] = ok ? min(max(have - key, 0), 16) : 0;
+        }
+      } else {
+        const int key = key0 + 16 * my_block;
+        const bool ok = (uint32_t)page < (uint32_t)a.c.n_pages;
+        if (!ok) set_flag(a.flags, kFlagIndex);
+        if ((kBlocks == 4 || wave < 2) && lane == 0) s_valid[buf][my_block] = ok ? min(max(have - key, 0), 16) : 0;
+        if (key < have) {
+          const size_t at = kv_page(a.c, ok ? page : 0, head) + (size_t)(key & ((1 << ps) - 1)) * D + lane * 8;
+          uint16_t* to = s_kv + buf * 2 * kTile + my_block * 16 * D;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv)
+            if (kBlocks == 4 || (wave >> 1) == kv) {
+              const uint16_t* from = static_cast<const uint16_t*>(kv ? a.c.v : a.c.k) + at;
+#pragma unroll
+              for (int n = 0; n < D / 32; ++n)
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + 512 * n),
+                                                 (lds_void*)(to + kv * kTile + 512 * n), 16, 0, 0);
+            }
+        }
+      }
+    };
+    auto finish = [&](int buf) {
+      if constexpr (I8) {
+#pragma unroll
+        for (int n = 0; n < kRaw; ++n) {
+          uint16_t* to = s_kv + buf * 2 * kTile + (tid + 256 * n) * 16;
+          *reinterpret_cast<bf16x8*>(to) = bf16x8_of_codes(u32x2{raw_k[n].x, raw_k[n].y});
+          *reinterpret_cast<bf16x8*>(to + 8) = bf16x8_of_codes(u32x2{raw_k[n].z, raw_k[n].w});
+          *reinterpret_cast<bf16x8*>(to + kTile) = bf16x8_of_codes(u32x2{raw_v[n].x, raw_v[n].y});
+          *reinterpret_cast<bf16x8*>(to + kTile + 8) = bf16x8_of_codes(u32x2{raw_v[n].z, raw_v[n].w});
+        }
+        if (tid < 2 * KT) (tid < KT ? s_ks : s_vs)[buf][tid % KT] = raw_scale;
+      }
+    };
+
+    int t = skip(u0 * kTiles);
+    __syncthreads();   // the item before is done with LDS
+    if (t < t_end) {
+      issue(t, 0, I8 ? 0 : page_of(t, my_block));
+      finish(0);
+    }
+    int next = skip(t + 1), page_v = I8 ? 0 : page_of(next, my_block);
+    for (int buf = 0; t < t_end; buf ^= 1) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      const int page = __builtin_amdgcn_readfirstlane(page_v);
+      const int after = skip(next + 1);
+      if (next < t_end) {
+        issue(next, buf ^ 1, page);
+        if (!I8) page_v = page_of(after, my_block);
+      }
+      const bool pre = t < own_begin;
+      const int key0 = (pre ? t : t - own_begin) * KT;
+      if (has_rows && (pre || key0 < lim_wave)) {
+        const uint16_t* sk = s_kv + buf * 2 * kTile + k_at;
+        const uint16_t* sv = s_kv + buf * 2 * kTile + kTile + v_at;
+        f32x16 st[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int n = 0; n < 16; ++n) st[b][n] = 0.f;
+        fed<NQ * NB>([&](int n) { return *reinterpret_cast<const bf16x8*>(sk + (n % NB) * 32 * D + (n / NB) * 256); },
+                     [&](int n, bf16x8 k) {
+                       st[n % NB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[n / NB], st[n % NB], 0, 0, 0);
+                     });
+        int valid[kBlocks], least = 16;
+#pragma unroll
+        for (int n = 0; n < kBlocks; ++n) {
+          valid[n] = __builtin_amdgcn_readfirstlane(s_valid[buf][n]);
+          least = min(least, valid[n]);
+        }
+        if constexpr (I8) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int n = 0; n < 16; ++n) st[b][n] *= s_ks[buf][32 * b + 16 * (n >> 3) + 8 * hh + (n & 7)];
+        }
+        const bool masked = least < 16 || (!pre && key0 + KT > lim_first);
+        if (masked) {
+          const int lim = (pre ? x.pre : lim_own) - key0 - 8 * hh;
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int n = 0; n < 16; ++n)
+              if ((n & 7) >= min(lim - 32 * b - 16 * (n >> 3), valid[2 * b + (n >> 3)] - 8 * hh)) st[b][n] = kNegInf;
+        }
+        float top = st[0][0];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int n = 0; n < 16; ++n) top = fmaxf(top, st[b][n]);
+        top = fmaxf(top, __shfl_xor(top, 32)) * scale;
+        if (__ballot(top > m_run + 8.f)) {
+          const float m_new = fmaxf(m_run, top);
+          const float alpha = __builtin_amdgcn_exp2f(m_run - (m_new == kNegInf ? 0.f : m_new));
+          m_run = m_new;
+          l_run *= alpha;
+#pragma unroll
+          for (int o = 0; o < NO; ++o)
+#pragma unroll
+            for (int n = 0; n < 16; ++n) acc[o][n] *= alpha;
+        }
+        const float base = m_run == kNegInf ? 0.f : m_run;
+        float sum = 0.f;
+        bf16x8 pf[NB][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            float e2 = __builtin_amdgcn_exp2f(fmaf(st[b][n], scale, -base));
+            sum += e2;
+            if constexpr (I8) e2 = st[b][n] == kNegInf ? 0.f : e2 * s_vs[buf][32 * b + 16 * (n >> 3) + 8 * hh + (n & 7)];
+            pf[b][n >> 3][n & 7] = (__bf16)e2;
+          }
+        l_run += sum;
+        if (!masked || I8) {
+          fed<NB * 2 * NO>(
+              [&](int n) { return *reinterpret_cast<const bf16x8*>(sv + (n / NO) * 2 * 8 * D + (n % NO) * 256); },
+              [&](int n, bf16x8 v) {
+                acc[n % NO] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pf[n / NO / 2][n / NO % 2], acc[n % NO], 0, 0, 0);
+              });
+        } else {
+          // values behind the tokens may be anything: 0 instead.  An infinity or NaN that only some of the
+          // rows see is kept out of the product, which has a 0 for the others, and added to those rows.
+          bool any = false;
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int o = 0; o < NO; ++o) {
+                bf16x8 v = keep_first(*reinterpret_cast<const bf16x8*>(sv + (4 * b + 2 * s) * 8 * D + o * 256),
+                                      valid[2 * b + s] - 8 * hh);
+                any |= drop_nonfinite(v);
+                acc[o] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pf[b][s], acc[o], 0, 0, 0);
+              }
+          if (__ballot(any)) {
+            const uint16_t* tile = s_kv + buf * 2 * kTile + kTile;
+            for (int n = 0; n < KT; ++n) {
+              if ((n & 15) >= s_valid[buf][n >> 4]) continue;
+              const bool mine = key0 + n < (pre ? x.pre : lim_own);
+#pragma unroll
+              for (int o = 0; o < NO; ++o)
+#pragma unroll
+                for (int d = 0; d < 16; ++d) {
+                  const float v = bf16lo(tile[v_place(D, n, 32 * o + 8 * (d >> 2) + 4 * hh + (d & 3))]);
+                  if (!(fabsf(v) <= __FLT_MAX__) && mine) acc[o][d] += v;
+                }
+            }
+          }
+        }
+      }
+      if (next < t_end) finish(buf ^ 1);
+      t = next;
+      next = after;
+    }
+    l_run += __shfl_xor(l_run, 32);
+    const int rr = r0 + c;
+    if (rr < x.rows) {
+      const bool whole = split == 1 && p.set == ATTN_ALL;
+      const size_t slot = ((size_t)it * KH + head) * kRows + 32 * wave + c;
+      const size_t row = (size_t)(x.row0 + i) * a.q_heads + h;
+#pragma unroll
+      for (int o = 0; o < NO; ++o)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const f32x4 v = {acc[o][4 * n], acc[o][4 * n + 1], acc[o][4 * n + 2], acc[o][4 * n + 3]};
+          const int d = 32 * o + 8 * n + 4 * hh;
+          if (whole) write_row(a, row, D, d, v, m_run, l_run);
+          else *reinterpret_cast<f32x4*>(p.o + slot * D + d) = v;
+        }
+      if (!whole && hh == 0) {
+        p.ml[slot * 2] = m_run;
+        p.ml[slot * 2 + 1] = l_run;
+      }
+    }
+  }
+}
+
 // The parts of one row and head, joined in order.  32 * D / 128 lanes have four
 // dimensions each; the rest of the workgroup shares the parts.
 template <int D>
@@ -306,6 +602,18 @@ hipError_t launch_attn_few(const AttnArgs& a, const AttnParts& p, int grid, hipS
   else if (a.c.dim == 128) { Q4NX_FEW(128); }
   else { Q4NX_FEW(256); }
 #undef Q4NX_FEW
+  return hipGetLastError();
+}
+
+hipError_t launch_attn_many(const AttnArgs& a, const AttnParts& p, int grid, hipStream_t s) {
+  const bool i8 = a.c.ks != nullptr;
+#define Q4NX_MANY(D, KT)                                                                                         \
+  if (i8) hipLaunchKernelGGL((k_attn_many<D, true, KT>), dim3(grid), dim3(256), 2 * 2 * KT * D * 2, s, a, p);    \
+  else hipLaunchKernelGGL((k_attn_many<D, false, KT>), dim3(grid), dim3(256), 2 * 2 * KT * D * 2, s, a, p)
+  if (a.c.dim == 64) { Q4NX_MANY(64, 64); }
+  else if (a.c.dim == 128) { Q4NX_MANY(128, 64); }
+  else { Q4NX_MANY(256, 32); }
+#undef Q4NX_MANY
   return hipGetLastError();
 }
 

@@ -105,6 +105,7 @@ inline int64_t attn_max_parts(int set, int n_seq, int64_t rows, int kv_heads, in
   return (rows / tile_rows + attn_entries(set, n_seq)) * kv_heads + target;
 }
 hipError_t launch_attn_few(const AttnArgs& a, const AttnParts& p, int grid, hipStream_t s);
+hipError_t launch_attn_many(const AttnArgs& a, const AttnParts& p, int grid, hipStream_t s);
 // own: the set of the sequences; prefix: of the prefix, or rows = 0
 hipError_t launch_attn_join(const AttnArgs& a, const AttnParts& own, const AttnParts& prefix, hipStream_t s);
 

@@ -1792,6 +1792,50 @@ void attn_shape(const q4nx_kv_cache* c, const q4nx_attn_batch* b, int q_heads, i
   sh.total = o;
 }
 
+int check_linear(const q4nx_linear* L, int M) {
+  if (!L) return fail(Q4NX_E_ARG, "linear_attn: null descriptor");
+  if (L->n_seq < 1 || L->n_seq > Q4NX_ATTN_MAX_SEQ || L->max_q < 1 || L->max_q > Q4NX_ATTN_MAX_M || L->n_slots < 1 ||
+      L->n_slots > (1 << 20))
+    return fail(Q4NX_E_ARG, "linear_attn: n_seq = %d, max_q = %d, n_slots = %d (1..%d, 1..%d, 1..1048576)", L->n_seq, L->max_q,
+                L->n_slots, (int)Q4NX_ATTN_MAX_SEQ, (int)Q4NX_ATTN_MAX_M);
+  if (M < 1 || M > Q4NX_ATTN_MAX_M) return fail(Q4NX_E_ARG, "linear_attn: M = %d outside 1..%d", M, (int)Q4NX_ATTN_MAX_M);
+  if (L->k_heads < 1 || L->k_heads > 256 || L->v_heads < 1 || L->v_heads > 1024 || L->v_heads % L->k_heads)
+    return fail(Q4NX_E_SHAPE, "linear_attn: %d key and %d value heads (1..256, a multiple of them up to 1024)", L->k_heads,
+                L->v_heads);
+  if ((L->dk != 64 && L->dk != 128) || (L->dv != 64 && L->dv != 128))
+    return fail(Q4NX_E_SHAPE, "linear_attn: dk = %d, dv = %d are not 64 or 128 each", L->dk, L->dv);
+  return Q4NX_OK;
+}
+
+// How one q4nx_linear_attn runs.
+struct LinearShape {
+  bool chunks;
+  int seg, items;      // rows of a segment; segments at most
+  bool carried;        // a sequence may have several
+  size_t plan, decay, state, total;
+};
+
+LinearShape linear_shape(const q4nx_linear* L, int M) {
+  LinearShape sh;
+  memset(&sh, 0, sizeof sh);
+  sh.total = 256;
+  sh.chunks = L->max_q > 16;
+  if (!sh.chunks) return sh;
+  const int64_t chunks = ((int64_t)M + 63) / 64 * L->v_heads;
+  sh.seg = 64 * (int)std::max<int64_t>(2, (chunks + 511) / 512);
+  sh.carried = L->max_q > sh.seg && L->n_seq * (int64_t)L->v_heads < 512;
+  if (!sh.carried) sh.seg = 1 << 30;
+  sh.items = sh.carried ? M / sh.seg + L->n_seq : L->n_seq;
+  if (!sh.carried) return sh;
+  auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+  size_t o = up(((size_t)L->n_seq + 1) * 4);
+  sh.decay = o;
+  o = up(o + (size_t)sh.items * L->v_heads * 8);
+  sh.state = o;
+  sh.total = up(o + (size_t)sh.items * L->v_heads * L->dk * L->dv * 4);
+  return sh;
+}
+
 int check_attn(const q4nx_kv_cache* c, const q4nx_attn_batch* b, int q_heads, int M, bool pointers) {
   const int st = check_cache(c, "attention", pointers);
   if (st) return st;
@@ -1941,27 +1985,18 @@ int q4nx_attention(const q4nx_kv_cache* cache, const q4nx_attn_batch* batch, con
 }
 
 size_t q4nx_linear_attn_ws(const q4nx_linear* L, int M) {
-  if (!L || M < 1 || M > Q4NX_ATTN_MAX_M) return 0;
-  return 256;
+  if (check_linear(L, M)) return 0;
+  return linear_shape(L, M).total;
 }
 
 int q4nx_linear_attn(const q4nx_linear* L, const uint16_t* q, int64_t q_ld, const uint16_t* k, int64_t k_ld,
                      const uint16_t* v, int64_t v_ld, const float* decay, int64_t decay_ld, int M, float scale,
                      const float* state, float* state_out, float* out, void* ws, size_t ws_bytes, uint32_t* flags,
                      void* stream) {
-  if (!L) return fail(Q4NX_E_ARG, "linear_attn: null descriptor");
+  const int st = check_linear(L, M);
+  if (st) return st;
   if (!q || !k || !v || !decay || !state || !state_out || !out) return fail(Q4NX_E_ARG, "linear_attn: null array");
   if (!L->q_start || !L->slots) return fail(Q4NX_E_ARG, "linear_attn: null q_start or slots");
-  if (L->n_seq < 1 || L->n_seq > Q4NX_ATTN_MAX_SEQ || L->max_q < 1 || L->max_q > Q4NX_ATTN_MAX_M || L->n_slots < 1 ||
-      L->n_slots > (1 << 20))
-    return fail(Q4NX_E_ARG, "linear_attn: n_seq = %d, max_q = %d, n_slots = %d (1..%d, 1..%d, 1..1048576)", L->n_seq, L->max_q,
-                L->n_slots, (int)Q4NX_ATTN_MAX_SEQ, (int)Q4NX_ATTN_MAX_M);
-  if (M < 1 || M > Q4NX_ATTN_MAX_M) return fail(Q4NX_E_ARG, "linear_attn: M = %d outside 1..%d", M, (int)Q4NX_ATTN_MAX_M);
-  if (L->k_heads < 1 || L->k_heads > 256 || L->v_heads < 1 || L->v_heads > 1024 || L->v_heads % L->k_heads)
-    return fail(Q4NX_E_SHAPE, "linear_attn: %d key and %d value heads (1..256, a multiple of them up to 1024)", L->k_heads,
-                L->v_heads);
-  if ((L->dk != 64 && L->dk != 128) || (L->dv != 64 && L->dv != 128))
-    return fail(Q4NX_E_SHAPE, "linear_attn: dk = %d, dv = %d are not 64 or 128 each", L->dk, L->dv);
   const int64_t kc = (int64_t)L->k_heads * L->dk, vc = (int64_t)L->v_heads * L->dv, most = (int64_t)1 << 40;
   if (q_ld < kc || k_ld < kc || v_ld < vc || q_ld > most || k_ld > most || v_ld > most)
     return fail(Q4NX_E_SHAPE, "linear_attn: row strides %lld, %lld, %lld below %lld, %lld, %lld columns, or too large",
@@ -1974,7 +2009,8 @@ int q4nx_linear_attn(const q4nx_linear* L, const uint16_t* q, int64_t q_ld, cons
     return fail(Q4NX_E_ALIGN, "linear_attn: q, k, v, the states and out must be 16-byte aligned, strides multiples of 8");
   if (!aligned(decay, 4) || !aligned(L->q_start, 4) || !aligned(L->slots, 4) || !aligned(L->fresh, 4) || !aligned(flags, 4))
     return fail(Q4NX_E_ALIGN, "linear_attn: decay, q_start, slots, fresh and flags must be 4-byte aligned");
-  const size_t need = q4nx_linear_attn_ws(L, M);
+  const LinearShape sh = linear_shape(L, M);
+  const size_t need = sh.total;
   if (!ws || ws_bytes < need) return fail(Q4NX_E_WORKSPACE, "linear_attn: workspace of %zu bytes, %zu needed", ws_bytes, need);
   if (!aligned(ws, 256)) return fail(Q4NX_E_ALIGN, "linear_attn: workspace not 256-byte aligned");
   const uint64_t sb = (uint64_t)L->n_slots * L->v_heads * L->dk * L->dv * 4, r = (uint64_t)M - 1;
@@ -2010,7 +2046,16 @@ int q4nx_linear_attn(const q4nx_linear* L, const uint16_t* q, int64_t q_ld, cons
   a.n_slots = L->n_slots;
   a.M = M;
   a.scale = scale;
-  return hip_status(q4nx::launch_linear_rows(a, static_cast<hipStream_t>(stream)), "linear_attn launch");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (!sh.chunks) return hip_status(q4nx::launch_linear_rows(a, s), "linear_attn launch");
+  a.seg = sh.seg;
+  if (sh.carried) {
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    a.plan = reinterpret_cast<int32_t*>(w + sh.plan);
+    a.seg_decay = reinterpret_cast<double*>(w + sh.decay);
+    a.seg_state = reinterpret_cast<float*>(w + sh.state);
+  }
+  return hip_status(q4nx::launch_linear_chunks(a, sh.items, s), "linear_attn launch");
 }
 
 int q4nx_decode(const q4nx_weight* w, float* out, void* stream) {

@@ -125,7 +125,14 @@ struct LinearArgs {
   uint32_t* flags;
   int32_t k_heads, v_heads, dk, dv, n_seq, n_slots, M;
   float scale;
+  // prompts: rows of a segment (a multiple of 64), and, where a sequence may have several, in the workspace
+  int32_t seg;
+  int32_t* plan;       // [n_seq + 1] first segment of each sequence
+  double* seg_decay;   // [segment][v_heads] sum of its decays
+  float* seg_state;    // [segment][v_heads][dk][dv], or null: a sequence is one segment
 };
 hipError_t launch_linear_rows(const LinearArgs& a, hipStream_t s);
+// items: segments at most
+hipError_t launch_linear_chunks(const LinearArgs& a, int items, hipStream_t s);
 
 }  // namespace q4nx

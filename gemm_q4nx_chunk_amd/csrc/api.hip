@@ -1997,7 +1997,7 @@ int q4nx_linear_attn(const q4nx_linear* L, const uint16_t* q, int64_t q_ld, cons
   if (st) return st;
   if (!q || !k || !v || !decay || !state || !state_out || !out) return fail(Q4NX_E_ARG, "linear_attn: null array");
   if (!L->q_start || !L->slots) return fail(Q4NX_E_ARG, "linear_attn: null q_start or slots");
-  const int64_t kc = (int64_t)L->k_heads * L->dk, vc = (int64_t)L->v_heads * L->dv, most = (int64_t)1 << 40;
+  const int64_t kc = (int64_t)L->k_heads * L->dk, vc = (int64_t)L->v_heads * L->dv, most = 1 << 24;
   if (q_ld < kc || k_ld < kc || v_ld < vc || q_ld > most || k_ld > most || v_ld > most)
     return fail(Q4NX_E_SHAPE, "linear_attn: row strides %lld, %lld, %lld below %lld, %lld, %lld columns, or too large",
                 (long long)q_ld, (long long)k_ld, (long long)v_ld, (long long)kc, (long long)kc, (long long)vc);

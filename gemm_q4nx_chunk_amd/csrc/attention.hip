@@ -29,28 +29,6 @@ __device__ __forceinline__ bf16x8 cache8(const void* p, size_t at) {
   else return *reinterpret_cast<const bf16x8*>(static_cast<const uint16_t*>(p) + at);
 }
 
-// N products of which each takes an operand from LDS: read(n) gives it, mul(n, v)
-// uses it.  Four operands are read while the four before them are used; the
-// scheduler, left alone, reads each right before its product and waits.
-template <int N, typename Read, typename Mul>
-__device__ __forceinline__ void fed(Read read, Mul mul) {
-  static_assert(N % 4 == 0, "groups of four");
-  bf16x8 v[2][4];
-#pragma unroll
-  for (int n = 0; n < 4; ++n) v[0][n] = read(n);
-#pragma unroll
-  for (int g = 0; g < N / 4; ++g) {
-    if (g + 1 < N / 4) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n) v[(g + 1) & 1][n] = read(4 * g + 4 + n);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int n = 0; n < 4; ++n) mul(4 * g + n, v[g & 1][n]);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-}
-
 // Four dimensions of a row and head, from d.  A sum of 0 is that of a row that
 // sees nothing (any other has its largest term, 1, or a NaN).
 __device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, int D, int d, f32x4 o, float m, float l) {
@@ -401,7 +379,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_many(AttnArgs a, AttnParts p) {
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int n = 0; n < 16; ++n) st[b][n] = 0.f;
-        fed<NQ * NB>([&](int n) { return *reinterpret_cast<const bf16x8*>(sk + (n % NB) * 32 * D + (n / NB) * 256); },
+        fed<4, NQ * NB>([&](int n) { return *reinterpret_cast<const bf16x8*>(sk + (n % NB) * 32 * D + (n / NB) * 256); },
                      [&](int n, bf16x8 k) {
                        st[n % NB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[n / NB], st[n % NB], 0, 0, 0);
                      });
@@ -456,7 +434,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_many(AttnArgs a, AttnParts p) {
           }
         l_run += sum;
         if (!masked || I8) {
-          fed<NB * 2 * NO>(
+          fed<4, NB * 2 * NO>(
               [&](int n) { return *reinterpret_cast<const bf16x8*>(sv + (n / NO) * 2 * 8 * D + (n % NO) * 256); },
               [&](int n, bf16x8 v) {
                 acc[n % NO] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pf[n / NO / 2][n / NO % 2], acc[n % NO], 0, 0, 0);

@@ -16,6 +16,29 @@ __device__ __forceinline__ void set_flag(uint32_t* flags, uint32_t bit) {
   if (flags) atomicOr(flags, bit);
 }
 
+// N products of which each takes operands from LDS: read(n) gives them, mul(n, v)
+// uses them.  G are read while the G before them are used; the scheduler, left
+// alone, either reads each right before its product and waits, or reads them all
+// and runs out of registers.
+template <int G, int N, typename Read, typename Mul>
+__device__ __forceinline__ void fed(Read read, Mul mul) {
+  static_assert(N % G == 0, "whole groups");
+  decltype(read(0)) v[2][G];
+#pragma unroll
+  for (int n = 0; n < G; ++n) v[0][n] = read(n);
+#pragma unroll
+  for (int g = 0; g < N / G; ++g) {
+    if (g + 1 < N / G) {
+#pragma unroll
+      for (int n = 0; n < G; ++n) v[(g + 1) & 1][n] = read(G * g + G + n);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < G; ++n) mul(G * g + n, v[g & 1][n]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // the paged cache
 // ---------------------------------------------------------------------------

@@ -15,50 +15,42 @@ struct LinearSeq {
   bool fresh;      // begins with zeros
 };
 
-// Sequence s of the call.  Starts that fall count as the largest before them; a
-// slot that an earlier sequence with rows has is none.  All of the workgroup's
-// threads call it; `mem` is LDS of their own.
-__device__ inline LinearSeq linear_seq(const LinearArgs& a, int s, int32_t* mem, bool flags) {
+// Sequence s of the call, whose rows are start..end (kept rising, within the rows).  A slot that an earlier
+// sequence with rows has is none.  All of the workgroup's threads call it; `taken` is LDS of their own.
+__device__ inline LinearSeq linear_seq(const LinearArgs& a, int s, int start, int end, int32_t* taken, bool flags) {
   const int tid = threadIdx.x;
+  if (tid == 0) *taken = 0;
+  const int raw_slot = a.slots[s], fresh = a.fresh ? a.fresh[s] : 0, raw0 = a.q_start[s], raw1 = a.q_start[s + 1];
   __syncthreads();
-  if (tid == 0) {
-    mem[0] = 0;   // the largest start up to s
-    mem[1] = 0;   // and up to s + 1
-    mem[2] = 0;   // the slot is taken
-  }
-  __syncthreads();
-  int up = 0;
-  for (int e = tid; e <= s; e += blockDim.x) {
-    const int raw = a.q_start[e];
-    up = max(up, min(max(raw, 0), a.M));
-  }
-  if (up) atomicMax(&mem[0], up);
-  __syncthreads();
-  const int row0 = mem[0], raw1 = a.q_start[s + 1], row1 = max(row0, min(max(raw1, 0), a.M));
-  const int raw0 = a.q_start[s];
-  const int raw_slot = a.slots[s];
-  bool bad = raw_slot < -1 || raw_slot >= a.n_slots;
-  if (raw_slot >= 0) {
-    // an earlier one with rows: its start rises to the next one's
+  if (raw_slot >= 0)
     for (int e = tid; e < s; e += blockDim.x)
       if (a.slots[e] == raw_slot) {
-        int before = 0;
+        int before = 0;   // rows: its start rises to the next one's
         for (int i = 0; i <= e; ++i) before = max(before, min(max(a.q_start[i], 0), a.M));
-        if (min(max(a.q_start[e + 1], 0), a.M) > before) mem[2] = 1;
+        if (min(max(a.q_start[e + 1], 0), a.M) > before) *taken = 1;
       }
-  }
   __syncthreads();
-  bad |= mem[2] != 0;
+  const bool bad = raw_slot < -1 || raw_slot >= a.n_slots || *taken;
   LinearSeq x;
-  x.row0 = row0;
-  x.rows = row1 - row0;
+  x.row0 = start;
+  x.rows = end - start;
   x.slot = bad ? -1 : raw_slot;
-  x.fresh = x.slot < 0 || (a.fresh && a.fresh[s]);
+  x.fresh = x.slot < 0 || fresh;
   if (flags && tid == 0) {
     if (bad && x.rows) set_flag(a.flags, kFlagIndex);
-    if (raw0 != row0 || raw1 != row1) set_flag(a.flags, kFlagRows);
+    if (raw0 != start || raw1 != end) set_flag(a.flags, kFlagRows);
   }
   return x;
+}
+
+// The largest of the first n + 1 row starts, each within the rows: where sequence n begins.  One wave at least.
+__device__ inline int linear_start(const LinearArgs& a, int n) {
+  const int lane = threadIdx.x & 63;
+  int up = 0;
+  for (int e = lane; e <= n; e += 64) up = max(up, min(max(a.q_start[e], 0), a.M));
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) up = max(up, __shfl_xor(up, off));
+  return up;
 }
 
 // exp of a decay; one above 0 or NaN counts as 0.
@@ -77,13 +69,14 @@ __device__ __forceinline__ float decay_of(const LinearArgs& a, int64_t row, int 
 template <int DK, int DV, int CW>
 __global__ __launch_bounds__(256) void k_linear_rows(LinearArgs a) {
   constexpr int LC = CW / 4, RG = 256 / LC, RP = DK / RG;
-  __shared__ int32_t s_seq[4];
+  __shared__ int32_t s_taken;
   __shared__ float s_q[DK], s_k[DK];
   __shared__ f32x4 s_o[RG][LC];
   const int tid = threadIdx.x, lc = tid % LC, rg = tid / LC;
   constexpr int kParts = DV / CW;
   const int part = blockIdx.x % kParts, h = blockIdx.x / kParts, sq = blockIdx.y;
-  const LinearSeq x = linear_seq(a, sq, s_seq, blockIdx.x == 0);
+  const int start = linear_start(a, sq), end = max(start, min(max(a.q_start[sq + 1], 0), a.M));
+  const LinearSeq x = linear_seq(a, sq, start, end, &s_taken, blockIdx.x == 0);
   if (x.rows == 0) return;
   const int kh = h / (a.v_heads / a.k_heads), col = part * CW + 4 * lc;
   const size_t at = ((size_t)max(x.slot, 0) * a.v_heads + h) * DK * DV + (size_t)rg * RP * DV + col;
@@ -149,6 +142,8 @@ namespace {
 
 constexpr int kChunk = 64;
 
+typedef __attribute__((address_space(3))) void lds_void;
+
 // bf16 parts of x: x = hi + mid + lo to 2^-24 (x below 2^127).
 struct Parts { bf16x8 p[3]; };
 __device__ __forceinline__ Parts parts_of(const float (&x)[8]) {
@@ -168,6 +163,8 @@ __device__ __forceinline__ Parts parts_of(const float (&x)[8]) {
 // The line of a 32-line operand that lane c holds: accumulators 8 t + n of half
 // h are then lines 16 t + 8 h + n.
 __device__ __forceinline__ int dealt(int c) { return 16 * (c >> 4) + 8 * ((c >> 2) & 1) + 4 * ((c >> 3) & 1) + (c & 3); }
+
+__device__ __forceinline__ bf16x8 ld8(const uint16_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
 
 __device__ __forceinline__ bool huge(uint32_t bits) { return (bits & 0x7F800000u) >= 0x7F000000u; }
 __device__ __forceinline__ bool nonfinite2(uint32_t w) {
@@ -213,17 +210,23 @@ __device__ inline void linear_plan(const LinearArgs& a, int32_t* first, int32_t*
 template <int DK, int DV, bool OUT>
 __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
   constexpr int kThreads = 2 * DV, kWaves = DV / 32, NT = DK / 32;
-  // elements: q [DK/8][64][8] | k likewise, then the rows' weights [3][8][64][8] | k^T [8][DK][8] | v^T [8][DV][8]
+  // elements: q [64][DK/8][8] | k likewise, then the rows' weights [3][8][64][8] | k^T [8][DK][8] | v^T [8][DV][8].
+  // Piece p of row r of q and k lies at p ^ turned(r), so that 16 rows' pieces of one column are 16 different
+  // places of the banks.
+  auto turned = [](int r) { return DK == 128 ? r & 15 : (r >> 1) & 7; };
   constexpr int kQ = 0, kK = OUT ? kChunk * DK : 0, kA = OUT ? (kChunk * DK > 3 * kChunk * kChunk ? kChunk * DK : 3 * kChunk * kChunk) : 0;
   constexpr int kKT = kK + kA, kVT = kKT + kChunk * DK;
   extern __shared__ __align__(16) uint16_t lds[];
   __shared__ double s_G[kChunk];
-  __shared__ float s_d[kChunk];
-  __shared__ int32_t s_seq[4];
+  __shared__ float s_d[kChunk], s_since[kChunk];
+  __shared__ __align__(16) float s_left[kChunk];
+  __shared__ int32_t s_taken;
   __shared__ int s_odd[2];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c = lane & 31, hh = lane >> 5;
-  const int h = blockIdx.x % a.v_heads, item = blockIdx.x / a.v_heads, kh = h / (a.v_heads / a.k_heads);
-  int seq, seg;
+  // neighbouring heads, which share q and k, on one XCD (workgroups go round the eight)
+  const int item = blockIdx.x / a.v_heads, nth = blockIdx.x % a.v_heads;
+  const int h = a.v_heads % 8 ? nth : (nth & 7) * (a.v_heads >> 3) + (nth >> 3), kh = h / (a.v_heads / a.k_heads);
+  int seq, seg, start, end;
   {
     int32_t* first = reinterpret_cast<int32_t*>(lds);
     linear_plan(a, first, first + kAttnMaxSeq + 1);
@@ -234,10 +237,11 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
     for (int b = 0; b < a.n_seq; b += 64) count += __popcll(__ballot(b + lane < a.n_seq && first[b + lane] <= item));
     seq = count - 1;
     seg = item - first[seq];
+    start = first[kAttnMaxSeq + 1 + seq];
+    end = first[kAttnMaxSeq + 2 + seq];
     if (!OUT && seg == first[seq + 1] - first[seq] - 1) return;   // what the last one adds, it adds itself
-    __syncthreads();
   }
-  const LinearSeq x = linear_seq(a, seq, s_seq, OUT && h == 0 && seg == 0);
+  const LinearSeq x = linear_seq(a, seq, start, end, &s_taken, OUT && h == 0 && seg == 0);
   const int row0 = x.row0 + seg * a.seg, rows = min(a.seg, x.rows - seg * a.seg);
   const size_t state_size = (size_t)DK * DV;
   // the lane's column and first line of its accumulators
@@ -252,7 +256,7 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int n = 0; n < 16; ++n) S[t][n] = from ? from[(size_t)(32 * t + 16 * (n >> 3) + line0 + (n & 7)) * DV + col] : 0.f;
+      for (int n = 0; n < 16; ++n) S[t][n] = from ? from[(uint32_t)(line0 * DV + col) + (32 * t + 16 * (n >> 3) + (n & 7)) * DV] : 0.f;
   }
   auto state_odd = [&]() {
     bool odd = false;
@@ -264,60 +268,87 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
   };
   double G_all = 0.0;
   bool bad = false;
+  // where the lane's operands lie: all else is an offset in the instruction
+  const uint16_t* const at_w = lds + kK + (hh * kChunk + c) * 8;
+  const int q_row = c * DK, k_row = dealt(c) * DK;
+  int q_turn = 8 * (hh ^ turned(c)), k_turn = 8 * (hh ^ turned(dealt(c)));
+  const uint16_t* const at_kt = lds + kKT + (hh * DK + dealt(c)) * 8;
+  const uint16_t* const at_vt = lds + kVT + (hh * DV + col) * 8;
   if (tid < 2) s_odd[tid] = 0;
   __syncthreads();
   for (int r0 = 0, turn = 0; r0 < rows; r0 += kChunk, turn ^= 1) {
     const int n_rows = min(kChunk, rows - r0);
     const int64_t g0 = row0 + r0;
-    bool odd = state_odd();
-    // operands to LDS; rows behind the last are zeros
+    bool odd = false;
+    // Operands to LDS.  Rows behind the last are the last again: no row's weight reaches them, and their share
+    // of the state is 0.  q's and k's rows go straight there, in whole lines; what is wanted token by token
+    // goes through registers.  No load stands under a branch, so that none waits for another.
+    const int last = n_rows - 1;
     if constexpr (OUT) {
-      for (int u = tid; u < kChunk * DK / 8; u += kThreads) {
-        const int r = (u & 15) | ((u >> 6) / (DK / 32) << 4), ch = ((u >> 4) & 3) + 4 * ((u >> 6) % (DK / 32));
-        u32x4 w = {0u, 0u, 0u, 0u}, y = w;
-        if (r < n_rows) {
-          w = *reinterpret_cast<const u32x4*>(a.q + (g0 + r) * a.q_ld + kh * DK + 8 * ch);
-          y = *reinterpret_cast<const u32x4*>(a.k + (g0 + r) * a.k_ld + kh * DK + 8 * ch);
-        }
+      constexpr int kRow = DK / 8;   // pieces of a row; a wave has 64 pieces at a time, whole rows
 #pragma unroll
-        for (int n = 0; n < 4; ++n) odd |= nonfinite2(w[n]);
-        *reinterpret_cast<u32x4*>(lds + kQ + (ch * kChunk + r) * 8) = w;
-        *reinterpret_cast<u32x4*>(lds + kK + (ch * kChunk + r) * 8) = y;
+      for (int n = 0; n < kRow / kWaves; ++n) {
+        const int piece = (wave * (kRow / kWaves) + n) * 64, r = (piece + lane) / kRow, from = 8 * ((lane % kRow) ^ turned(r));
+        const int row = min(r, last);
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)(a.q + g0 * a.q_ld + kh * DK + (row * (uint32_t)a.q_ld + from)),
+            (lds_void*)(lds + kQ + piece * 8), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)(a.k + g0 * a.k_ld + kh * DK + (row * (uint32_t)a.k_ld + from)),
+            (lds_void*)(lds + kK + piece * 8), 16, 0, 0);
       }
     }
-    auto transpose = [&](const uint16_t* src, int64_t ld, int width, int at) {
-      for (int u = tid; u < 8 * width / 2; u += kThreads) {
+    {
+      constexpr int kK8 = 4 * DK / kThreads, kV8 = 4 * DV / kThreads;
+      uint32_t tk[kK8][8], tv[kV8][8];
+      auto fetch = [&](const uint16_t* src, uint32_t ld, int width, int u, uint32_t (&w)[8]) {
         const int d = 2 * (u % (width / 2)), r = 8 * (u / (width / 2));
-        uint32_t w[8];
 #pragma unroll
-        for (int n = 0; n < 8; ++n) w[n] = r + n < n_rows ? *reinterpret_cast<const uint32_t*>(src + (g0 + r + n) * ld + d) : 0u;
+        for (int n = 0; n < 8; ++n) w[n] = *reinterpret_cast<const uint32_t*>(src + (min(r + n, last) * ld + d));
+      };
+#pragma unroll
+      for (int n = 0; n < kK8; ++n) fetch(a.k + g0 * a.k_ld + kh * DK, (uint32_t)a.k_ld, DK, tid + n * kThreads, tk[n]);
+#pragma unroll
+      for (int n = 0; n < kV8; ++n) fetch(a.v + g0 * a.v_ld + h * DV, (uint32_t)a.v_ld, DV, tid + n * kThreads, tv[n]);
+      if (wave == kWaves - 1) {
+        const float d = decay_of(a, g0 + min(lane, last), h, bad);
+        s_d[lane] = d;
+        // in powers of two; exp of less than -1e5 is 0 in fp32, and sums of these stay exact to 2^-30
+        double G = lane <= last ? (double)fmaxf(d, -1e5f) * 1.4426950408889634 : 0.0;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+          const double o = __shfl_up(G, off);
+          if (lane >= off) G += o;
+        }
+        s_G[lane] = G;
+        s_since[lane] = __builtin_amdgcn_exp2f((float)G);
+        const float left = __builtin_amdgcn_exp2f((float)(__shfl(G, 63) - G));
+        s_left[lane] = lane <= last ? left : 0.f;
+      }
+      auto store = [&](int width, int at, int u, const uint32_t (&w)[8]) {
+        const int d = 2 * (u % (width / 2)), r = 8 * (u / (width / 2));
         u32x4 lo, hi;
 #pragma unroll
+        for (int n = 0; n < 8; ++n) odd |= nonfinite2(w[n]);
+#pragma unroll
         for (int n = 0; n < 4; ++n) {
-          odd |= nonfinite2(w[2 * n]) || nonfinite2(w[2 * n + 1]);
           lo[n] = __builtin_amdgcn_perm(w[2 * n + 1], w[2 * n], 0x05040100u);
           hi[n] = __builtin_amdgcn_perm(w[2 * n + 1], w[2 * n], 0x07060302u);
         }
         uint16_t* to = lds + at + ((r >> 3) * width + d) * 8;
         *reinterpret_cast<u32x4*>(to) = lo;
         *reinterpret_cast<u32x4*>(to + 8) = hi;
-      }
-    };
-    transpose(a.k + kh * DK, a.k_ld, DK, kKT);
-    transpose(a.v + h * DV, a.v_ld, DV, kVT);
-    if (wave == kWaves - 1) {
-      const float d = lane < n_rows ? decay_of(a, g0 + lane, h, bad) : 0.f;
-      s_d[lane] = d;
-      double G = (double)fmaxf(d, -1e5f);   // exp of less is 0 in fp32, and sums of these stay exact to 2^-30
+      };
 #pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const double o = __shfl_up(G, off);
-        if (lane >= off) G += o;
-      }
-      s_G[lane] = G;
+      for (int n = 0; n < kK8; ++n) store(DK, kKT, tid + n * kThreads, tk[n]);
+#pragma unroll
+      for (int n = 0; n < kV8; ++n) store(DV, kVT, tid + n * kThreads, tv[n]);
     }
+    odd |= state_odd();
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     if (odd) s_odd[turn] = 1;
     __syncthreads();
+    asm volatile("" : "+v"(q_turn), "+v"(k_turn));   // or every place is formed ahead of the loop, and spilled
     const bool slow = s_odd[turn] != 0;
     if (tid == 0) s_odd[turn ^ 1] = 0;
     const double G_last = s_G[kChunk - 1];
@@ -335,7 +366,8 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
             const int line = 32 * b + 16 * (n >> 3) + line0 + (n & 7);
             const float kk = bf16lo(lds[kKT + ((t >> 3) * DK + line) * 8 + (t & 7)]);
             S[b][n] = fmaf(kk, v, f == 0.f ? 0.f : f * S[b][n]);
-            if constexpr (OUT) o = fmaf(bf16lo(lds[kQ + ((line >> 3) * kChunk + t) * 8 + (line & 7)]), S[b][n], o);
+            if constexpr (OUT) o = fmaf(bf16lo(lds[kQ + t * DK + 8 * ((line >> 3) ^ turned(t)) + (line & 7)]), S[b][n], o);
+            if ((n & 3) == 3) __builtin_amdgcn_sched_barrier(0);   // or all of the row's operands are read at once, and spill
           }
         if constexpr (OUT) {
           o += __shfl_xor(o, 32);
@@ -355,17 +387,17 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
         if (tile < 3) {
 #pragma unroll
           for (int n = 0; n < 16; ++n) w[m][n] = 0.f;
-#pragma unroll
-          for (int s = 0; s < DK / 16; ++s)
-            w[m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                *reinterpret_cast<const bf16x8*>(lds + kK + ((2 * s + hh) * kChunk + 32 * tj + dealt(c)) * 8),
-                *reinterpret_cast<const bf16x8*>(lds + kQ + ((2 * s + hh) * kChunk + 32 * ti + c) * 8), w[m], 0, 0, 0);
+          struct Pair { bf16x8 k, q; };
+          const uint16_t *kp = lds + kK + k_row + 32 * tj * DK, *qp = lds + kQ + q_row + 32 * ti * DK;
+          fed<2, DK / 16>([&](int s) { return Pair{ld8(kp + (k_turn ^ 16 * s)), ld8(qp + (q_turn ^ 16 * s))}; },
+                          [&](int, const Pair& x) { w[m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.k, x.q, w[m], 0, 0, 0); });
           const int row = 32 * ti + c;
           const double Gi = s_G[row];
+          const double* Gj = s_G + 32 * tj + line0;
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
-            const int j = 32 * tj + 16 * (n >> 3) + line0 + (n & 7);
-            w[m][n] = j <= row ? w[m][n] * expf((float)(Gi - s_G[j])) : 0.f;
+            const int j = 16 * (n >> 3) + (n & 7);
+            w[m][n] = j <= row - 32 * tj - line0 ? w[m][n] * __builtin_amdgcn_exp2f((float)(Gi - Gj[j])) : 0.f;
           }
         }
       }
@@ -373,6 +405,7 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
 #pragma unroll
       for (int m = 0; m < kMine; ++m) {
         const int tile = wave + m * kWaves, ti = tile > 0, tj = tile > 1;
+        uint16_t* to = lds + kK + ((4 * tj + hh) * kChunk + 32 * ti + c) * 8;
         if (tile < 3)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -382,73 +415,87 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
             const Parts q3 = parts_of(f);
 #pragma unroll
             for (int i = 0; i < 3; ++i)
-              *reinterpret_cast<bf16x8*>(lds + kK + i * kChunk * kChunk + ((4 * tj + 2 * t + hh) * kChunk + 32 * ti + c) * 8) = q3.p[i];
+              *reinterpret_cast<bf16x8*>(to + i * kChunk * kChunk + 2 * t * kChunk * 8) = q3.p[i];
           }
       }
+      const float* since = s_since + 4 * hh;
       // q S, scaled by each row's decay since the chunk's beginning
       f32x16 o[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int n = 0; n < 16; ++n) o[i][n] = 0.f;
+      struct Rows { bf16x8 q[2]; };
+      fed<1, 2 * NT>([&](int n) { return Rows{{ld8(lds + kQ + q_row + (q_turn ^ 16 * n)),
+                                               ld8(lds + kQ + q_row + 32 * DK + (q_turn ^ 16 * n))}}; },
+                     [&](int n, const Rows& x) {
+                       float f[8];
 #pragma unroll
-      for (int b = 0; b < NT; ++b)
+                       for (int i = 0; i < 8; ++i) f[i] = S[n >> 1][8 * (n & 1) + i];
+                       const Parts s3 = parts_of(f);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          float f[8];
+                       for (int k = 2; k >= 0; --k)
 #pragma unroll
-          for (int n = 0; n < 8; ++n) f[n] = S[b][8 * t + n];
-          const Parts s3 = parts_of(f);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const bf16x8 q8 = *reinterpret_cast<const bf16x8*>(lds + kQ + ((4 * b + 2 * t + hh) * kChunk + 32 * i + c) * 8);
-#pragma unroll
-            for (int k = 2; k >= 0; --k) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q8, s3.p[k], o[i], 0, 0, 0);
-          }
-        }
+                         for (int i = 0; i < 2; ++i) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.q[i], s3.p[k], o[i], 0, 0, 0);
+                     });
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int n = 0; n < 16; ++n) o[i][n] *= expf((float)s_G[32 * i + 8 * (n >> 2) + 4 * hh + (n & 3)]);
+        for (int n = 0; n < 16; ++n) o[i][n] *= since[32 * i + 8 * (n >> 2) + (n & 3)];
       __syncthreads();
+      // six steps of 16 keys: two of the upper rows, four of the lower
+      struct Step { bf16x8 w[3], v; };
+      fed<1, 6>([&](int n) {
+                  const int i = n > 1, s = i ? n - 2 : n;
+                  Step x;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+                  for (int k = 0; k < 3; ++k) x.w[k] = ld8(at_w + k * kChunk * kChunk + (2 * s * kChunk + 32 * i) * 8);
+                  x.v = ld8(at_vt + 2 * s * DV * 8);
+                  return x;
+                },
+                [&](int n, const Step& x) {
 #pragma unroll
-        for (int s = 0; s < 2 + 2 * i; ++s) {
-          const bf16x8 v8 = *reinterpret_cast<const bf16x8*>(lds + kVT + ((2 * s + hh) * DV + col) * 8);
-#pragma unroll
-          for (int k = 2; k >= 0; --k)
-            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                *reinterpret_cast<const bf16x8*>(lds + kK + k * kChunk * kChunk + ((2 * s + hh) * kChunk + 32 * i + c) * 8), v8, o[i], 0, 0, 0);
-        }
+                  for (int k = 2; k >= 0; --k) o[n > 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.w[k], x.v, o[n > 1], 0, 0, 0);
+                });
+      // byte offsets of 32 bits from the chunk's first row, formed here (hoisted, they would spill)
+      uint8_t* op = reinterpret_cast<uint8_t*>(a.out + (g0 * a.v_heads + h) * DV);
+      uint32_t step = 4u * a.v_heads * DV;
+      asm volatile("" : "+s"(step));
+      const uint32_t off = 4 * hh * step + 4 * col;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
-          const int row = 32 * i + 8 * (n >> 2) + 4 * hh + (n & 3);
-          if (row < n_rows) a.out[((size_t)(g0 + row) * a.v_heads + h) * DV + col] = o[i][n] * a.scale;
+          const int row = 32 * i + 8 * (n >> 2) + (n & 3);
+          if (row + 4 * hh < n_rows) *reinterpret_cast<float*>(op + (off + row * step)) = o[i][n] * a.scale;
         }
     }
     // the state
-    const float f_all = expf((float)G_last);
+    const float f_all = __builtin_amdgcn_exp2f((float)G_last);
 #pragma unroll
     for (int b = 0; b < NT; ++b)
 #pragma unroll
       for (int n = 0; n < 16; ++n) S[b][n] *= f_all;
+    struct Tokens { bf16x8 k[NT], v; f32x4 left[2]; };
+    fed<1, 4>([&](int s) {
+                Tokens x;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const bf16x8 v8 = *reinterpret_cast<const bf16x8*>(lds + kVT + ((2 * s + hh) * DV + col) * 8);
-      float f[8];
+                for (int b = 0; b < NT; ++b) x.k[b] = ld8(at_kt + (2 * s * DK + 32 * b) * 8);
+                x.v = ld8(at_vt + 2 * s * DV * 8);
+                x.left[0] = *reinterpret_cast<const f32x4*>(&s_left[16 * s + 8 * hh]);
+                x.left[1] = *reinterpret_cast<const f32x4*>(&s_left[16 * s + 8 * hh + 4]);
+                return x;
+              },
+              [&](int, const Tokens& x) {
+                float f[8];
 #pragma unroll
-      for (int n = 0; n < 8; ++n) f[n] = (float)v8[n] * expf((float)(G_last - s_G[16 * s + 8 * hh + n]));
-      const Parts v3 = parts_of(f);
+                for (int n = 0; n < 8; ++n) f[n] = (float)x.v[n] * x.left[n >> 2][n & 3];
+                const Parts v3 = parts_of(f);
 #pragma unroll
-      for (int b = 0; b < NT; ++b) {
-        const bf16x8 k8 = *reinterpret_cast<const bf16x8*>(lds + kKT + ((2 * s + hh) * DK + 32 * b + dealt(c)) * 8);
+                for (int k = 2; k >= 0; --k)
 #pragma unroll
-        for (int k = 2; k >= 0; --k) S[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, v3.p[k], S[b], 0, 0, 0);
-      }
-    }
+                  for (int b = 0; b < NT; ++b) S[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x.k[b], v3.p[k], S[b], 0, 0, 0);
+              });
     __syncthreads();   // the operands are done with
   }
   if (bad) set_flag(a.flags, kFlagDecay);
@@ -463,25 +510,25 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int n = 0; n < 16; ++n) to[(size_t)(32 * t + 16 * (n >> 3) + line0 + (n & 7)) * DV + col] = S[t][n];
+      for (int n = 0; n < 16; ++n) to[(uint32_t)(line0 * DV + col) + (32 * t + 16 * (n >> 3) + (n & 7)) * DV] = S[t][n];
 }
 
 // The states that a sequence's segments begin with: what segment s left becomes
 // what segment s + 1 begins with.
 template <int DK, int DV>
 __global__ __launch_bounds__(256) void k_linear_carry(LinearArgs a) {
-  __shared__ int32_t s_seq[4];
+  __shared__ int32_t s_taken;
   constexpr int kParts = DK * DV / 1024;
   const int part = blockIdx.x % kParts, h = blockIdx.x / kParts, seq = blockIdx.y;
   const int first = a.plan[seq], segs = a.plan[seq + 1] - first;
   if (segs < 2) return;
-  const LinearSeq x = linear_seq(a, seq, s_seq, false);
+  const LinearSeq x = linear_seq(a, seq, 0, 0, &s_taken, false);
   const size_t at = (size_t)part * 1024 + 4 * threadIdx.x, size = (size_t)DK * DV;
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   if (!x.fresh) S = *reinterpret_cast<const f32x4*>(a.state + ((size_t)x.slot * a.v_heads + h) * size + at);
   for (int s = 0; s + 1 < segs; ++s) {
     const size_t i = (size_t)(first + s) * a.v_heads + h;
-    const float f = expf((float)a.seg_decay[i]);
+    const float f = __builtin_amdgcn_exp2f((float)a.seg_decay[i]);
     float* p = a.seg_state + i * size + at;
     const f32x4 u = *reinterpret_cast<const f32x4*>(p);
 #pragma unroll

@@ -1774,12 +1774,14 @@ void attn_shape(const q4nx_kv_cache* c, const q4nx_attn_batch* b, int q_heads, i
   const bool apart = b->prefix_len > 0 && b->n_seq > 1 && (int64_t)b->max_q * group < 128;
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   size_t o = 0;
-  auto place = [&](q4nx::AttnParts& p, int set, bool many, int& grid, size_t& plan, size_t& po, size_t& ml) {
+  auto place = [&](q4nx::AttnParts& p, int set, int64_t tile, int& grid, size_t& plan, size_t& po, size_t& ml) {
+    const bool many = tile > 32;
     p.set = set;
-    p.rows = many ? 128 : 16;
-    p.target = many ? 512 : 2048;
-    const int64_t parts = q4nx::attn_max_parts(set, b->n_seq, rows, KH, p.rows, p.target);
-    grid = (int)std::min<int64_t>(parts, many ? 1 << 20 : 1024);
+    p.rows = many ? 128 : tile > 16 ? 32 : 16;
+    p.slots = 512;
+    p.shares = many ? 512 : 2048;
+    const int64_t parts = q4nx::attn_max_parts(p, b->n_seq, rows, KH);
+    grid = (int)std::min<int64_t>(parts, many ? 1 << 20 : 2048);
     plan = o;
     o = up(o + (2 + 2 * (size_t)q4nx::attn_entries(set, b->n_seq)) * 4);
     po = o;
@@ -1787,8 +1789,8 @@ void attn_shape(const q4nx_kv_cache* c, const q4nx_attn_batch* b, int q_heads, i
     ml = o;
     o = up(o + (size_t)parts * p.rows * 8);
   };
-  place(sh.own, apart ? q4nx::ATTN_OWN : q4nx::ATTN_ALL, (int64_t)b->max_q * group > 16, sh.own_grid, sh.own_plan, sh.own_o, sh.own_ml);
-  if (apart) place(sh.pre, q4nx::ATTN_PREFIX, rows > 16, sh.pre_grid, sh.pre_plan, sh.pre_o, sh.pre_ml);
+  place(sh.own, apart ? q4nx::ATTN_OWN : q4nx::ATTN_ALL, (int64_t)b->max_q * group, sh.own_grid, sh.own_plan, sh.own_o, sh.own_ml);
+  if (apart) place(sh.pre, q4nx::ATTN_PREFIX, rows, sh.pre_grid, sh.pre_plan, sh.pre_o, sh.pre_ml);
   sh.total = o;
 }
 

@@ -22,12 +22,27 @@ constexpr float kNegInf = -__builtin_huge_valf();
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-// Eight elements of the cache.
+// Eight elements of the cache, as they come.
 template <bool I8>
-__device__ __forceinline__ bf16x8 cache8(const void* p, size_t at) {
-  if constexpr (I8) return bf16x8_of_codes(*reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(p) + at));
-  else return *reinterpret_cast<const bf16x8*>(static_cast<const uint16_t*>(p) + at);
-}
+struct Raw {
+  u32x4 w;
+  __device__ __forceinline__ void load(const void* p, size_t at) { w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at); }
+  __device__ __forceinline__ bf16x8 get() const { return __builtin_bit_cast(bf16x8, w); }
+  // the first `n` of the eight, and, if `finite`, no infinity or NaN; whether there was one
+  __device__ __forceinline__ bool keep(int n, bool finite) {
+    bf16x8 v = keep_first(get(), n);
+    const bool odd = finite && drop_nonfinite(v);
+    w = __builtin_bit_cast(u32x4, v);
+    return odd;
+  }
+};
+template <>
+struct Raw<true> {
+  u32x2 w;
+  __device__ __forceinline__ void load(const void* p, size_t at) { w = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(p) + at); }
+  __device__ __forceinline__ bf16x8 get() const { return bf16x8_of_codes(w); }
+  __device__ __forceinline__ bool keep(int, bool) { return false; }
+};
 
 // Four dimensions of a row and head, from d.  A sum of 0 is that of a row that
 // sees nothing (any other has its largest term, 1, or a NaN).
@@ -48,175 +63,263 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, int D, 
 
 }  // namespace
 
-// Few rows (up to 16 a tile): a sequence's one row, or a window's, with the
-// query heads of one key head.  The workgroup's four waves take 32 keys each of
-// a unit of 128, with maxima, sums and outputs of their own that are joined at
-// the end, so that a unit's K and V are read once, straight into registers.
-// Bound by memory.
-template <int D, bool I8>
+// Few rows (16 or 32 a tile): a sequence's one row, or a window's, with the query
+// heads of one key head.  The workgroup's four waves take 32 keys each of a unit
+// of 128, with maxima, sums and outputs of their own that are joined at the end,
+// so that a unit's K and V are read once, straight into registers.  The next
+// keys are asked for as soon as the products have taken the last ones, the next
+// values likewise: 16 KB a wave are always on the way.  Bound by memory, so that
+// the softmax's numerators can enter in two bf16 parts, which hold 16 bits.
+template <int D, bool I8, int RB>
 __global__ __launch_bounds__(256) void k_attn_few(AttnArgs a, AttnParts p) {
-  constexpr int kRows = 16, NS = D / 32, NJ = D / 16, kLd = D + 4;
+  constexpr int kRows = 16 * RB, NS = D / 32, NJ = D / 16, kLd = D + 4;
   __shared__ AttnPlan plan;
   __shared__ float s_m[4][kRows], s_l[4][kRows];
-  extern __shared__ __align__(16) float s_o[];   // [4][kRows][kLd]
+  extern __shared__ __align__(16) float s_o[];   // [4][16][kLd]
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c = lane & 15, g = lane >> 4;
-  const int total = attn_plan(a, p, plan), entries = p.set == ATTN_PREFIX ? 1 : a.n_seq;
-  const int KH = a.c.heads;
+  const int KH = a.c.heads, ps = a.c.page_shift;
+  const bool small = a.n_seq <= 64;
+  AttnWavePlan wp;
+  int total;
+  if (small) {
+    wp = attn_wave_plan(a, p);
+    total = wp.total;
+  } else {
+    total = attn_plan(a, p, plan);
+  }
   for (int idx = blockIdx.x; idx < total * KH; idx += gridDim.x) {
     const int head = idx % KH, it = idx / KH;
-    const int e = attn_find(plan, entries, it);
-    const AttnEntry x = attn_entry(a, plan.start, p.set, kRows, e);
-    const int split = max(1, (x.units + plan.per - 1) / plan.per), local = it - plan.first[e];
-    const int part = local % split, rt = local / split;
-    // the lane's row
-    const int r = min(rt * kRows + c, x.rows - 1), r_last = min(rt * kRows + kRows, x.rows) - 1;
-    const int i = r / a.group, h = head * a.group + r % a.group;
+    const AttnPlace at = small ? attn_wave_place(a, p, wp, it) : attn_place(a, p, plan, it);
+    const AttnEntry& x = at.x;
+    const int local = it - at.first, part = local % at.split, rt = local / at.split;
+    // the lane's rows
+    int r[RB], lim_own[RB];
     auto seen = [&](int row) { return min(max(x.causal + row / a.group + 1, 0), x.own); };
-    const int lim_own = seen(r), lim_first = seen(rt * kRows), lim_last = seen(r_last);
+    bf16x8 qf[RB][NS];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      r[b] = min(rt * kRows + 16 * b + c, x.rows - 1);
+      lim_own[b] = seen(r[b]);
+      const uint16_t* qp = a.q + ((size_t)(x.row0 + r[b] / a.group) * a.q_heads + head * a.group + r[b] % a.group) * D + 8 * g;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) qf[b][s] = *reinterpret_cast<const bf16x8*>(qp + 32 * s);
+    }
+    const int lim_first = seen(rt * kRows), lim_last = seen(min(rt * kRows + kRows, x.rows) - 1);
     const int pre_units = attn_units(x.pre), units = pre_units + attn_units(lim_last);
-    const int per = (units + split - 1) / split, u0 = part * per, u1 = min(units, u0 + per);
-    bf16x8 qf[NS];
-    const uint16_t* qp = a.q + ((size_t)(x.row0 + i) * a.q_heads + h) * D + 8 * g;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) qf[s] = *reinterpret_cast<const bf16x8*>(qp + 32 * s);
+    const int per = (units + at.split - 1) / at.split, u0 = part * per, u1 = min(units, u0 + per);
+    const int32_t* own_pages = p.set == ATTN_PREFIX ? nullptr : a.pages + (size_t)at.e * a.pages_ld;
 
-    f32x4 acc[NJ];
+    f32x4 acc[RB][NJ];
+    float m_run[RB], l_run[RB];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m_run = kNegInf, l_run = 0.f;
-    const int32_t* own_pages = p.set == ATTN_PREFIX ? nullptr : a.pages + (size_t)e * a.pages_ld;
-    for (int u = u0; u < u1; ++u) {
-      const bool pre = u < pre_units;
-      const int key0 = (pre ? u : u - pre_units) * kAttnUnit + 32 * wave;
-      const int have = pre ? x.pre : lim_last;   // keys from here on are no row's
-      if (key0 >= have) continue;
-      const int32_t* table = pre ? a.prefix_pages : own_pages;
-      const int ps = a.c.page_shift;
-      // the 16 tokens of each half: their page, and the lane's 8 keys' half
-      size_t at0, at1;
-      const bool ok0 = attn_page(a.c, a.flags, table[key0 >> ps], head, at0);
-      bool ok1 = false;   // a half of no keys reads what is there of the first one's page
-      if (key0 + 16 >= have) at1 = at0;
-      else ok1 = attn_page(a.c, a.flags, table[(key0 + 16) >> ps], head, at1);
-      const int t0 = key0 & ((1 << ps) - 1), t1 = (key0 + 16) & ((1 << ps) - 1);
-      // keys: line c of block b holds token 8 (c / 4) + 4 b + c % 4, in half c / 8
-      const size_t kb = (c & 8 ? at1 + (size_t)t1 * D : at0 + (size_t)t0 * D) + g * 128 +
-                        ((8 * (c >> 2) + (c & 3)) & 15) * 8;
-      const size_t vb = (g & 2 ? at1 + (size_t)t1 * D : at0 + (size_t)t0 * D) +
-                        (size_t)(g & 1) * 8 * D + c * 8;
-      f32x4 st[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-      bf16x8 vf[NJ];
+    for (int b = 0; b < RB; ++b) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[b][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      m_run[b] = kNegInf;
+      l_run[b] = 0.f;
+    }
+
+    // 32 keys: the 16 of each half may lie in pages of their own
+    struct Keys {
+      int u, key0, have;     // keys from `have` on are no row's
+      bool pre, ok0, ok1;
+      size_t at0, at1;       // first elements of the halves' pages, and the tokens there
+      int t0, t1;
+    };
+    auto next_unit = [&](int u) {   // the wave's next unit with keys, from u on
+      if (u < pre_units && u * kAttnUnit + 32 * wave >= x.pre) u = pre_units;
+      return u < u1 && (u < pre_units || (u - pre_units) * kAttnUnit + 32 * wave < lim_last) ? u : u1;
+    };
+    auto keys_of = [&](int u) {
+      Keys k;
+      k.u = u;
+      k.pre = u < pre_units;
+      k.key0 = (k.pre ? u : u - pre_units) * kAttnUnit + 32 * wave;
+      k.have = k.pre ? x.pre : lim_last;
+      const int32_t* table = k.pre ? a.prefix_pages : own_pages;
+      k.ok0 = attn_page(a.c, a.flags, table[k.key0 >> ps], head, k.at0);
+      k.ok1 = false;   // a half of no keys reads what is there of the first one's page
+      if (k.key0 + 16 >= k.have) k.at1 = k.at0;
+      else k.ok1 = attn_page(a.c, a.flags, table[(k.key0 + 16) >> ps], head, k.at1);
+      k.t0 = k.key0 & ((1 << ps) - 1);
+      k.t1 = (k.key0 + 16) & ((1 << ps) - 1);
+      return k;
+    };
+    Raw<I8> kf[2 * NS], vf[NJ];
+    f32x4 ks[I8 ? 2 : 1], vs[I8 ? 2 : 1];
+    auto scales = [&](const float* from, const Keys& k, f32x4* to) {
+      const float* f = from + (g & 2 ? k.at1 / D + k.t1 : k.at0 / D + k.t0) + (g & 1) * 8;
+      to[0] = *reinterpret_cast<const f32x4*>(f);
+      to[1] = *reinterpret_cast<const f32x4*>(f + 4);
+    };
+    // line c of block b holds token 8 (c / 4) + 4 b + c % 4, in half c / 8
+    auto ask_keys = [&](const Keys& k) {
+      const size_t from = (c & 8 ? k.at1 + (size_t)k.t1 * D : k.at0 + (size_t)k.t0 * D) + g * 128 + ((8 * (c >> 2) + (c & 3)) & 15) * 8;
 #pragma unroll
       for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-          st[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(cache8<I8>(a.c.k, kb + s * 512 + b * 32), qf[s], st[b], 0, 0, 0);
+        for (int b = 0; b < 2; ++b) kf[2 * s + b].load(a.c.k, from + s * 512 + b * 32);
+      if constexpr (I8) scales(a.c.ks, k, ks);
+    };
+    auto ask_values = [&](const Keys& k) {
+      const size_t from = (g & 2 ? k.at1 + (size_t)k.t1 * D : k.at0 + (size_t)k.t0 * D) + (size_t)(g & 1) * 8 * D + c * 8;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) vf[j] = cache8<I8>(a.c.v, vb + j * 128);
-      float z[8], vs[8];
+      for (int j = 0; j < NJ; ++j) vf[j].load(a.c.v, from + j * 128);
+      if constexpr (I8) scales(a.c.vs, k, vs);
+    };
+
+    int u = next_unit(u0);
+    Keys cur;
+    if (u < u1) {
+      cur = keys_of(u);
+      ask_keys(cur);
+      ask_values(cur);
+    }
+    while (u < u1) {
+      const int un = next_unit(u + 1);
+      const Keys nxt = un < u1 ? keys_of(un) : cur;   // the last keys are asked for twice: no load stands under a branch
+      f32x4 st[RB][2];
 #pragma unroll
-      for (int n = 0; n < 8; ++n) z[n] = st[n >> 2][n & 3] * a.scale;
-      if constexpr (I8) {
-        const size_t sb = (g & 2 ? at1 / D + t1 : at0 / D + t0) + (g & 1) * 8;
+      for (int b = 0; b < RB; ++b) st[b][0] = st[b][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const bf16x8 k8 = kf[2 * s + n].get();
+#pragma unroll
+          for (int b = 0; b < RB; ++b) st[b][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8, qf[b][s], st[b][n], 0, 0, 0);
+        }
+      float z[RB][8];
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-          z[n] *= a.c.ks[sb + n];
-          vs[n] = a.c.vs[sb + n];
+          z[b][n] = st[b][n >> 2][n & 3] * a.scale;
+          if constexpr (I8) z[b][n] *= ks[n >> 2][n & 3];
+        }
+      __builtin_amdgcn_sched_barrier(0);
+      ask_keys(nxt);
+      __builtin_amdgcn_sched_barrier(0);
+      const int mine = cur.key0 + 8 * g;   // the lane's first key
+      const bool ok = g & 2 ? cur.ok1 : cur.ok0;
+      const bool masked = cur.key0 + 32 > (cur.pre ? x.pre : lim_first) || !cur.ok0 || !cur.ok1;
+      if (masked) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          const int lim = ok ? (cur.pre ? x.pre : lim_own[b]) - mine : 0;
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+            if (n >= lim) z[b][n] = kNegInf;
         }
       }
-      const int mine = key0 + 8 * g;   // the lane's first key
-      const bool ok = g & 2 ? ok1 : ok0;
-      if (key0 + 32 > (pre ? x.pre : lim_first) || !ok0 || !ok1) {
-        const int lim = ok ? (pre ? x.pre : lim_own) - mine : 0, there = ok ? have - mine : 0;
+      bf16x8 hi[RB], lo[RB];
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
-          if (n >= lim) z[n] = kNegInf;
-        if constexpr (!I8) {
+      for (int b = 0; b < RB; ++b) {
+        float top = z[b][0];
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) vf[j] = keep_first(vf[j], there);
-          // an infinity or NaN that only some of the rows see is kept out of the product, which has a 0
-          // for the others, and added to those rows
-          if (!pre && lim_first < lim_last) {
-            bool any = false;
+        for (int n = 1; n < 8; ++n) top = fmaxf(top, z[b][n]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        if (__ballot(top > m_run[b] + 8.f)) {   // as below, in many rows
+          const float m_new = fmaxf(m_run[b], top);
+          const float alpha = __builtin_amdgcn_exp2f(m_run[b] - (m_new == kNegInf ? 0.f : m_new));
+          m_run[b] = m_new;
+          l_run[b] *= alpha;
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) any |= drop_nonfinite(vf[j]);
-            if (__ballot(any)) {
-              for (int n = 0; n < 32 && key0 + n < have; ++n) {
-                const bool half = n & 16;
-                if (!(half ? ok1 : ok0)) continue;
-                const uint16_t* vp = static_cast<const uint16_t*>(a.c.v) + (half ? at1 : at0);
-                const int tok = half ? t1 + (n & 15) : t0 + n;
+          for (int j = 0; j < NJ; ++j) acc[b][j] *= alpha;
+        }
+        const float base = m_run[b] == kNegInf ? 0.f : m_run[b];
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                  for (int d = 0; d < 4; ++d) {
-                    const float v = bf16lo(vp[v_place(D, tok, 16 * j + 4 * g + d)]);
-                    if (!(fabsf(v) <= __FLT_MAX__) && key0 + n < lim_own) acc[j][d] += v;
-                  }
-              }
-            }
-          }
+        for (int n = 0; n < 8; ++n) {
+          float e = __builtin_amdgcn_exp2f(z[b][n] - base);
+          l_run[b] += e;
+          if constexpr (I8) e = z[b][n] == kNegInf ? 0.f : e * vs[n >> 2][n & 3];
+          hi[b][n] = (__bf16)e;
+          lo[b][n] = (__bf16)(e - (float)hi[b][n]);
         }
       }
-      float top = z[0];
+      bool odd = false;
+      if (!I8 && masked) {
+        // values behind the tokens may be anything: 0 instead.  An infinity or NaN that only some of the rows
+        // see is kept out of the product, which has a 0 for the others, and added to those rows.
+        const int there = ok ? cur.have - mine : 0;
+        const bool some = !cur.pre && lim_first < lim_last;
 #pragma unroll
-      for (int n = 1; n < 8; ++n) top = fmaxf(top, z[n]);
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float m_new = fmaxf(m_run, top), base = m_new == kNegInf ? 0.f : m_new;
-      const float alpha = __builtin_amdgcn_exp2f(m_run - base);
-      m_run = m_new;
-      float pr[8], sum = 0.f;
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        pr[n] = __builtin_amdgcn_exp2f(z[n] - base);
-        sum += pr[n];
-        if constexpr (I8) pr[n] = z[n] == kNegInf ? 0.f : pr[n] * vs[n];
+        for (int j = 0; j < NJ; ++j) odd |= vf[j].keep(there, some);
       }
-      l_run = l_run * alpha + sum;
-      const bf16x8 pf = bf16x8_of(pr);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        acc[j] *= alpha;
-        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[j], pf, acc[j], 0, 0, 0);
+        const bf16x8 v8 = vf[j].get();
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          acc[b][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8, lo[b], acc[b][j], 0, 0, 0);
+          acc[b][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8, hi[b], acc[b][j], 0, 0, 0);
+        }
       }
+      if (!I8 && __ballot(odd)) {
+        for (int n = 0; n < 32 && cur.key0 + n < cur.have; ++n) {
+          const bool half = n & 16;
+          if (!(half ? cur.ok1 : cur.ok0)) continue;
+          const uint16_t* vp = static_cast<const uint16_t*>(a.c.v) + (half ? cur.at1 : cur.at0);
+          const int tok = half ? cur.t1 + (n & 15) : cur.t0 + n;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              const float v = bf16lo(vp[v_place(D, tok, 16 * j + 4 * g + d)]);
+#pragma unroll
+              for (int b = 0; b < RB; ++b)
+                if (!(fabsf(v) <= __FLT_MAX__) && cur.key0 + n < lim_own[b]) acc[b][j][d] += v;
+            }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      ask_values(nxt);
+      cur = nxt;
+      u = un;
     }
     // the four waves' parts become one
-    l_run += __shfl_xor(l_run, 16);
-    l_run += __shfl_xor(l_run, 32);
-    __syncthreads();   // the item before has been read
-    if (g == 0) s_m[wave][c] = m_run;
-    __syncthreads();
-    float m_all = s_m[0][c];
-#pragma unroll
-    for (int w = 1; w < 4; ++w) m_all = fmaxf(m_all, s_m[w][c]);
-    const float f = m_all == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m_run - m_all);
-    if (g == 0) s_l[wave][c] = l_run * f;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      *reinterpret_cast<f32x4*>(&s_o[(wave * kRows + c) * kLd + 16 * j + 4 * g]) = acc[j] * f;
-    __syncthreads();
-    const bool whole = split == 1 && p.set == ATTN_ALL;
+    const bool whole = at.split == 1 && p.set == ATTN_ALL;
     const size_t slot = (size_t)it * KH + head;
-    for (int q4 = tid; q4 < kRows * (D / 4); q4 += 256) {
-      const int row = q4 / (D / 4), d = 4 * (q4 % (D / 4)), rr = rt * kRows + row;
-      if (rr >= x.rows) continue;
-      f32x4 o = *reinterpret_cast<const f32x4*>(&s_o[row * kLd + d]);
-      float l = s_l[0][row], m = s_m[0][row];
+    __syncthreads();   // the item before has been read
 #pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        o += *reinterpret_cast<const f32x4*>(&s_o[(w * kRows + row) * kLd + d]);
-        l += s_l[w][row];
-        m = fmaxf(m, s_m[w][row]);
-      }
-      if (whole) {
-        const int qrow = x.row0 + rr / a.group, qh = head * a.group + rr % a.group;
-        write_row(a, ((size_t)qrow * a.q_heads + qh), D, d, o, m, l);
-      } else {
-        *reinterpret_cast<f32x4*>(p.o + (slot * kRows + row) * D + d) = o;
-        if (d == 0) {
-          p.ml[(slot * kRows + row) * 2] = m;
-          p.ml[(slot * kRows + row) * 2 + 1] = l;
+    for (int b = 0; b < RB; ++b) {
+      l_run[b] += __shfl_xor(l_run[b], 16);
+      l_run[b] += __shfl_xor(l_run[b], 32);
+      if (g == 0) s_m[wave][16 * b + c] = m_run[b];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      float m_all = s_m[0][16 * b + c];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) m_all = fmaxf(m_all, s_m[w][16 * b + c]);
+      const float f = m_all == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m_run[b] - m_all);
+      if (g == 0) s_l[wave][16 * b + c] = l_run[b] * f;
+      if (b > 0) __syncthreads();   // the block before has been read
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        *reinterpret_cast<f32x4*>(&s_o[(wave * 16 + c) * kLd + 16 * j + 4 * g]) = acc[b][j] * f;
+      __syncthreads();
+      for (int q4 = tid; q4 < 16 * (D / 4); q4 += 256) {
+        const int row = q4 / (D / 4), d = 4 * (q4 % (D / 4)), tr = 16 * b + row, rr = rt * kRows + tr;
+        if (rr >= x.rows) continue;
+        f32x4 o = *reinterpret_cast<const f32x4*>(&s_o[row * kLd + d]);
+        float l = s_l[0][tr], m = s_m[0][tr];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) {
+          o += *reinterpret_cast<const f32x4*>(&s_o[(w * 16 + row) * kLd + d]);
+          l += s_l[w][tr];
+          m = fmaxf(m, s_m[w][tr]);
+        }
+        if (whole) {
+          write_row(a, (size_t)(x.row0 + rr / a.group) * a.q_heads + head * a.group + rr % a.group, D, d, o, m, l);
+        } else {
+          *reinterpret_cast<f32x4*>(p.o + (slot * kRows + tr) * D + d) = o;
+          if (d == 0) {
+            p.ml[(slot * kRows + tr) * 2] = m;
+            p.ml[(slot * kRows + tr) * 2 + 1] = l;
+          }
         }
       }
     }
@@ -242,8 +345,16 @@ __global__ __launch_bounds__(256, 2) void k_attn_many(AttnArgs a, AttnParts p) {
   __shared__ __align__(16) float s_ks[I8 ? 2 : 1][I8 ? KT : 4], s_vs[I8 ? 2 : 1][I8 ? KT : 4];
   extern __shared__ __align__(16) uint16_t s_kv[];    // [2][K | V]
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c = lane & 31, hh = lane >> 5;
-  const int total = attn_plan(a, p, plan), entries = p.set == ATTN_PREFIX ? 1 : a.n_seq;
   const int KH = a.c.heads, ps = a.c.page_shift;
+  const bool small = a.n_seq <= 64;
+  AttnWavePlan wp;
+  int total;
+  if (small) {
+    wp = attn_wave_plan(a, p);
+    total = wp.total;
+  } else {
+    total = attn_plan(a, p, plan);
+  }
   // -Inf of a key that is not seen stays -Inf under any scale
   const float scale = a.scale == 0.f ? 1e-45f : fabsf(a.scale);
   const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
@@ -252,11 +363,11 @@ __global__ __launch_bounds__(256, 2) void k_attn_many(AttnArgs a, AttnParts p) {
   const int k_at = (line >> 4) * 16 * D + hh * 128 + (line & 15) * 8, v_at = hh * 8 * D + c * 8;
   for (int idx = blockIdx.x; idx < total * KH; idx += gridDim.x) {
     const int head = idx % KH, nth = idx / KH;
-    const int e = attn_find(plan, entries, nth);
-    const AttnEntry x = attn_entry(a, plan.start, p.set, kRows, e);
-    const int split = max(1, (x.units + plan.per - 1) / plan.per);
-    const int local = x.tiles * split - 1 - (nth - plan.first[e]);   // the last tiles see most keys: first
-    const int part = local % split, rt = local / split, it = plan.first[e] + local;
+    const AttnPlace at = small ? attn_wave_place(a, p, wp, nth) : attn_place(a, p, plan, nth);
+    const AttnEntry& x = at.x;
+    const int split = at.split, e = at.e;
+    const int local = x.tiles * split - 1 - (nth - at.first);   // the last tiles see most keys: first
+    const int part = local % split, rt = local / split, it = at.first + local;
     const int r0 = rt * kRows + 32 * wave;
     const bool has_rows = r0 < x.rows;
     const int r = min(r0 + c, x.rows - 1);
@@ -497,13 +608,14 @@ __global__ __launch_bounds__(256, 2) void k_attn_many(AttnArgs a, AttnParts p) {
   }
 }
 
-// The parts of one row and head, joined in order.  32 * D / 128 lanes have four
-// dimensions each; the rest of the workgroup shares the parts.
-template <int D>
+// The parts of one row and head, joined in order.  D / 4 lanes have four
+// dimensions each of a head; with GROUPS > 1 so many of them share the head's
+// parts (few rows, many parts), else a workgroup has several heads of its row.
+template <int D, int GROUPS>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, AttnParts own, AttnParts pre) {
-  constexpr int L = D / 4, kGroups = 256 / L;
-  __shared__ float s_o[kGroups][D + 4];
-  __shared__ float s_l[kGroups];
+  constexpr int L = D / 4, kHeads = 256 / L / GROUPS;
+  __shared__ float s_o[GROUPS > 1 ? GROUPS : 1][D + 4];
+  __shared__ float s_l[GROUPS];
   const int m = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
   // the row's sequence; starts that fall count as the largest before them
   int seq = -1, begin = 0, row0 = 0;
@@ -511,74 +623,93 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, AttnParts own, At
     int up = 0, before = 0;
     for (int b = 0; b <= a.n_seq; b += 64) {
       const int e = b + lane;
-      int v = e <= a.n_seq ? min(max(a.q_start[e], 0), a.M) : 0;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int o = __shfl_up(v, off);
-        if (lane >= off) v = max(v, o);
-      }
-      v = max(v, up);
+      const int v = max(wave_scan_max(e <= a.n_seq ? min(max(a.q_start[e], 0), a.M) : 0), up);
       if (b == 0) row0 = __shfl(v, 0);
-      const uint64_t at = __ballot(e <= a.n_seq && v <= m);
-      const int n = __popcll(at);
+      const int n = __popcll(__ballot(e <= a.n_seq && v <= m));
       if (n) begin = __shfl(v, n - 1);
       before += n;
       up = __shfl(v, 63);
-      if (b + 63 <= a.n_seq && n < 64) break;
+      if (n < 64) break;
     }
     seq = before - 1;
   }
   if (seq < 0 || seq >= a.n_seq) return;   // no sequence's row
   const int i = m - begin, KH = a.c.heads;
   const int split = own.plan[2 + 2 * seq + 1], first = own.plan[2 + 2 * seq];
-  const int pre_split = pre.rows ? pre.plan[3] : 0;
+  const int pre_split = pre.rows ? pre.plan[3] : 0, parts = split + pre_split;
   if (!pre.rows && split == 1) return;     // written by its only part
-  const int grp = tid / L, d = 4 * (tid % L);
-  for (int h = blockIdx.y; h < a.q_heads; h += gridDim.y) {
-    const int head = h / a.group, r = i * a.group + h % a.group, rt = r / own.rows;
-    const size_t slot0 = ((size_t)(first + rt * split) * KH + head) * own.rows + r % own.rows, step = (size_t)KH * own.rows;
-    const int rp = (m - row0) * a.group + h % a.group;
-    const size_t pslot0 = pre.rows ? ((size_t)(rp / pre.rows * pre_split) * KH + head) * pre.rows + rp % pre.rows : 0;
-    const size_t pstep = (size_t)KH * pre.rows;
-    float top = kNegInf;
-    for (int s = lane; s < split + pre_split; s += 64)
-      top = fmaxf(top, s < pre_split ? pre.ml[2 * (pslot0 + s * pstep)] : own.ml[2 * (slot0 + (s - pre_split) * step)]);
+  const int grp = GROUPS > 1 ? tid / L : 0, l0 = tid % L, d = 4 * l0;
+  const int h = GROUPS > 1 ? blockIdx.y : blockIdx.y * kHeads + tid / L;
+  if (GROUPS == 1 && h >= a.q_heads) return;
+  const int head = h / a.group, r = i * a.group + h % a.group, rt = r / own.rows;
+  const size_t slot0 = ((size_t)(first + rt * split) * KH + head) * own.rows + r % own.rows, step = (size_t)KH * own.rows;
+  const int rp = (m - row0) * a.group + h % a.group;
+  const size_t pslot0 = pre.rows ? ((size_t)(rp / pre.rows * pre_split) * KH + head) * pre.rows + rp % pre.rows : 0;
+  const size_t pstep = (size_t)KH * pre.rows;
+  auto ml_of = [&](int s) { return s < pre_split ? pre.ml + 2 * (pslot0 + s * pstep) : own.ml + 2 * (slot0 + (s - pre_split) * step); };
+  auto o_of = [&](int s) {
+    return *reinterpret_cast<const f32x4*>(s < pre_split ? pre.o + (pslot0 + s * pstep) * D + d : own.o + (slot0 + (s - pre_split) * step) * D + d);
+  };
+  constexpr int kSeen = GROUPS > 1 ? 64 : L;   // lanes that look for the maximum together
+  float top = kNegInf;
+  for (int s = lane % kSeen; s < parts; s += kSeen) top = fmaxf(top, ml_of(s)[0]);
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    float l = 0.f;
-    const float base = top == kNegInf ? 0.f : top;
-    for (int s = grp; s < split + pre_split; s += kGroups) {
-      const bool is_pre = s < pre_split;
-      const size_t slot = is_pre ? pslot0 + s * pstep : slot0 + (s - pre_split) * step;
-      const float* ml = (is_pre ? pre.ml : own.ml) + 2 * slot;
-      const float f = __builtin_amdgcn_exp2f(ml[0] - base);
-      l += f * ml[1];
-      o += f * *reinterpret_cast<const f32x4*>((is_pre ? pre.o : own.o) + slot * D + d);
+  for (int off = kSeen / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+  const float base = top == kNegInf ? 0.f : top;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+  int s = grp;
+  for (; s + 3 * GROUPS < parts; s += 4 * GROUPS) {   // four parts on the way at once
+    f32x4 v[4];
+    float f[4], w[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const float* ml = ml_of(s + n * GROUPS);
+      f[n] = ml[0];
+      w[n] = ml[1];
+      v[n] = o_of(s + n * GROUPS);
     }
-    __syncthreads();
-    *reinterpret_cast<f32x4*>(&s_o[grp][d]) = o;
-    if (d == 0) s_l[grp] = l;
-    __syncthreads();
-    if (grp == 0) {
 #pragma unroll
-      for (int w = 1; w < kGroups; ++w) {
-        o += *reinterpret_cast<const f32x4*>(&s_o[w][d]);
-        l += s_l[w];
-      }
-      write_row(a, (size_t)m * a.q_heads + h, D, d, o, top, l);
+    for (int n = 0; n < 4; ++n) {
+      f[n] = __builtin_amdgcn_exp2f(f[n] - base);
+      l += f[n] * w[n];
+      o += f[n] * v[n];
     }
   }
+  for (; s < parts; s += GROUPS) {
+    const float* ml = ml_of(s);
+    const f32x4 v = o_of(s);
+    const float f = __builtin_amdgcn_exp2f(ml[0] - base);
+    l += f * ml[1];
+    o += f * v;
+  }
+  if constexpr (GROUPS > 1) {
+    *reinterpret_cast<f32x4*>(&s_o[grp][d]) = o;
+    if (l0 == 0) s_l[grp] = l;
+    __syncthreads();
+    if (grp > 0) return;
+#pragma unroll
+    for (int w = 1; w < GROUPS; ++w) {
+      o += *reinterpret_cast<const f32x4*>(&s_o[w][d]);
+      l += s_l[w];
+    }
+  }
+  write_row(a, (size_t)m * a.q_heads + h, D, d, o, top, l);
 }
 
 hipError_t launch_attn_few(const AttnArgs& a, const AttnParts& p, int grid, hipStream_t s) {
-  const bool i8 = a.c.ks != nullptr;
-#define Q4NX_FEW(D)                                                                                              \
-  if (i8) hipLaunchKernelGGL((k_attn_few<D, true>), dim3(grid), dim3(256), 4 * 16 * (D + 4) * 4, s, a, p);       \
-  else hipLaunchKernelGGL((k_attn_few<D, false>), dim3(grid), dim3(256), 4 * 16 * (D + 4) * 4, s, a, p)
-  if (a.c.dim == 64) { Q4NX_FEW(64); }
-  else if (a.c.dim == 128) { Q4NX_FEW(128); }
-  else { Q4NX_FEW(256); }
+  const bool i8 = a.c.ks != nullptr, two = p.rows == 32;
+#define Q4NX_FEW(D, I8, RB) \
+  hipLaunchKernelGGL((k_attn_few<D, I8, RB>), dim3(grid), dim3(256), 4 * 16 * (D + 4) * 4, s, a, p)
+#define Q4NX_FEW_D(D)                    \
+  if (i8 && two) Q4NX_FEW(D, true, 2);   \
+  else if (i8) Q4NX_FEW(D, true, 1);     \
+  else if (two) Q4NX_FEW(D, false, 2);   \
+  else Q4NX_FEW(D, false, 1)
+  if (a.c.dim == 64) { Q4NX_FEW_D(64); }
+  else if (a.c.dim == 128) { Q4NX_FEW_D(128); }
+  else { Q4NX_FEW_D(256); }
+#undef Q4NX_FEW_D
 #undef Q4NX_FEW
   return hipGetLastError();
 }
@@ -596,11 +727,17 @@ hipError_t launch_attn_many(const AttnArgs& a, const AttnParts& p, int grid, hip
 }
 
 hipError_t launch_attn_join(const AttnArgs& a, const AttnParts& own, const AttnParts& prefix, hipStream_t s) {
-  // many rows fill the GPU by themselves, and most of them have one part
-  const dim3 grid(a.M, a.M >= 1024 ? 1 : std::min(a.q_heads, 1024 / a.M + 1));
-  if (a.c.dim == 64) hipLaunchKernelGGL(k_attn_join<64>, grid, dim3(256), 0, s, a, own, prefix);
-  else if (a.c.dim == 128) hipLaunchKernelGGL(k_attn_join<128>, grid, dim3(256), 0, s, a, own, prefix);
-  else hipLaunchKernelGGL(k_attn_join<256>, grid, dim3(256), 0, s, a, own, prefix);
+  // from about 64 rows of 32 heads on the heads alone fill the GPU (64 rows, 26 parts: TBD)
+#define Q4NX_JOIN(D)                                                                                                     \
+  if ((int64_t)a.M * a.q_heads < 2048)                                                                                   \
+    hipLaunchKernelGGL((k_attn_join<D, 1024 / D>), dim3(a.M, a.q_heads), dim3(256), 0, s, a, own, prefix);               \
+  else                                                                                                                   \
+    hipLaunchKernelGGL((k_attn_join<D, 1>), dim3(a.M, (a.q_heads + 1024 / D - 1) / (1024 / D)), dim3(256), 0, s, a, own, \
+                       prefix)
+  if (a.c.dim == 64) { Q4NX_JOIN(64); }
+  else if (a.c.dim == 128) { Q4NX_JOIN(128); }
+  else { Q4NX_JOIN(256); }
+#undef Q4NX_JOIN
   return hipGetLastError();
 }
 

@@ -96,7 +96,7 @@ enum AttnSet : int {
   ATTN_PREFIX = 2,   // all rows as one, with the prefix
 };
 
-// What a set's kernel leaves for the join: in ints, total, then each entry's
+// What a set's kernel leaves for the join: from the third int on, each entry's
 // first part and parts a row tile.
 struct AttnParts {
   int32_t* plan;     // [2 + 2 * entries]
@@ -104,7 +104,8 @@ struct AttnParts {
   float* ml;         // [part][tile rows][2]: maximum (log2), sum
   int32_t rows;      // of a tile
   int32_t set;       // AttnSet
-  int32_t target;    // parts that a whole batch is cut into, about
+  int32_t slots;     // workgroups that run at once
+  int32_t shares;    // the shares of a batch of more tiles than half of them
 };
 
 struct AttnArgs {
@@ -123,11 +124,12 @@ struct AttnArgs {
 
 // Entries of a set.
 inline int attn_entries(int set, int n_seq) { return set == ATTN_PREFIX ? 1 : n_seq; }
-// Parts at most: each row tile's last part may be short, and the others make up the target.
-inline int64_t attn_max_parts(int set, int n_seq, int64_t rows, int kv_heads, int tile_rows, int target) {
-  return (rows / tile_rows + attn_entries(set, n_seq)) * kv_heads + target;
+// Parts at most: each row tile's last part may be short, and the others make up the slots or shares.
+inline int64_t attn_max_parts(const AttnParts& p, int n_seq, int64_t rows, int kv_heads) {
+  return (rows / p.rows + attn_entries(p.set, n_seq)) * kv_heads + (p.slots > p.shares ? p.slots : p.shares);
 }
 hipError_t launch_attn_few(const AttnArgs& a, const AttnParts& p, int grid, hipStream_t s);
+// p.rows: 16 or 32
 hipError_t launch_attn_many(const AttnArgs& a, const AttnParts& p, int grid, hipStream_t s);
 // own: the set of the sequences; prefix: of the prefix, or rows = 0
 hipError_t launch_attn_join(const AttnArgs& a, const AttnParts& own, const AttnParts& prefix, hipStream_t s);

@@ -1778,8 +1778,8 @@ void attn_shape(const q4nx_kv_cache* c, const q4nx_attn_batch* b, int q_heads, i
     const bool many = tile > 32;
     p.set = set;
     p.rows = many ? 128 : tile > 16 ? 32 : 16;
-    p.slots = 512;
-    p.shares = many ? 512 : 2048;
+    p.slots = !many ? 512 : c->head_dim == 64 ? 768 : c->head_dim == 128 ? 512 : 256;
+    p.shares = many ? p.slots : 2048;
     const int64_t parts = q4nx::attn_max_parts(p, b->n_seq, rows, KH);
     grid = (int)std::min<int64_t>(parts, many ? 1 << 20 : 2048);
     plan = o;

@@ -11,6 +11,7 @@
 // tokens, which is what one 16-byte piece of the cache's values holds.  So K and
 // V go from memory to the matrix cores as they lie, in whole lines.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_core.h"
 
@@ -337,7 +338,7 @@ __global__ __launch_bounds__(256) void k_attn_few(AttnArgs a, AttnParts p) {
 // by 2^8: numerators up to 2^8 lose nothing in bf16 or in the fp32 sums, and the
 // outputs are rescaled a few times a row instead of once a tile.
 template <int D, bool I8, int KT>
-__global__ __launch_bounds__(256, 2) void k_attn_many(AttnArgs a, AttnParts p) {
+__global__ __launch_bounds__(256, D == 64 ? 3 : D == 256 ? 1 : 2) void k_attn_many(AttnArgs a, AttnParts p) {
   constexpr int kRows = 128, NQ = D / 16, NB = KT / 32, NO = D / 32, kBlocks = KT / 16, kTiles = kAttnUnit / KT;
   constexpr int kTile = KT * D;   // elements of K or V
   __shared__ AttnPlan plan;
@@ -403,41 +404,50 @@ __global__ __launch_bounds__(256, 2) void k_attn_many(AttnArgs a, AttnParts p) {
     constexpr int kRaw = I8 ? KT * D / 16 / 256 : 1;
     u32x4 raw_k[kRaw], raw_v[kRaw];
     float raw_scale = 0.f;
-    const int my_block = kBlocks == 4 ? wave : wave & 1;
+    // the 16-token block of the wave's n-th piece, and of the lane's scale (8 bits)
+    auto block_of = [&](int n) { return I8 ? (wave * 64 + 256 * n) / D : kBlocks == 4 ? wave : wave & 1; };
+    const int scale_block = tid % KT / 16;
     auto page_of = [&](int t, int blk) {   // 0 where nothing is to be loaded
       const bool pre = t < own_begin;
       const int key = (pre ? t : t - own_begin) * KT + 16 * blk, have = pre ? x.pre : lim_last;
       return t < t_end && key < have ? (pre ? a.prefix_pages : own_pages)[key >> ps] : 0;
     };
-    auto issue = [&](int t, int buf, int page) {
+    // pages: of the wave's pieces, asked for a tile ahead, as the loads that need them would wait for them
+    struct Pages { int piece[kRaw], scale; };
+    auto ask_pages = [&](int t) {
+      Pages g;
+#pragma unroll
+      for (int n = 0; n < kRaw; ++n) g.piece[n] = page_of(t, block_of(n));
+      g.scale = I8 ? page_of(t, scale_block) : 0;
+      return g;
+    };
+    auto issue = [&](int t, int buf, const Pages& g) {
       const bool pre = t < own_begin;
       const int key0 = (pre ? t : t - own_begin) * KT, have = pre ? x.pre : lim_last;
       if constexpr (I8) {
 #pragma unroll
         for (int n = 0; n < kRaw; ++n) {
-          const int at = tid + 256 * n, blk = at / D;
-          const int key = key0 + 16 * blk;
-          const int pg = key < have ? (pre ? a.prefix_pages : own_pages)[key >> ps] : 0;
-          const size_t base = kv_page(a.c, (uint32_t)pg < (uint32_t)a.c.n_pages ? pg : 0, head) + (size_t)(key & ((1 << ps) - 1)) * D + (at % D) * 16;
+          const int page = __builtin_amdgcn_readfirstlane(g.piece[n]), key = key0 + 16 * block_of(n);
+          const size_t base = kv_page(a.c, (uint32_t)page < (uint32_t)a.c.n_pages ? page : 0, head) +
+                              (size_t)(key & ((1 << ps) - 1)) * D + ((tid + 256 * n) % D) * 16;
           raw_k[n] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.c.k) + base);
           raw_v[n] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.c.v) + base);
         }
         if (tid < 2 * KT) {
           const int tok = tid % KT, key = key0 + tok;
-          const int pg = key < have ? (pre ? a.prefix_pages : own_pages)[key >> ps] : 0;
-          const bool ok = (uint32_t)pg < (uint32_t)a.c.n_pages;
+          const bool ok = (uint32_t)g.scale < (uint32_t)a.c.n_pages;
           if (!ok) set_flag(a.flags, kFlagIndex);
-          raw_scale = (tid < KT ? a.c.ks : a.c.vs)[((((size_t)(ok ? pg : 0) * KH + head) << ps)) + (key & ((1 << ps) - 1))];
+          raw_scale = (tid < KT ? a.c.ks : a.c.vs)[(((size_t)(ok ? g.scale : 0) * KH + head) << ps) + (key & ((1 << ps) - 1))];
           if (tid < KT && (tok & 15) == 0) s_valid[buf][tok >> 4] = ok ? min(max(have - key, 0), 16) : 0;
         }
       } else {
-        const int key = key0 + 16 * my_block;
+        const int blk = block_of(0), key = key0 + 16 * blk, page = __builtin_amdgcn_readfirstlane(g.piece[0]);
         const bool ok = (uint32_t)page < (uint32_t)a.c.n_pages;
         if (!ok) set_flag(a.flags, kFlagIndex);
-        if ((kBlocks == 4 || wave < 2) && lane == 0) s_valid[buf][my_block] = ok ? min(max(have - key, 0), 16) : 0;
+        if ((kBlocks == 4 || wave < 2) && lane == 0) s_valid[buf][blk] = ok ? min(max(have - key, 0), 16) : 0;
         if (key < have) {
           const size_t at = kv_page(a.c, ok ? page : 0, head) + (size_t)(key & ((1 << ps) - 1)) * D + lane * 8;
-          uint16_t* to = s_kv + buf * 2 * kTile + my_block * 16 * D;
+          uint16_t* to = s_kv + buf * 2 * kTile + blk * 16 * D;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv)
             if (kBlocks == 4 || (wave >> 1) == kv) {
@@ -467,18 +477,18 @@ __global__ __launch_bounds__(256, 2) void k_attn_many(AttnArgs a, AttnParts p) {
     int t = skip(u0 * kTiles);
     __syncthreads();   // the item before is done with LDS
     if (t < t_end) {
-      issue(t, 0, I8 ? 0 : page_of(t, my_block));
+      issue(t, 0, ask_pages(t));
       finish(0);
     }
-    int next = skip(t + 1), page_v = I8 ? 0 : page_of(next, my_block);
+    int next = skip(t + 1);
+    Pages pages = ask_pages(next);
     for (int buf = 0; t < t_end; buf ^= 1) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
-      const int page = __builtin_amdgcn_readfirstlane(page_v);
       const int after = skip(next + 1);
       if (next < t_end) {
-        issue(next, buf ^ 1, page);
-        if (!I8) page_v = page_of(after, my_block);
+        issue(next, buf ^ 1, pages);
+        pages = ask_pages(after);
       }
       const bool pre = t < own_begin;
       const int key0 = (pre ? t : t - own_begin) * KT;
@@ -490,7 +500,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_many(AttnArgs a, AttnParts p) {
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int n = 0; n < 16; ++n) st[b][n] = 0.f;
-        fed<4, NQ * NB>([&](int n) { return *reinterpret_cast<const bf16x8*>(sk + (n % NB) * 32 * D + (n / NB) * 256); },
+        fed<D == 64 ? 2 : 4, NQ * NB>([&](int n) { return *reinterpret_cast<const bf16x8*>(sk + (n % NB) * 32 * D + (n / NB) * 256); },
                      [&](int n, bf16x8 k) {
                        st[n % NB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[n / NB], st[n % NB], 0, 0, 0);
                      });
@@ -538,14 +548,28 @@ __global__ __launch_bounds__(256, 2) void k_attn_many(AttnArgs a, AttnParts p) {
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
-            float e2 = __builtin_amdgcn_exp2f(fmaf(st[b][n], scale, -base));
+            const float e2 = __builtin_amdgcn_exp2f(fmaf(st[b][n], scale, -base));
             sum += e2;
-            if constexpr (I8) e2 = st[b][n] == kNegInf ? 0.f : e2 * s_vs[buf][32 * b + 16 * (n >> 3) + 8 * hh + (n & 7)];
-            pf[b][n >> 3][n & 7] = (__bf16)e2;
+            if constexpr (I8) st[b][n] = e2;
+            else pf[b][n >> 3][n & 7] = (__bf16)e2;
           }
+        if constexpr (I8) {
+          // a token that a row does not see may have any scale
+          auto weigh = [&](auto some) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int n = 0; n < 16; ++n) {
+                const float v = st[b][n] * s_vs[buf][32 * b + 16 * (n >> 3) + 8 * hh + (n & 7)];
+                pf[b][n >> 3][n & 7] = (__bf16)(some && st[b][n] == 0.f ? 0.f : v);
+              }
+          };
+          if (masked) weigh(std::true_type{});
+          else weigh(std::false_type{});
+        }
         l_run += sum;
         if (!masked || I8) {
-          fed<4, NB * 2 * NO>(
+          fed<D == 64 ? 2 : 4, NB * 2 * NO>(
               [&](int n) { return *reinterpret_cast<const bf16x8*>(sv + (n / NO) * 2 * 8 * D + (n % NO) * 256); },
               [&](int n, bf16x8 v) {
                 acc[n % NO] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pf[n / NO / 2][n / NO % 2], acc[n % NO], 0, 0, 0);
@@ -721,7 +745,7 @@ hipError_t launch_attn_many(const AttnArgs& a, const AttnParts& p, int grid, hip
   else hipLaunchKernelGGL((k_attn_many<D, false, KT>), dim3(grid), dim3(256), 2 * 2 * KT * D * 2, s, a, p)
   if (a.c.dim == 64) { Q4NX_MANY(64, 64); }
   else if (a.c.dim == 128) { Q4NX_MANY(128, 64); }
-  else { Q4NX_MANY(256, 32); }
+  else { Q4NX_MANY(256, 64); }
 #undef Q4NX_MANY
   return hipGetLastError();
 }

@@ -1774,14 +1774,13 @@ void attn_shape(const q4nx_kv_cache* c, const q4nx_attn_batch* b, int q_heads, i
   const bool apart = b->prefix_len > 0 && b->n_seq > 1 && (int64_t)b->max_q * group < 128;
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   size_t o = 0;
-  auto place = [&](q4nx::AttnParts& p, int set, int64_t tile, int& grid, size_t& plan, size_t& po, size_t& ml) {
-    const bool many = tile > 32;
+  auto place = [&](q4nx::AttnParts& p, int set, int tile, int slots, int& grid, size_t& plan, size_t& po, size_t& ml) {
     p.set = set;
-    p.rows = many ? 128 : tile > 16 ? 32 : 16;
-    p.slots = !many ? 512 : c->head_dim == 64 ? 768 : c->head_dim == 128 ? 512 : 256;
-    p.shares = many ? p.slots : 2048;
+    p.rows = tile;
+    p.slots = slots;
+    p.shares = tile == 128 ? slots : 1024;
     const int64_t parts = q4nx::attn_max_parts(p, b->n_seq, rows, KH);
-    grid = (int)std::min<int64_t>(parts, many ? 1 << 20 : 2048);
+    grid = (int)std::min<int64_t>(parts, tile == 128 ? 1 << 20 : 2048);
     plan = o;
     o = up(o + (2 + 2 * (size_t)q4nx::attn_entries(set, b->n_seq)) * 4);
     po = o;
@@ -1789,8 +1788,12 @@ void attn_shape(const q4nx_kv_cache* c, const q4nx_attn_batch* b, int q_heads, i
     ml = o;
     o = up(o + (size_t)parts * p.rows * 8);
   };
-  place(sh.own, apart ? q4nx::ATTN_OWN : q4nx::ATTN_ALL, (int64_t)b->max_q * group, sh.own_grid, sh.own_plan, sh.own_o, sh.own_ml);
-  if (apart) place(sh.pre, q4nx::ATTN_PREFIX, rows, sh.pre_grid, sh.pre_plan, sh.pre_o, sh.pre_ml);
+  const int64_t mine = (int64_t)b->max_q * group;
+  const int tile = mine > 32 ? 128 : mine > 16 ? 32 : 16;
+  const int slots = tile < 128 ? 512 : c->head_dim == 64 ? 768 : c->head_dim == 128 ? 512 : 256;
+  place(sh.own, apart ? q4nx::ATTN_OWN : q4nx::ATTN_ALL, tile, slots, sh.own_grid, sh.own_plan, sh.own_o, sh.own_ml);
+  if (apart)
+    place(sh.pre, q4nx::ATTN_PREFIX, rows > 32 ? 128 : tile, 256, sh.pre_grid, sh.pre_plan, sh.pre_o, sh.pre_ml);
   sh.total = o;
 }
 
@@ -1977,11 +1980,7 @@ int q4nx_attention(const q4nx_kv_cache* cache, const q4nx_attn_batch* batch, con
   at(sh.own, sh.own_plan, sh.own_o, sh.own_ml);
   if (sh.pre.rows) at(sh.pre, sh.pre_plan, sh.pre_o, sh.pre_ml);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  auto launch = [&](const q4nx::AttnParts& p, int grid) {
-    return p.rows == 128 ? q4nx::launch_attn_many(a, p, grid, s) : q4nx::launch_attn_few(a, p, grid, s);
-  };
-  hipError_t e = launch(sh.own, sh.own_grid);
-  if (e == hipSuccess && sh.pre.rows) e = launch(sh.pre, sh.pre_grid);
+  hipError_t e = q4nx::launch_attn(a, sh.own, sh.own_grid, sh.pre, sh.pre_grid, s);
   if (e == hipSuccess) e = q4nx::launch_attn_join(a, sh.own, sh.pre, s);
   return hip_status(e, "attention launch");
 }

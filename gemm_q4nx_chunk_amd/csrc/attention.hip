@@ -30,9 +30,9 @@ struct Raw {
   __device__ __forceinline__ void load(const void* p, size_t at) { w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at); }
   __device__ __forceinline__ bf16x8 get() const { return __builtin_bit_cast(bf16x8, w); }
   // the first `n` of the eight, and, if `finite`, no infinity or NaN; whether there was one
-  __device__ __forceinline__ bool keep(int n, bool finite) {
+  __device__ __forceinline__ uint32_t keep(int n, bool finite) {
     bf16x8 v = keep_first(get(), n);
-    const bool odd = finite && drop_nonfinite(v);
+    const uint32_t odd = finite ? drop_nonfinite(v) : 0u;
     w = __builtin_bit_cast(u32x4, v);
     return odd;
   }
@@ -42,7 +42,7 @@ struct Raw<true> {
   u32x2 w;
   __device__ __forceinline__ void load(const void* p, size_t at) { w = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(p) + at); }
   __device__ __forceinline__ bf16x8 get() const { return bf16x8_of_codes(w); }
-  __device__ __forceinline__ bool keep(int, bool) { return false; }
+  __device__ __forceinline__ uint32_t keep(int, bool) { return 0u; }
 };
 
 // Four dimensions of a row and head, from d.  A sum of 0 is that of a row that
@@ -72,25 +72,16 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, int D, 
 // values likewise: 16 KB a wave are always on the way.  Bound by memory, so that
 // the softmax's numerators can enter in two bf16 parts, which hold 16 bits.
 template <int D, bool I8, int RB>
-__global__ __launch_bounds__(256) void k_attn_few(AttnArgs a, AttnParts p) {
+__device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, int block, int blocks, AttnPlan& plan, uint8_t* lds) {
   constexpr int kRows = 16 * RB, NS = D / 32, NJ = D / 16, kLd = D + 4;
-  __shared__ AttnPlan plan;
   __shared__ float s_m[4][kRows], s_l[4][kRows];
-  extern __shared__ __align__(16) float s_o[];   // [4][16][kLd]
+  float* const s_o = reinterpret_cast<float*>(lds);   // [4][16][kLd]
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c = lane & 15, g = lane >> 4;
   const int KH = a.c.heads, ps = a.c.page_shift;
-  const bool small = a.n_seq <= 64;
-  AttnWavePlan wp;
-  int total;
-  if (small) {
-    wp = attn_wave_plan(a, p);
-    total = wp.total;
-  } else {
-    total = attn_plan(a, p, plan);
-  }
-  for (int idx = blockIdx.x; idx < total * KH; idx += gridDim.x) {
+  const int total = attn_plan(a, p, plan, block == 0);
+  for (int idx = block; idx < total * KH; idx += blocks) {
     const int head = idx % KH, it = idx / KH;
-    const AttnPlace at = small ? attn_wave_place(a, p, wp, it) : attn_place(a, p, plan, it);
+    const AttnPlace at = attn_place(a, p, plan, it);
     const AttnEntry& x = at.x;
     const int local = it - at.first, part = local % at.split, rt = local / at.split;
     // the lane's rows
@@ -239,7 +230,7 @@ __global__ __launch_bounds__(256) void k_attn_few(AttnArgs a, AttnParts p) {
           lo[b][n] = (__bf16)(e - (float)hi[b][n]);
         }
       }
-      bool odd = false;
+      uint32_t odd = 0;
       if (!I8 && masked) {
         // values behind the tokens may be anything: 0 instead.  An infinity or NaN that only some of the rows
         // see is kept out of the product, which has a 0 for the others, and added to those rows.
@@ -257,7 +248,7 @@ __global__ __launch_bounds__(256) void k_attn_few(AttnArgs a, AttnParts p) {
           acc[b][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8, hi[b], acc[b][j], 0, 0, 0);
         }
       }
-      if (!I8 && __ballot(odd)) {
+      if (!I8 && __ballot(odd != 0)) {
         for (int n = 0; n < 32 && cur.key0 + n < cur.have; ++n) {
           const bool half = n & 16;
           if (!(half ? cur.ok1 : cur.ok0)) continue;
@@ -271,6 +262,7 @@ __global__ __launch_bounds__(256) void k_attn_few(AttnArgs a, AttnParts p) {
 #pragma unroll
               for (int b = 0; b < RB; ++b)
                 if (!(fabsf(v) <= __FLT_MAX__) && cur.key0 + n < lim_own[b]) acc[b][j][d] += v;
+              if (d == 3) __builtin_amdgcn_sched_barrier(0);   // or all are read at once, and spill others
             }
         }
       }
@@ -338,33 +330,25 @@ __global__ __launch_bounds__(256) void k_attn_few(AttnArgs a, AttnParts p) {
 // by 2^8: numerators up to 2^8 lose nothing in bf16 or in the fp32 sums, and the
 // outputs are rescaled a few times a row instead of once a tile.
 template <int D, bool I8, int KT>
-__global__ __launch_bounds__(256, D == 64 ? 3 : D == 256 ? 1 : 2) void k_attn_many(AttnArgs a, AttnParts p) {
+__device__ __forceinline__ void attn_many(const AttnArgs& a, const AttnParts& p, int block, int blocks, AttnPlan& plan, uint8_t* lds) {
   constexpr int kRows = 128, NQ = D / 16, NB = KT / 32, NO = D / 32, kBlocks = KT / 16, kTiles = kAttnUnit / KT;
   constexpr int kTile = KT * D;   // elements of K or V
-  __shared__ AttnPlan plan;
   __shared__ __align__(16) int32_t s_valid[2][4];     // tokens that count of each 16
+  __shared__ int32_t s_odd;
   __shared__ __align__(16) float s_ks[I8 ? 2 : 1][I8 ? KT : 4], s_vs[I8 ? 2 : 1][I8 ? KT : 4];
-  extern __shared__ __align__(16) uint16_t s_kv[];    // [2][K | V]
+  uint16_t* const s_kv = reinterpret_cast<uint16_t*>(lds);   // [2][K | V]
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c = lane & 31, hh = lane >> 5;
   const int KH = a.c.heads, ps = a.c.page_shift;
-  const bool small = a.n_seq <= 64;
-  AttnWavePlan wp;
-  int total;
-  if (small) {
-    wp = attn_wave_plan(a, p);
-    total = wp.total;
-  } else {
-    total = attn_plan(a, p, plan);
-  }
+  const int total = attn_plan(a, p, plan, block == 0);
   // -Inf of a key that is not seen stays -Inf under any scale
   const float scale = a.scale == 0.f ? 1e-45f : fabsf(a.scale);
   const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
   // where the lane's operands lie in a tile
   const int line = 16 * ((c >> 3) >> 1) + 8 * ((c >> 2) & 1) + 4 * ((c >> 3) & 1) + (c & 3);
   const int k_at = (line >> 4) * 16 * D + hh * 128 + (line & 15) * 8, v_at = hh * 8 * D + c * 8;
-  for (int idx = blockIdx.x; idx < total * KH; idx += gridDim.x) {
+  for (int idx = block; idx < total * KH; idx += blocks) {
     const int head = idx % KH, nth = idx / KH;
-    const AttnPlace at = small ? attn_wave_place(a, p, wp, nth) : attn_place(a, p, plan, nth);
+    const AttnPlace at = attn_place(a, p, plan, nth);
     const AttnEntry& x = at.x;
     const int split = at.split, e = at.e;
     const int local = x.tiles * split - 1 - (nth - at.first);   // the last tiles see most keys: first
@@ -375,7 +359,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : D == 256 ? 1 : 2) void k_attn_ma
     const int i = r / a.group, h = head * a.group + r % a.group;
     auto seen = [&](int row) { return min(max(x.causal + row / a.group + 1, 0), x.own); };
     const int lim_own = seen(r), lim_first = seen(min(r0, x.rows - 1)), lim_wave = seen(min(r0 + 31, x.rows - 1));
-    const int lim_last = seen(min(rt * kRows + kRows, x.rows) - 1);
+    const int lim_tile = seen(rt * kRows), lim_last = seen(min(rt * kRows + kRows, x.rows) - 1);
     const int pre_units = attn_units(x.pre), units = pre_units + attn_units(lim_last);
     const int per = (units + split - 1) / split, u0 = part * per, u1 = min(units, u0 + per);
     // tiles: [0, pre_end) of the prefix, [own_begin, own_end) of the sequence's own
@@ -492,6 +476,32 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : D == 256 ? 1 : 2) void k_attn_ma
       }
       const bool pre = t < own_begin;
       const int key0 = (pre ? t : t - own_begin) * KT;
+      int valid[kBlocks], least = 16;
+#pragma unroll
+      for (int n = 0; n < kBlocks; ++n) {
+        valid[n] = __builtin_amdgcn_readfirstlane(s_valid[buf][n]);
+        least = min(least, valid[n]);
+      }
+      // A tile that some rows do not see whole: values behind the tokens may be anything, and an infinity or NaN of
+      // a token would reach the rows that do not see it, as a product with 0.  Both become 0 here, and the rows
+      // that do see it get it below.
+      bool odd = false;
+      if (!I8 && (least < 16 || (!pre && key0 + KT > lim_tile))) {
+        if (tid == 0) s_odd = 0;
+        __syncthreads();
+        uint32_t any = 0;
+#pragma unroll
+        for (int n = 0; n < kTile / 8 / 256; ++n) {
+          const int grp = (tid + 256 * n) / D;
+          bf16x8* at = reinterpret_cast<bf16x8*>(s_kv + buf * 2 * kTile + kTile) + tid + 256 * n;
+          bf16x8 v = keep_first(*at, s_valid[buf][grp >> 1] - 8 * (grp & 1));
+          any |= drop_nonfinite(v);
+          *at = v;
+        }
+        if (any) s_odd = 1;
+        __syncthreads();
+        odd = __builtin_amdgcn_readfirstlane(s_odd) != 0;
+      }
       if (has_rows && (pre || key0 < lim_wave)) {
         const uint16_t* sk = s_kv + buf * 2 * kTile + k_at;
         const uint16_t* sv = s_kv + buf * 2 * kTile + kTile + v_at;
@@ -504,12 +514,6 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : D == 256 ? 1 : 2) void k_attn_ma
                      [&](int n, bf16x8 k) {
                        st[n % NB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[n / NB], st[n % NB], 0, 0, 0);
                      });
-        int valid[kBlocks], least = 16;
-#pragma unroll
-        for (int n = 0; n < kBlocks; ++n) {
-          valid[n] = __builtin_amdgcn_readfirstlane(s_valid[buf][n]);
-          least = min(least, valid[n]);
-        }
         if constexpr (I8) {
 #pragma unroll
           for (int b = 0; b < NB; ++b)
@@ -545,7 +549,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : D == 256 ? 1 : 2) void k_attn_ma
         float sum = 0.f;
         bf16x8 pf[NB][2];
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < NB; ++b) {
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
             const float e2 = __builtin_amdgcn_exp2f(fmaf(st[b][n], scale, -base));
@@ -553,6 +557,8 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : D == 256 ? 1 : 2) void k_attn_ma
             if constexpr (I8) st[b][n] = e2;
             else pf[b][n >> 3][n & 7] = (__bf16)e2;
           }
+          __builtin_amdgcn_sched_barrier(0);   // or the values' reads come ahead of all this, and registers spill
+        }
         if constexpr (I8) {
           // a token that a row does not see may have any scale
           auto weigh = [&](auto some) {
@@ -568,40 +574,28 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : D == 256 ? 1 : 2) void k_attn_ma
           else weigh(std::false_type{});
         }
         l_run += sum;
-        if (!masked || I8) {
-          fed<D == 64 ? 2 : 4, NB * 2 * NO>(
-              [&](int n) { return *reinterpret_cast<const bf16x8*>(sv + (n / NO) * 2 * 8 * D + (n % NO) * 256); },
-              [&](int n, bf16x8 v) {
-                acc[n % NO] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pf[n / NO / 2][n / NO % 2], acc[n % NO], 0, 0, 0);
-              });
-        } else {
-          // values behind the tokens may be anything: 0 instead.  An infinity or NaN that only some of the
-          // rows see is kept out of the product, which has a 0 for the others, and added to those rows.
-          bool any = false;
+        fed<D == 64 ? 2 : 4, NB * 2 * NO>(
+            [&](int n) { return *reinterpret_cast<const bf16x8*>(sv + (n / NO) * 2 * 8 * D + (n % NO) * 256); },
+            [&](int n, bf16x8 v) {
+              acc[n % NO] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pf[n / NO / 2][n / NO % 2], acc[n % NO], 0, 0, 0);
+            });
+        if (odd) {
+          int h4 = 4 * hh;
+          asm volatile("" : "+v"(h4));   // or the places below are formed ahead of the loops, and spilled
+          for (int n = 0; n < KT; ++n) {
+            if ((n & 15) >= s_valid[buf][n >> 4]) continue;
+            const int key = key0 + n;
+            const uint16_t* vp = static_cast<const uint16_t*>(a.c.v) +
+                                 kv_page(a.c, (pre ? a.prefix_pages : own_pages)[key >> ps], head);   // a page of the cache
+            const bool mine = key < (pre ? x.pre : lim_own);
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
+            for (int o = 0; o < NO; ++o)
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-              for (int o = 0; o < NO; ++o) {
-                bf16x8 v = keep_first(*reinterpret_cast<const bf16x8*>(sv + (4 * b + 2 * s) * 8 * D + o * 256),
-                                      valid[2 * b + s] - 8 * hh);
-                any |= drop_nonfinite(v);
-                acc[o] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pf[b][s], acc[o], 0, 0, 0);
+              for (int d = 0; d < 16; ++d) {
+                const float v = bf16lo(vp[v_place(D, key & ((1 << ps) - 1), 32 * o + 8 * (d >> 2) + h4 + (d & 3))]);
+                if (!(fabsf(v) <= __FLT_MAX__) && mine) acc[o][d] += v;
+                if ((d & 3) == 3) __builtin_amdgcn_sched_barrier(0);   // or all are read at once, and spill others
               }
-          if (__ballot(any)) {
-            const uint16_t* tile = s_kv + buf * 2 * kTile + kTile;
-            for (int n = 0; n < KT; ++n) {
-              if ((n & 15) >= s_valid[buf][n >> 4]) continue;
-              const bool mine = key0 + n < (pre ? x.pre : lim_own);
-#pragma unroll
-              for (int o = 0; o < NO; ++o)
-#pragma unroll
-                for (int d = 0; d < 16; ++d) {
-                  const float v = bf16lo(tile[v_place(D, n, 32 * o + 8 * (d >> 2) + 4 * hh + (d & 3))]);
-                  if (!(fabsf(v) <= __FLT_MAX__) && mine) acc[o][d] += v;
-                }
-            }
           }
         }
       }
@@ -610,11 +604,13 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : D == 256 ? 1 : 2) void k_attn_ma
       next = after;
     }
     l_run += __shfl_xor(l_run, 32);
-    const int rr = r0 + c;
+    int mine = r0 + c;
+    asm volatile("" : "+v"(mine));   // the row's place is formed again here, not kept over the tiles
+    const int rr = mine;
     if (rr < x.rows) {
       const bool whole = split == 1 && p.set == ATTN_ALL;
       const size_t slot = ((size_t)it * KH + head) * kRows + 32 * wave + c;
-      const size_t row = (size_t)(x.row0 + i) * a.q_heads + h;
+      const size_t row = (size_t)(x.row0 + rr / a.group) * a.q_heads + head * a.group + rr % a.group;
 #pragma unroll
       for (int o = 0; o < NO; ++o)
 #pragma unroll
@@ -630,6 +626,40 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : D == 256 ? 1 : 2) void k_attn_ma
       }
     }
   }
+}
+
+constexpr int attn_lds(int dim, int rows) { return rows == 128 ? 2 * 2 * 64 * dim * 2 : 4 * 16 * (dim + 4) * 4; }
+
+// Registers for three workgroups a CU at 64 dimensions, two at 128, one at 256.
+constexpr int attn_occupancy(int dim, int rows) { return dim == 256 ? 1 : dim == 64 && rows != 32 ? 3 : 2; }
+
+template <int D, bool I8, int ROWS>
+__device__ __forceinline__ void attn_rows(const AttnArgs& a, const AttnParts& p, int block, int blocks, AttnPlan& plan, uint8_t* lds) {
+  if constexpr (ROWS == 128) attn_many<D, I8, 64>(a, p, block, blocks, plan, lds);
+  else attn_few<D, I8, ROWS / 16>(a, p, block, blocks, plan, lds);
+}
+
+template <int D, bool I8, int ROWS>
+__global__ __launch_bounds__(256, attn_occupancy(D, ROWS)) void k_attn(AttnArgs a, AttnParts p) {
+  __shared__ AttnPlan plan;
+  extern __shared__ __align__(16) uint8_t lds[];
+  attn_rows<D, I8, ROWS>(a, p, blockIdx.x, gridDim.x, plan, lds);
+}
+
+// Several sequences behind a prefix, in one launch: pre_grid workgroups have the
+// prefix's parts (tiles of PRE rows), the others the sequences' (OWN rows).  Side
+// by side, the prefix's products fill the matrix cores while the sequences' keys
+// and values stream (16 windows over 8 bits: 45 us, one after the other 71; 64
+// tokens behind 8192: 97 for 109).
+template <int D, bool I8, int OWN, int PRE>
+__global__ __launch_bounds__(256, attn_occupancy(D, OWN)) void k_attn_shared(AttnArgs a, AttnPair sets, int pre_grid) {
+  __shared__ AttnPlan plan;
+  extern __shared__ __align__(16) uint8_t lds[];
+  const bool is_pre = (int)blockIdx.x < pre_grid;
+  const int block = is_pre ? blockIdx.x : blockIdx.x - pre_grid, blocks = is_pre ? pre_grid : gridDim.x - pre_grid;
+  if constexpr (OWN == PRE) attn_rows<D, I8, OWN>(a, sets.p[is_pre], block, blocks, plan, lds);
+  else if (is_pre) attn_rows<D, I8, PRE>(a, sets.p[1], block, blocks, plan, lds);
+  else attn_rows<D, I8, OWN>(a, sets.p[0], block, blocks, plan, lds);
 }
 
 // The parts of one row and head, joined in order.  D / 4 lanes have four
@@ -721,32 +751,33 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, AttnParts own, At
   write_row(a, (size_t)m * a.q_heads + h, D, d, o, top, l);
 }
 
-hipError_t launch_attn_few(const AttnArgs& a, const AttnParts& p, int grid, hipStream_t s) {
-  const bool i8 = a.c.ks != nullptr, two = p.rows == 32;
-#define Q4NX_FEW(D, I8, RB) \
-  hipLaunchKernelGGL((k_attn_few<D, I8, RB>), dim3(grid), dim3(256), 4 * 16 * (D + 4) * 4, s, a, p)
-#define Q4NX_FEW_D(D)                    \
-  if (i8 && two) Q4NX_FEW(D, true, 2);   \
-  else if (i8) Q4NX_FEW(D, true, 1);     \
-  else if (two) Q4NX_FEW(D, false, 2);   \
-  else Q4NX_FEW(D, false, 1)
-  if (a.c.dim == 64) { Q4NX_FEW_D(64); }
-  else if (a.c.dim == 128) { Q4NX_FEW_D(128); }
-  else { Q4NX_FEW_D(256); }
-#undef Q4NX_FEW_D
-#undef Q4NX_FEW
-  return hipGetLastError();
+template <int D, bool I8>
+static void launch_attn_of(const AttnArgs& a, const AttnParts& own, int own_grid, const AttnParts& pre, int pre_grid, hipStream_t s) {
+#define Q4NX_ONE(ROWS) hipLaunchKernelGGL((k_attn<D, I8, ROWS>), dim3(own_grid), dim3(256), attn_lds(D, ROWS), s, a, own)
+#define Q4NX_SHARED(OWN, PRE)                                                                    \
+  hipLaunchKernelGGL((k_attn_shared<D, I8, OWN, PRE>), dim3(pre_grid + own_grid), dim3(256),     \
+                     std::max(attn_lds(D, OWN), attn_lds(D, PRE)), s, a, (AttnPair{{own, pre}}), pre_grid)
+  if (pre.rows == 0) {
+    if (own.rows == 128) Q4NX_ONE(128);
+    else if (own.rows == 32) Q4NX_ONE(32);
+    else Q4NX_ONE(16);
+  } else if (own.rows == 128) Q4NX_SHARED(128, 128);
+  else if (own.rows == 32 && pre.rows == 32) Q4NX_SHARED(32, 32);
+  else if (own.rows == 32) Q4NX_SHARED(32, 128);
+  else if (pre.rows == 16) Q4NX_SHARED(16, 16);
+  else Q4NX_SHARED(16, 128);
+#undef Q4NX_ONE
+#undef Q4NX_SHARED
 }
 
-hipError_t launch_attn_many(const AttnArgs& a, const AttnParts& p, int grid, hipStream_t s) {
-  const bool i8 = a.c.ks != nullptr;
-#define Q4NX_MANY(D, KT)                                                                                         \
-  if (i8) hipLaunchKernelGGL((k_attn_many<D, true, KT>), dim3(grid), dim3(256), 2 * 2 * KT * D * 2, s, a, p);    \
-  else hipLaunchKernelGGL((k_attn_many<D, false, KT>), dim3(grid), dim3(256), 2 * 2 * KT * D * 2, s, a, p)
-  if (a.c.dim == 64) { Q4NX_MANY(64, 64); }
-  else if (a.c.dim == 128) { Q4NX_MANY(128, 64); }
-  else { Q4NX_MANY(256, 64); }
-#undef Q4NX_MANY
+hipError_t launch_attn(const AttnArgs& a, const AttnParts& own, int own_grid, const AttnParts& pre, int pre_grid, hipStream_t s) {
+#define Q4NX_ATTN(D)                                                    \
+  if (a.c.ks) launch_attn_of<D, true>(a, own, own_grid, pre, pre_grid, s); \
+  else launch_attn_of<D, false>(a, own, own_grid, pre, pre_grid, s)
+  if (a.c.dim == 64) { Q4NX_ATTN(64); }
+  else if (a.c.dim == 128) { Q4NX_ATTN(128); }
+  else { Q4NX_ATTN(256); }
+#undef Q4NX_ATTN
   return hipGetLastError();
 }
 

@@ -12,6 +12,7 @@ namespace q4nx {
 struct AttnPlan {
   int32_t start[kAttnMaxSeq + 1];   // first row of each sequence: rising, in 0..M
   int32_t first[kAttnMaxSeq + 1];   // first part of each entry
+  int32_t own[kAttnMaxSeq];         // tokens of each sequence, within its pages
   int32_t per;                      // units of keys in a part
   int64_t sums[4];                  // of the waves
 };
@@ -26,7 +27,7 @@ struct AttnEntry {
 
 __device__ __forceinline__ int attn_units(int keys) { return (keys + kAttnUnit - 1) / kAttnUnit; }
 
-__device__ __forceinline__ AttnEntry attn_entry(const AttnArgs& a, const int32_t* start, int set, int tile_rows, int e) {
+__device__ __forceinline__ AttnEntry attn_entry(const AttnArgs& a, const int32_t* start, const int32_t* own, int set, int tile_rows, int e) {
   AttnEntry x;
   if (set == ATTN_PREFIX) {
     x.row0 = start[0];
@@ -38,9 +39,7 @@ __device__ __forceinline__ AttnEntry attn_entry(const AttnArgs& a, const int32_t
     const int n = start[e + 1] - start[e];
     x.row0 = start[e];
     x.rows = n * a.group;
-    const int64_t most = (int64_t)a.pages_ld << a.c.page_shift;
-    const int have = a.kv_len[e];
-    x.own = max(0, (int)min((int64_t)have, most));
+    x.own = own[e];
     x.pre = set == ATTN_ALL ? a.prefix_len : 0;
     x.causal = x.own - n;
   }
@@ -82,8 +81,11 @@ __device__ __forceinline__ T scan256(T v, int64_t* sums, T& total) {
   return MAX ? max(v, before) : v + before;
 }
 
-// Fills the plan; returns the parts of one key head.  All 256 threads call it.
-__device__ inline int attn_plan(const AttnArgs& a, const AttnParts& p, AttnPlan& s) {
+// Fills the plan; returns the parts of one key head.  All 256 threads call it; the set's first workgroup writes
+// what the join needs.
+__device__ inline int attn_plan_small(const AttnArgs& a, const AttnParts& p, AttnPlan& s, bool first);
+__device__ inline int attn_plan(const AttnArgs& a, const AttnParts& p, AttnPlan& s, bool first) {
+  if (a.n_seq <= 64) return attn_plan_small(a, p, s, first);
   const int tid = threadIdx.x, n = a.n_seq;
   // row starts, kept rising and within the rows (starts are >= 0, so 0 is the scan's neutral value)
   {
@@ -94,8 +96,13 @@ __device__ inline int attn_plan(const AttnArgs& a, const AttnParts& p, AttnPlan&
       const int up = max(scan256<int, true>(v, s.sums, total), carry);
       if (e <= n) {
         s.start[e] = up;
-        const bool bad_len = e < n && (a.kv_len[e] < 0 || a.kv_len[e] > (int64_t)a.pages_ld << a.c.page_shift);
-        if (blockIdx.x == 0 && (raw != up || bad_len)) set_flag(a.flags, kFlagLength);
+        bool bad = raw != up;
+        if (e < n) {
+          const int have = a.kv_len[e];
+          s.own[e] = max(0, (int)min((int64_t)have, (int64_t)a.pages_ld << a.c.page_shift));
+          bad |= have != s.own[e];
+        }
+        if (first && bad) set_flag(a.flags, kFlagLength);
       }
       carry = max(carry, total);
     }
@@ -105,7 +112,7 @@ __device__ inline int attn_plan(const AttnArgs& a, const AttnParts& p, AttnPlan&
   int64_t work = 0, total;
   int tiles = 0, all_tiles;
   for (int e = tid; e < entries; e += 256) {
-    const AttnEntry x = attn_entry(a, s.start, p.set, p.rows, e);
+    const AttnEntry x = attn_entry(a, s.start, s.own, p.set, p.rows, e);
     work += (int64_t)x.tiles * x.units;
     tiles += x.tiles;
   }
@@ -117,7 +124,7 @@ __device__ inline int attn_plan(const AttnArgs& a, const AttnParts& p, AttnPlan&
     const int e = b + tid;
     int parts = 0, split = 0;
     if (e < entries) {
-      const AttnEntry x = attn_entry(a, s.start, p.set, p.rows, e);
+      const AttnEntry x = attn_entry(a, s.start, s.own, p.set, p.rows, e);
       split = x.tiles ? max(1, (x.units + per - 1) / per) : 0;
       parts = x.tiles * split;
     }
@@ -125,7 +132,7 @@ __device__ inline int attn_plan(const AttnArgs& a, const AttnParts& p, AttnPlan&
     const int up = scan256<int, false>(parts, s.sums, all) + carry;
     if (e < entries) {
       s.first[e] = up - parts;
-      if (blockIdx.x == 0) {
+      if (first) {
         p.plan[2 + 2 * e] = up - parts;
         p.plan[2 + 2 * e + 1] = split;
       }
@@ -143,10 +150,6 @@ __device__ inline int attn_plan(const AttnArgs& a, const AttnParts& p, AttnPlan&
 // One part's place: its entry, that entry's first part and number of parts.
 struct AttnPlace { int e, first, split; AttnEntry x; };
 
-// A plan of up to 64 entries needs no LDS and no barrier: each wave holds it, an entry a lane.  (One token of 777:
-// the kernel 9.7 us with the workgroup's scans, 7.6 us with these.)
-struct AttnWavePlan { int start, end, own, units, tiles, split, first, total; };
-
 __device__ __forceinline__ int wave_scan_max(int v) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -157,65 +160,51 @@ __device__ __forceinline__ int wave_scan_max(int v) {
   return v;
 }
 
-__device__ __forceinline__ AttnWavePlan attn_wave_plan(const AttnArgs& a, const AttnParts& p) {
-  const int lane = threadIdx.x & 63, n = a.n_seq;   // at most 64
-  AttnWavePlan w;
+// A plan of up to 64 sequences is one wave's work, with one barrier (one token of 777: 7.6 us for 9.7 with the
+// workgroup's scans).  Each wave forms it, the first writes it.
+__device__ inline int attn_plan_small(const AttnArgs& a, const AttnParts& p, AttnPlan& s, bool first) {
+  const int tid = threadIdx.x, lane = tid & 63, n = a.n_seq;   // at most 64
   const int raw0 = a.q_start[min(lane, n)], raw1 = a.q_start[min(lane + 1, n)], have = a.kv_len[min(lane, n - 1)];
-  const int64_t most = (int64_t)a.pages_ld << a.c.page_shift;
-  w.start = wave_scan_max(min(max(raw0, 0), a.M));
-  w.end = max(w.start, min(max(raw1, 0), a.M));
-  w.own = max(0, (int)min((int64_t)have, most));
-  if (blockIdx.x == 0 && lane < n && (raw0 != w.start || raw1 != w.end || have != w.own)) set_flag(a.flags, kFlagLength);
-  int rows = (w.end - w.start) * a.group;
-  if (p.set == ATTN_PREFIX) {
-    w.start = __shfl(w.start, 0);
-    w.end = __shfl(w.end, n - 1);
-    w.own = 0;
-    rows = lane == 0 ? (w.end - w.start) * a.group : 0;
-  }
-  if (lane >= n) rows = 0;
-  w.tiles = (rows + p.rows - 1) / p.rows;
-  w.units = attn_units(p.set == ATTN_OWN ? 0 : a.prefix_len) + attn_units(w.own);
-  int64_t work = (int64_t)w.tiles * w.units;
-  int tiles = w.tiles;
+  const int start = wave_scan_max(min(max(raw0, 0), a.M)), end = max(start, min(max(raw1, 0), a.M));
+  const int own = max(0, (int)min((int64_t)have, (int64_t)a.pages_ld << a.c.page_shift));
+  if (first && tid < n && (raw0 != start || raw1 != end || have != own)) set_flag(a.flags, kFlagLength);
+  const int begin = __shfl(start, 0), last = __shfl(end, n - 1);
+  const bool is_pre = p.set == ATTN_PREFIX;
+  const int rows = is_pre ? (lane == 0 ? (last - begin) * a.group : 0) : lane < n ? (end - start) * a.group : 0;
+  const int units = attn_units(p.set == ATTN_OWN ? 0 : a.prefix_len) + (is_pre ? 0 : attn_units(own));
+  const int my_tiles = (rows + p.rows - 1) / p.rows;
+  int64_t work = (int64_t)my_tiles * units;
+  int tiles = my_tiles;
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) {
     work += __shfl_xor(work, off);
     tiles += __shfl_xor(tiles, off);
   }
   const int per = attn_per(a, p, work, tiles);
-  w.split = w.tiles ? max(1, (w.units + per - 1) / per) : 0;
-  const int parts = w.tiles * w.split;
+  const int split = my_tiles ? max(1, (units + per - 1) / per) : 0, parts = my_tiles * split;
   int up = parts;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
     const int o = __shfl_up(up, off);
     if (lane >= off) up += o;
   }
-  w.first = up - parts;
-  w.total = __shfl(up, 63);
-  if (blockIdx.x == 0 && threadIdx.x < (p.set == ATTN_PREFIX ? 1 : n)) {
-    p.plan[2 + 2 * lane] = w.first;
-    p.plan[3 + 2 * lane] = w.split;
+  if (tid < n) {
+    s.start[lane] = start;
+    s.first[lane] = up - parts;
+    s.own[lane] = own;
+    if (first && (!is_pre || lane == 0)) {
+      p.plan[2 + 2 * lane] = up - parts;
+      p.plan[3 + 2 * lane] = split;
+    }
   }
-  return w;
-}
-
-__device__ __forceinline__ AttnPlace attn_wave_place(const AttnArgs& a, const AttnParts& p, const AttnWavePlan& w, int it) {
-  const int lane = threadIdx.x & 63, entries = p.set == ATTN_PREFIX ? 1 : a.n_seq;
-  AttnPlace r;
-  r.e = __popcll(__ballot(lane < entries && w.first <= it)) - 1;
-  const int start = __builtin_amdgcn_readlane(w.start, r.e), end = __builtin_amdgcn_readlane(w.end, r.e);
-  r.first = __builtin_amdgcn_readlane(w.first, r.e);
-  r.split = __builtin_amdgcn_readlane(w.split, r.e);
-  r.x.row0 = start;
-  r.x.rows = (end - start) * a.group;
-  r.x.own = __builtin_amdgcn_readlane(w.own, r.e);
-  r.x.pre = p.set == ATTN_OWN ? 0 : a.prefix_len;
-  r.x.causal = r.x.own - (end - start);
-  r.x.tiles = __builtin_amdgcn_readlane(w.tiles, r.e);
-  r.x.units = __builtin_amdgcn_readlane(w.units, r.e);
-  return r;
+  if (tid == 0) {
+    s.start[n] = last;
+    s.per = per;
+  }
+  const int total = __shfl(up, 63);
+  if (tid == 0) s.first[is_pre ? 1 : n] = total;
+  __syncthreads();
+  return total;
 }
 
 // The entry that a part of a key head belongs to: the last whose first part is
@@ -232,7 +221,7 @@ __device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a, const AttnPar
   AttnPlace r;
   r.e = attn_find(s, p.set == ATTN_PREFIX ? 1 : a.n_seq, it);
   r.first = s.first[r.e];
-  r.x = attn_entry(a, s.start, p.set, p.rows, r.e);
+  r.x = attn_entry(a, s.start, s.own, p.set, p.rows, r.e);
   r.split = max(1, (r.x.units + s.per - 1) / s.per);
   return r;
 }
@@ -261,26 +250,24 @@ __device__ __forceinline__ bf16x8 bf16x8_of_codes(u32x2 w) {
   return r;
 }
 
-// Which of the eight tokens behind `keep` count: the others' values become 0.
+// The first `keep` of eight tokens' values; the others become 0.  (Here and below without truth values, of which
+// there would be more than scalar registers.)
 __device__ __forceinline__ bf16x8 keep_first(bf16x8 v, int keep) {
   u32x4 w = __builtin_bit_cast(u32x4, v);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t mask = (keep > 2 * i ? 0xFFFFu : 0u) | (keep > 2 * i + 1 ? 0xFFFF0000u : 0u);
-    w[i] &= mask;
-  }
+  for (int i = 0; i < 4; ++i) w[i] &= (uint32_t)((0xFFFFFFFFull << (16 * min(max(keep - 2 * i, 0), 2))) >> 32);
   return __builtin_bit_cast(bf16x8, w);
 }
 
-// Infinities and NaNs become 0; returns whether there was one.
-__device__ __forceinline__ bool drop_nonfinite(bf16x8& v) {
+// Infinities and NaNs become 0; not 0 if there was one.
+__device__ __forceinline__ uint32_t drop_nonfinite(bf16x8& v) {
   u32x4 w = __builtin_bit_cast(u32x4, v);
-  bool any = false;
+  uint32_t any = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const bool lo = (w[i] & 0x7F80u) == 0x7F80u, hi = (w[i] & 0x7F800000u) == 0x7F800000u;
-    any |= lo || hi;
-    w[i] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+    const uint32_t top = ((w[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;   // each half's highest bit
+    any |= top;
+    w[i] &= ~(top | (top - (top >> 15)));
   }
   v = __builtin_bit_cast(bf16x8, w);
   return any;

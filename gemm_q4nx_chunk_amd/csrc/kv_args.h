@@ -108,6 +108,8 @@ struct AttnParts {
   int32_t shares;    // the shares of a batch of more tiles than half of them
 };
 
+struct AttnPair { AttnParts p[2]; };   // the sequences', the prefix's
+
 struct AttnArgs {
   KvCache c;
   const uint16_t* q;
@@ -128,9 +130,8 @@ inline int attn_entries(int set, int n_seq) { return set == ATTN_PREFIX ? 1 : n_
 inline int64_t attn_max_parts(const AttnParts& p, int n_seq, int64_t rows, int kv_heads) {
   return (rows / p.rows + attn_entries(p.set, n_seq)) * kv_heads + (p.slots > p.shares ? p.slots : p.shares);
 }
-hipError_t launch_attn_few(const AttnArgs& a, const AttnParts& p, int grid, hipStream_t s);
-// p.rows: 16 or 32
-hipError_t launch_attn_many(const AttnArgs& a, const AttnParts& p, int grid, hipStream_t s);
+// Tiles of own: 16, 32 or 128 rows; of the prefix: own's or 128 (rows = 0: no prefix, or with the sequences).
+hipError_t launch_attn(const AttnArgs& a, const AttnParts& own, int own_grid, const AttnParts& pre, int pre_grid, hipStream_t s);
 // own: the set of the sequences; prefix: of the prefix, or rows = 0
 hipError_t launch_attn_join(const AttnArgs& a, const AttnParts& own, const AttnParts& prefix, hipStream_t s);
 

@@ -1790,7 +1790,7 @@ void attn_shape(const q4nx_kv_cache* c, const q4nx_attn_batch* b, int q_heads, i
   };
   const int64_t mine = (int64_t)b->max_q * group;
   const int tile = mine > 32 ? 128 : mine > 16 ? 32 : 16;
-  const int slots = tile < 128 ? 512 : c->head_dim == 64 ? 768 : c->head_dim == 128 ? 512 : 256;
+  const int slots = c->head_dim == 256 ? 256 : c->head_dim == 64 && tile == 128 ? 768 : 512;
   place(sh.own, apart ? q4nx::ATTN_OWN : q4nx::ATTN_ALL, tile, slots, sh.own_grid, sh.own_plan, sh.own_o, sh.own_ml);
   if (apart)
     place(sh.pre, q4nx::ATTN_PREFIX, rows > 32 ? 128 : tile, 256, sh.pre_grid, sh.pre_plan, sh.pre_o, sh.pre_ml);
@@ -1912,11 +1912,11 @@ int q4nx_kv_append(const q4nx_kv_cache* cache, const q4nx_rope* rope, const q4nx
     a.rot = rope->dim;
     a.interleaved = rope->interleaved != 0;
   }
-  // about a thousand workgroups: up to eight tokens each where there are many,
-  // one token's heads over several where there are few
-  a.tile = std::max(1, std::min(q4nx::kAppendTile, M / 512));
-  const int tiles = (M + a.tile - 1) / a.tile, heads = a.q.heads + 2 * a.c.heads;
-  const int head_parts = std::min((a.tile * heads * D / 8 + 255) / 256, std::max(1, 1024 / tiles));
+  // one token a workgroup, its heads over several of them, until there are many (64 tokens of 20 heads of 256:
+  // 4.4 us, eight a workgroup TBD); then eight, so that values can be stored eight tokens at a time
+  a.tile = M >= 512 ? q4nx::kAppendTile : 1;
+  const int tiles = q4nx::append_tiles(a), heads = a.q.heads + 2 * a.c.heads;
+  const int head_parts = std::min((a.tile * heads * D / 16 + 255) / 256, std::max(1, 1024 / tiles));
   return hip_status(q4nx::launch_kv_append(a, head_parts, static_cast<hipStream_t>(stream)), "kv_append launch");
 }
 

@@ -630,8 +630,11 @@ __device__ __forceinline__ void attn_many(const AttnArgs& a, const AttnParts& p,
 
 constexpr int attn_lds(int dim, int rows) { return rows == 128 ? 2 * 2 * 64 * dim * 2 : 4 * 16 * (dim + 4) * 4; }
 
-// Registers for three workgroups a CU at 64 dimensions, two at 128, one at 256.
-constexpr int attn_occupancy(int dim, int rows) { return dim == 256 ? 1 : dim == 64 && rows != 32 ? 3 : 2; }
+// Workgroups a CU that the registers are cut for.  (Three of 16 rows at 128 dimensions: 8 bits 46 us for 52, 64
+// tokens of 2000; bf16 spills, 80 for 72.)
+constexpr int attn_occupancy(int dim, bool i8, int rows) {
+  return dim == 256 ? 1 : dim == 64 ? (rows == 32 ? 2 : 3) : i8 && rows == 16 ? 3 : 2;
+}
 
 template <int D, bool I8, int ROWS>
 __device__ __forceinline__ void attn_rows(const AttnArgs& a, const AttnParts& p, int block, int blocks, AttnPlan& plan, uint8_t* lds) {
@@ -640,7 +643,7 @@ __device__ __forceinline__ void attn_rows(const AttnArgs& a, const AttnParts& p,
 }
 
 template <int D, bool I8, int ROWS>
-__global__ __launch_bounds__(256, attn_occupancy(D, ROWS)) void k_attn(AttnArgs a, AttnParts p) {
+__global__ __launch_bounds__(256, attn_occupancy(D, I8, ROWS)) void k_attn(AttnArgs a, AttnParts p) {
   __shared__ AttnPlan plan;
   extern __shared__ __align__(16) uint8_t lds[];
   attn_rows<D, I8, ROWS>(a, p, blockIdx.x, gridDim.x, plan, lds);
@@ -652,7 +655,7 @@ __global__ __launch_bounds__(256, attn_occupancy(D, ROWS)) void k_attn(AttnArgs 
 // and values stream (16 windows over 8 bits: 45 us, one after the other 71; 64
 // tokens behind 8192: 97 for 109).
 template <int D, bool I8, int OWN, int PRE>
-__global__ __launch_bounds__(256, attn_occupancy(D, OWN)) void k_attn_shared(AttnArgs a, AttnPair sets, int pre_grid) {
+__global__ __launch_bounds__(256, attn_occupancy(D, I8, OWN > PRE ? OWN : PRE)) void k_attn_shared(AttnArgs a, AttnPair sets, int pre_grid) {
   __shared__ AttnPlan plan;
   extern __shared__ __align__(16) uint8_t lds[];
   const bool is_pre = (int)blockIdx.x < pre_grid;

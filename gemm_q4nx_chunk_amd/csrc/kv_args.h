@@ -81,6 +81,8 @@ struct AppendArgs {
   int32_t M, rot, interleaved, tile;   // tile: rows of a workgroup
 };
 constexpr int kAppendTile = 8;
+// Tiles of a whole eight begin where the first row's run of slots does, so that there may be one more.
+inline int append_tiles(const AppendArgs& a) { return (a.M + a.tile - 1) / a.tile + (a.tile == kAppendTile ? 1 : 0); }
 hipError_t launch_kv_append(const AppendArgs& a, int head_parts, hipStream_t s);
 
 // ---------------------------------------------------------------------------

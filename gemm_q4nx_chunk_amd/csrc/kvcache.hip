@@ -2,12 +2,16 @@
 //
 //   t = pos * inv_freq[i];  (a, b) -> (a cos t - b sin t, b cos t + a sin t)
 //
-// A workgroup has a few tokens and a part of their heads: it forms the angles
-// of its tokens once (fp64: pos * inv_freq is exact there, and the sine and
-// cosine reduce it without losing a far position's digits), keeps them in LDS,
-// and turns every head with them.  D/8 neighbouring lanes hold a head, eight
-// values each, so that an 8-bit head's largest value is a few lane exchanges
-// away.  Each value is read once and written once.
+// A workgroup has one token or eight and a part of their heads: it forms the
+// angles of its tokens once (fp64: pos * inv_freq is exact there, and the sine
+// and cosine reduce it without losing a far position's digits), keeps them in
+// LDS, and turns every head with them.  A lane has two pieces of eight values, so
+// that both sides of a pair and what the cache holds together are one lane's.
+// Each value is read once and written once.
+//
+// Eight tokens whose slots are a run (a prompt's; the tiles begin where the first
+// row's run of eight does) have their values exchanged through LDS and stored
+// sixteen bytes at a time; others' values go to their places one by one.
 //
 // bf16 values are rounded from fp32.  8-bit codes are formed in fp64 from the
 // turned fp64 values: a code next to a rounding border depends on nothing that
@@ -15,6 +19,8 @@
 //
 // Of rows with one slot the last is stored: each workgroup looks its tokens'
 // slots up among the later rows, so that no two workgroups write one place.
+#include <type_traits>
+
 #include "kv_args.h"
 
 namespace q4nx {
@@ -54,16 +60,20 @@ __device__ __forceinline__ double mul_add(double a, double b, double c) { return
 
 }  // namespace
 
-// I8: the cache's type; T: what values are turned in.
-template <int D, bool I8, typename T>
+// I8: the cache's type; T: what values are turned in; TM: tokens of a workgroup.
+template <int D, bool I8, typename T, int TM>
 __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
-  constexpr int L = D / 8;             // lanes of a head
+  constexpr int L = D / 16;            // lanes of a head: 4, 8 or 16
   constexpr int kItems = 256 / L;      // heads at a time
+  typedef typename std::conditional<I8, uint8_t, uint16_t>::type Elem;
   extern __shared__ __align__(16) uint8_t lds[];
-  Turn<T>* turn = reinterpret_cast<Turn<T>*>(lds);   // [tile][rot / 2]
-  __shared__ int s_slot[kAppendTile];
-  __shared__ int s_dead[kAppendTile];
-  const int tid = threadIdx.x, m0 = blockIdx.x * a.tile, rows = min(a.tile, a.M - m0);
+  Turn<T>* turn = reinterpret_cast<Turn<T>*>(lds);   // [TM][rot / 2]
+  __shared__ int s_slot[TM], s_dead[TM];
+  __shared__ __align__(16) Elem s_v[TM == 8 ? kItems : 1][TM == 8 ? D + 8 : 1];
+  const int tid = threadIdx.x;
+  const int off = TM == 8 ? max(a.slots[0], 0) & 7 : 0;
+  const int m0 = max((int)blockIdx.x * TM - off, 0), rows = min((int)(blockIdx.x + 1) * TM - off, a.M) - m0;
+  if (rows <= 0) return;
   const int half = a.inv_freq ? a.rot / 2 : 0;
   for (int i = tid; i < rows * half; i += 256) {
     const int t = i / half, p = i - t * half;
@@ -86,106 +96,186 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
   }
   __syncthreads();
 
-  const int qh = a.q.p ? a.q.heads : 0, heads = qh + 2 * a.c.heads;
-  const int l = tid % L;
-  for (int it = blockIdx.y * kItems + tid / L; it < rows * heads; it += gridDim.y * kItems) {
-    const int t = it / heads, h = it - t * heads, m = m0 + t;
-    const bool is_q = h < qh, is_v = h >= qh + a.c.heads;
-    const HeadRows& src = is_q ? a.q : is_v ? a.v : a.k;
-    const int head = is_q ? h : is_v ? h - qh - a.c.heads : h - qh;
-    if (!is_q && (s_slot[t] < 0 || s_dead[t])) continue;   // the same in a head's lanes
-    const int64_t row = (int64_t)m * src.ld + (int64_t)head * D;
-    // the lane's values: four from d0 and four from d1
-    const bool turns = !is_v && 4 * l < half;
-    const int d0 = turns && !a.interleaved ? 4 * l : 8 * l;
-    const int d1 = turns && !a.interleaved ? half + 4 * l : 8 * l + 4;
-    const f32x4 x0 = load4(src, row + d0), x1 = load4(src, row + d1);
-    T y[8];
+  // A head's 16 values of a lane: piece e0 of eight and piece e1.
+  const int qh = a.q.p ? a.q.heads : 0, KH = a.c.heads;
+  auto place = [&](int t) { return kv_page(a.c, s_slot[t] >> a.c.page_shift, 0); };
+  // 8 bits: a head's scale over its lanes, and the lane's codes
+  auto codes_of = [&](const T (&y)[16], float& scale, uint32_t (&w)[4]) {
+    T top = 0;
+    bool nan = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[i] = x0[i];
-      y[4 + i] = x1[i];
+    for (int i = 0; i < 16; ++i) {
+      top = fmax(top, fabs(y[i]));
+      nan |= y[i] != y[i];
     }
-    if (turns) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Turn<T> w = turn[t * half + 4 * l + i];
-        if (a.interleaved) {
-          const T p = y[2 * i], r = y[2 * i + 1];
-          y[2 * i] = mul_add(p, w.c, -r * w.s);
-          y[2 * i + 1] = mul_add(r, w.c, p * w.s);
-        } else {
-          const T p = y[i], r = y[4 + i];
+    for (int o = 1; o < L; o <<= 1) {
+      top = fmax(top, __shfl_xor(top, o));
+      nan |= __shfl_xor((int)nan, o) != 0;
+    }
+    scale = nan ? __builtin_nanf("") : (float)(top / (T)127);
+    const bool plain = scale > 0.f && scale <= __FLT_MAX__;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int code = plain ? (int)fmin(fmax(rint(y[i] / (T)scale), (T)-127), (T)127) : 0;
+      w[i >> 2] |= (uint32_t)(code & 255) << (8 * (i & 3));
+    }
+  };
+  auto load16 = [&](const HeadRows& src, int64_t row, int e0, int e1, T (&y)[16]) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const f32x4 x = load4(src, row + 8 * (n < 2 ? e0 : e1) + 4 * (n & 1));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[4 * n + i] = x[i];
+    }
+  };
+
+  // q and k.  8 bits: a head's lanes side by side, to find its largest value; else eight tokens side by side, whose
+  // pieces lie together in the cache.
+  for (int it = blockIdx.y * 256 + tid; it < rows * (qh + KH) * L; it += gridDim.y * 256) {
+    int l, t, h;
+    if (I8 || TM == 1) {
+      l = it % L;
+      const int u = it / L;
+      t = u % rows;
+      h = u / rows;
+    } else {
+      t = it % rows;
+      const int u = it / rows;
+      l = u % L;
+      h = u / L;
+    }
+    const int m = m0 + t;
+    const bool is_q = h < qh;
+    const HeadRows& src = is_q ? a.q : a.k;
+    const int head = is_q ? h : h - qh;
+    const bool kept = s_slot[t] >= 0 && !s_dead[t];
+    int e0 = 2 * l, e1 = 2 * l + 1;
+    if (!a.interleaved && 8 * l < half) {
+      e0 = l;
+      e1 = l + half / 8;
+    }
+    T y[16];
+    load16(src, (int64_t)m * src.ld + (int64_t)head * D, e0, e1, y);
+    if (!a.interleaved) {
+      if (8 * l < half) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const Turn<T> w = turn[t * half + 8 * l + i];
+          const T p = y[i], r = y[8 + i];
           y[i] = mul_add(p, w.c, -r * w.s);
-          y[4 + i] = mul_add(r, w.c, p * w.s);
+          y[8 + i] = mul_add(r, w.c, p * w.s);
         }
       }
+    } else if (8 * l < half) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const Turn<T> w = turn[t * half + 8 * l + i];
+        const T p = y[2 * i], r = y[2 * i + 1];
+        y[2 * i] = mul_add(p, w.c, -r * w.s);
+        y[2 * i + 1] = mul_add(r, w.c, p * w.s);
+      }
     }
+    u32x4 w[2];
+#pragma unroll
+    for (int n = 0; n < 8; ++n) w[n >> 2][n & 3] = bf16_pair((float)y[2 * n], (float)y[2 * n + 1]);
     if (is_q) {
       uint16_t* o = a.q_out + ((size_t)m * qh + head) * D;
-      *reinterpret_cast<u32x2*>(o + d0) = u32x2{bf16_pair((float)y[0], (float)y[1]), bf16_pair((float)y[2], (float)y[3])};
-      *reinterpret_cast<u32x2*>(o + d1) = u32x2{bf16_pair((float)y[4], (float)y[5]), bf16_pair((float)y[6], (float)y[7])};
-      continue;
+      *reinterpret_cast<u32x4*>(o + 8 * e0) = w[0];
+      *reinterpret_cast<u32x4*>(o + 8 * e1) = w[1];
     }
-    const int page = s_slot[t] >> a.c.page_shift, tok = s_slot[t] & ((1 << a.c.page_shift) - 1);
-    const size_t base = kv_page(a.c, page, head);
     if constexpr (I8) {
-      T top = 0;
-      bool nan = false;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        top = fmax(top, fabs(y[i]));
-        nan |= y[i] != y[i];
+      float scale;
+      uint32_t c[4];
+      codes_of(y, scale, c);   // of q's heads too: the lanes stay together
+      if (!is_q && kept) {
+        const int tok = s_slot[t] & ((1 << a.c.page_shift) - 1);
+        uint8_t* o = static_cast<uint8_t*>(a.c.k) + place(t) + ((size_t)head << a.c.page_shift) * D;
+        *reinterpret_cast<u32x2*>(o + k_place(D, tok, 8 * e0)) = u32x2{c[0], c[1]};
+        *reinterpret_cast<u32x2*>(o + k_place(D, tok, 8 * e1)) = u32x2{c[2], c[3]};
+        if (l == 0) a.c.ks[place(t) / D + ((size_t)head << a.c.page_shift) + tok] = scale;
       }
+    } else if (!is_q && kept) {
+      const int tok = s_slot[t] & ((1 << a.c.page_shift) - 1);
+      uint16_t* o = static_cast<uint16_t*>(a.c.k) + place(t) + ((size_t)head << a.c.page_shift) * D;
+      *reinterpret_cast<u32x4*>(o + k_place(D, tok, 8 * e0)) = w[0];
+      *reinterpret_cast<u32x4*>(o + k_place(D, tok, 8 * e1)) = w[1];
+    }
+  }
+
+  // v: a head's lanes side by side, then its tokens
+  bool run = TM == 8 && rows == 8 && s_slot[0] >= 0 && (s_slot[0] & 7) == 0;
+  if constexpr (TM == 8)
+    for (int t = 0; t < 8 && run; ++t) run = s_slot[t] == s_slot[0] + t && !s_dead[t];
+  const int items = rows * KH * L;
+  for (int base = blockIdx.y * 256; base < items; base += gridDim.y * 256) {
+    const int it = base + tid, l = it % L, u = it / L, t = u % rows, head = u / rows;
+    const bool mine = it < items;
+    T y[16];
+    if (mine) load16(a.v, (int64_t)(m0 + t) * a.v.ld + (int64_t)head * D, 2 * l, 2 * l + 1, y);
+    else
 #pragma unroll
-      for (int off = 1; off < L; off <<= 1) {
-        top = fmax(top, __shfl_xor(top, off));
-        nan |= __shfl_xor((int)nan, off) != 0;
-      }
-      const float scale = nan ? __builtin_nanf("") : (float)(top / (T)127);
-      const bool plain = scale > 0.f && scale <= __FLT_MAX__;
-      uint32_t w[2] = {0u, 0u};
+      for (int i = 0; i < 16; ++i) y[i] = 0;
+    const bool kept = mine && s_slot[t] >= 0 && !s_dead[t];
+    const int tok = kept ? s_slot[t] & ((1 << a.c.page_shift) - 1) : 0;
+    Elem e[16];
+    if constexpr (I8) {
+      float scale;
+      uint32_t c[4];
+      codes_of(y, scale, c);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int code = plain ? (int)fmin(fmax(rint(y[i] / (T)scale), (T)-127), (T)127) : 0;
-        w[i >> 2] |= (uint32_t)(code & 255) << (8 * (i & 3));
-      }
-      if (is_v) {
-        uint8_t* o = static_cast<uint8_t*>(a.c.v) + base;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[v_place(D, tok, 8 * l + i)] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
-      } else {
-        uint8_t* o = static_cast<uint8_t*>(a.c.k) + base;
-        *reinterpret_cast<uint32_t*>(o + k_place(D, tok, d0)) = w[0];
-        *reinterpret_cast<uint32_t*>(o + k_place(D, tok, d1)) = w[1];
-      }
-      if (l == 0) (is_v ? a.c.vs : a.c.ks)[(((size_t)page * a.c.heads + head) << a.c.page_shift) + tok] = scale;
+      for (int i = 0; i < 16; ++i) e[i] = (uint8_t)(c[i >> 2] >> (8 * (i & 3)));
+      if (kept && l == 0) a.c.vs[place(t) / D + ((size_t)head << a.c.page_shift) + tok] = scale;
     } else {
-      const uint32_t w[4] = {bf16_pair((float)y[0], (float)y[1]), bf16_pair((float)y[2], (float)y[3]),
-                             bf16_pair((float)y[4], (float)y[5]), bf16_pair((float)y[6], (float)y[7])};
-      if (is_v) {
-        uint16_t* o = static_cast<uint16_t*>(a.c.v) + base;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[v_place(D, tok, 8 * l + i)] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-      } else {
-        uint16_t* o = static_cast<uint16_t*>(a.c.k) + base;
-        *reinterpret_cast<u32x2*>(o + k_place(D, tok, d0)) = u32x2{w[0], w[1]};
-        *reinterpret_cast<u32x2*>(o + k_place(D, tok, d1)) = u32x2{w[2], w[3]};
+      for (int i = 0; i < 16; ++i) e[i] = __builtin_bit_cast(uint16_t, (__bf16)(float)y[i]);
+    }
+    if (TM == 8 && run) {   // the same in the whole workgroup
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s_v[tid / L][16 * l + i] = e[i];
+      __syncthreads();
+      // 8 tokens of a dimension, 256 / L / 8 heads at a time
+      const int head0 = base / L / 8;
+      for (int n = tid; n < kItems / 8 * D; n += 256) {
+        const int hl = n / D, d = n % D;
+        if (head0 + hl < KH) {
+          const size_t at = place(0) + ((size_t)(head0 + hl) << a.c.page_shift) * D +
+                            v_place(D, s_slot[0] & ((1 << a.c.page_shift) - 1), d);
+          Elem x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = s_v[8 * hl + i][d];
+          if constexpr (I8) {
+            *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.c.v) + at) = __builtin_bit_cast(u32x2, x);
+          } else {
+            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.c.v) + at) = __builtin_bit_cast(u32x4, x);
+          }
+        }
       }
+      __syncthreads();
+    } else if (kept) {
+      Elem* o = static_cast<Elem*>(a.c.v) + place(t) + ((size_t)head << a.c.page_shift) * D;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[v_place(D, tok, 16 * l + i)] = e[i];
     }
   }
 }
 
 hipError_t launch_kv_append(const AppendArgs& a, int head_parts, hipStream_t s) {
-  const dim3 grid((a.M + a.tile - 1) / a.tile, head_parts);
+  const dim3 grid(append_tiles(a), head_parts);
   const bool i8 = a.c.ks != nullptr;
   const size_t lds = a.inv_freq ? (size_t)a.tile * (a.rot / 2) * (i8 ? 16 : 8) : 0;
-#define Q4NX_APPEND(D)                                                                            \
-  if (i8) hipLaunchKernelGGL((k_kv_append<D, true, double>), grid, dim3(256), lds, s, a);         \
-  else hipLaunchKernelGGL((k_kv_append<D, false, float>), grid, dim3(256), lds, s, a)
-  if (a.c.dim == 64) { Q4NX_APPEND(64); }
-  else if (a.c.dim == 128) { Q4NX_APPEND(128); }
-  else { Q4NX_APPEND(256); }
+#define Q4NX_APPEND(D, I8, T)                                                                                            \
+  if (a.tile == kAppendTile) hipLaunchKernelGGL((k_kv_append<D, I8, T, kAppendTile>), grid, dim3(256), lds, s, a);       \
+  else hipLaunchKernelGGL((k_kv_append<D, I8, T, 1>), grid, dim3(256), lds, s, a)
+#define Q4NX_APPEND_D(D)                    \
+  if (i8) { Q4NX_APPEND(D, true, double); } \
+  else { Q4NX_APPEND(D, false, float); }
+  if (a.c.dim == 64) { Q4NX_APPEND_D(64) }
+  else if (a.c.dim == 128) { Q4NX_APPEND_D(128) }
+  else { Q4NX_APPEND_D(256) }
+#undef Q4NX_APPEND_D
 #undef Q4NX_APPEND
   return hipGetLastError();
 }

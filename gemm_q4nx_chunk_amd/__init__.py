@@ -594,19 +594,25 @@ def rope(inv_freq, pos, dim: int, interleaved: bool = False) -> Rope:
     return r
 
 
+def _row_step(t, columns: int, width: int, what: str) -> int:
+    """Elements between a tensor's rows of heads `width` wide; its other dimensions lie as they come."""
+    st = t.stride()
+    if len(st) < 2:
+        return columns
+    if st[-1] != 1 or (len(st) == 3 and st[1] != width and t.shape[1] > 1):
+        raise Q4nxError(E_SHAPE, f"{what}: the columns of a row must be contiguous")
+    return columns if st[0] < columns and t.shape[0] == 1 else st[0]
+
+
 def heads(t, n: int, head_dim: int, ld: int | None = None, bf16: bool | None = None) -> Heads:
     """M rows of n heads: fp32, or bf16 (bf16 or int16 tensors), rows ld elements apart (a tensor's first stride)."""
     if isinstance(t, int):
         return Heads(t, n * head_dim if ld is None else ld, n, _BF16 if bf16 else _F32)
-    if t.element_size() not in (2, 4):
+    size = t.element_size()
+    if size != 2 and size != 4:
         raise Q4nxError(E_ARG, f"heads of type {t.dtype}: fp32 or bf16 are taken")
-    if t.dim() < 2:
-        step = n * head_dim
-    else:
-        if t.stride(-1) != 1 or (t.dim() == 3 and t.stride(1) != head_dim):
-            raise Q4nxError(E_SHAPE, "heads: the columns of a row must be contiguous")
-        step = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), n * head_dim)
-    h = Heads(t.data_ptr(), step if ld is None else ld, n, (t.element_size() == 2) if bf16 is None else bf16)
+    h = Heads(t.data_ptr(), _row_step(t, n * head_dim, head_dim, "heads") if ld is None else ld, n,
+              size == 2 if bf16 is None else bf16)
     h._owner = t
     return h
 
@@ -616,12 +622,17 @@ def kv_append(cache: KvCache, k, v, slots, M: int, rope: Rope | None = None, q=N
     """k and v (tensors of kv_heads heads a row, or what heads() made) to the cache's slots[M], k turned by rope; q turned
     into q_out (bf16 [M][q_heads][head_dim])."""
     D, n = cache.head_dim, cache.kv_heads
-    if q is not None and q_heads is None and not isinstance(q, Heads):
-        raise Q4nxError(E_ARG, "kv_append: q without q_heads")
-    qh, kh, vh = (t if t is None or isinstance(t, Heads) else heads(t, c, D) for t, c in ((q, q_heads), (k, n), (v, n)))
-    ref = lambda s: None if s is None else ctypes.byref(s)  # noqa: E731
-    _check(_lib.q4nx_kv_append(ctypes.byref(cache), ref(rope), ref(qh), _ptr(q_out), ref(kh), ref(vh), _ptr(slots), M,
-                               _ptr(flags), _stream(stream)))
+    if not isinstance(k, Heads):
+        k = heads(k, n, D)
+    if not isinstance(v, Heads):
+        v = heads(v, n, D)
+    if q is not None and not isinstance(q, Heads):
+        if q_heads is None:
+            raise Q4nxError(E_ARG, "kv_append: q without q_heads")
+        q = heads(q, q_heads, D)
+    ref = ctypes.byref
+    _check(_lib.q4nx_kv_append(ref(cache), None if rope is None else ref(rope), None if q is None else ref(q), _ptr(q_out),
+                               ref(k), ref(v), _ptr(slots), M, _ptr(flags), _stream(stream)))
 
 
 def attn_batch(q_start, kv_len, pages, max_q: int, prefix_len: int = 0, prefix_pages=None, n_seq: int | None = None,
@@ -675,11 +686,7 @@ def linear_attn(seqs: Linear, q, k, v, decay, k_heads: int, v_heads: int, dk: in
     def step(t, ld, columns, width):
         if ld is not None:
             return ld
-        if isinstance(t, int) or t.dim() < 2:
-            return columns
-        if t.stride(-1) != 1 or (t.dim() == 3 and t.stride(1) != width):
-            raise Q4nxError(E_SHAPE, "linear_attn: the columns of a row must be contiguous")
-        return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), columns)
+        return columns if isinstance(t, int) else _row_step(t, columns, width, "linear_attn")
     if decay_ld is None:
         decay_ld = 0 if not isinstance(decay, int) and decay.dim() == 1 else step(decay, None, v_heads, 1)
     if n_slots is None:

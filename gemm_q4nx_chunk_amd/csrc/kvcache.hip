@@ -48,10 +48,12 @@ __device__ __forceinline__ f32x4 load4(const HeadRows& h, int64_t at) {
 template <typename T>
 struct Turn { T c, s; };
 
+// To fp32: the angle less whole turns in fp64 (2 pi in two parts, so that nothing of a turn's digits is lost), then
+// the fp32 functions.
 __device__ __forceinline__ void turn_of(double angle, Turn<float>& t) {
-  double s, c;
-  sincos(angle, &s, &c);
-  t = {(float)c, (float)s};
+  const double turns = rint(angle * 0.15915494309189535);
+  const double rest = fma(-turns, 2.4492935982947064e-16, fma(-turns, 6.283185307179586, angle));
+  sincosf((float)rest, &t.s, &t.c);
 }
 __device__ __forceinline__ void turn_of(double angle, Turn<double>& t) { sincos(angle, &t.s, &t.c); }
 
@@ -89,10 +91,19 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
     s_dead[tid] = 0;
   }
   __syncthreads();
+  // a later row with one of these slots; most are out of their range
+  int lo = 0x7FFFFFFF, hi = -1;
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+    if (t < rows && s_slot[t] >= 0) {
+      lo = min(lo, s_slot[t]);
+      hi = max(hi, s_slot[t]);
+    }
   for (int j = m0 + 1 + tid; j < a.M; j += 256) {
     const int slot = a.slots[j];
-    for (int t = 0; t < rows; ++t)
-      if (slot == s_slot[t] && m0 + t < j) s_dead[t] = 1;   // every writer writes the same
+    if (slot >= lo && slot <= hi)
+      for (int t = 0; t < rows; ++t)
+        if (slot == s_slot[t] && m0 + t < j) s_dead[t] = 1;   // every writer writes the same
   }
   __syncthreads();
 
@@ -115,11 +126,12 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
     }
     scale = nan ? __builtin_nanf("") : (float)(top / (T)127);
     const bool plain = scale > 0.f && scale <= __FLT_MAX__;
+    const T inv = plain ? (T)1 / (T)scale : 0;   // a quotient's last bits of 53 are all that this costs
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = 0u;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int code = plain ? (int)fmin(fmax(rint(y[i] / (T)scale), (T)-127), (T)127) : 0;
+      const int code = plain ? (int)fmin(fmax(rint(y[i] * inv), (T)-127), (T)127) : 0;
       w[i >> 2] |= (uint32_t)(code & 255) << (8 * (i & 3));
     }
   };

@@ -2,6 +2,7 @@
 //
 //   S_t = exp(d_t) S_{t-1} + k_t v_t^T,   out_t = scale q_t^T S_t
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_args.h"
 
@@ -22,14 +23,15 @@ __device__ inline LinearSeq linear_seq(const LinearArgs& a, int s, int start, in
   if (tid == 0) *taken = 0;
   const int raw_slot = a.slots[s], fresh = a.fresh ? a.fresh[s] : 0, raw0 = a.q_start[s], raw1 = a.q_start[s + 1];
   __syncthreads();
-  if (raw_slot >= 0)
+  if (raw_slot >= 0 && s > 0) {
     for (int e = tid; e < s; e += blockDim.x)
       if (a.slots[e] == raw_slot) {
         int before = 0;   // rows: its start rises to the next one's
         for (int i = 0; i <= e; ++i) before = max(before, min(max(a.q_start[i], 0), a.M));
         if (min(max(a.q_start[e + 1], 0), a.M) > before) *taken = 1;
       }
-  __syncthreads();
+    __syncthreads();
+  }
   const bool bad = raw_slot < -1 || raw_slot >= a.n_slots || *taken;
   LinearSeq x;
   x.row0 = start;
@@ -144,19 +146,28 @@ constexpr int kChunk = 64;
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-// bf16 parts of x: x = hi + mid + lo to 2^-24 (x below 2^127).
+// bf16 parts of x, its first, second and third eight bits: x = hi + mid + lo.  (Cut, not rounded, so that no part
+// of a finite x overflows.)
 struct Parts { bf16x8 p[3]; };
 __device__ __forceinline__ Parts parts_of(const float (&x)[8]) {
   Parts r;
+  u32x4 w[3];
 #pragma unroll
-  for (int n = 0; n < 8; ++n) {
-    const __bf16 hi = (__bf16)x[n];
-    const float r1 = x[n] - (float)hi;
-    const __bf16 mid = (__bf16)r1;
-    r.p[0][n] = hi;
-    r.p[1][n] = mid;
-    r.p[2][n] = (__bf16)(r1 - (float)mid);
+  for (int n = 0; n < 4; ++n) {
+    uint32_t b[3][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float v = x[2 * n + i];
+      b[0][i] = __float_as_uint(v);
+      const float r1 = v - __uint_as_float(b[0][i] & 0xFFFF0000u);
+      b[1][i] = __float_as_uint(r1);
+      b[2][i] = __float_as_uint(r1 - __uint_as_float(b[1][i] & 0xFFFF0000u));
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) w[k][n] = __builtin_amdgcn_perm(b[k][1], b[k][0], 0x07060302u);   // upper halves
   }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) r.p[k] = __builtin_bit_cast(bf16x8, w[k]);
   return r;
 }
 
@@ -166,10 +177,8 @@ __device__ __forceinline__ int dealt(int c) { return 16 * (c >> 4) + 8 * ((c >> 
 
 __device__ __forceinline__ bf16x8 ld8(const uint16_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
 
-__device__ __forceinline__ bool huge(uint32_t bits) { return (bits & 0x7F800000u) >= 0x7F000000u; }
-__device__ __forceinline__ bool nonfinite2(uint32_t w) {
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
+// The highest bit of each half that holds an infinity or NaN (and other bits).
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
 
 // Exclusive sums of the sequences' segments: first[s] for s in 0..n_seq, in LDS.
 __device__ inline void linear_plan(const LinearArgs& a, int32_t* first, int32_t* start) {
@@ -258,13 +267,14 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
 #pragma unroll
       for (int n = 0; n < 16; ++n) S[t][n] = from ? from[(uint32_t)(line0 * DV + col) + (32 * t + 16 * (n >> 3) + (n & 7)) * DV] : 0.f;
   }
+  // A state that holds an infinity or NaN has no parts.
   auto state_odd = [&]() {
-    bool odd = false;
+    float zero = 0.f;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int n = 0; n < 16; ++n) odd |= huge(__float_as_uint(S[t][n]));
-    return odd;
+      for (int n = 0; n < 16; ++n) zero = fmaf(S[t][n], 0.f, zero);
+    return !(zero == 0.f);
   };
   double G_all = 0.0;
   bool bad = false;
@@ -276,14 +286,31 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
   const uint16_t* const at_vt = lds + kVT + (hh * DV + col) * 8;
   if (tid < 2) s_odd[tid] = 0;
   __syncthreads();
+  constexpr int kK8 = 4 * DK / kThreads, kV8 = 4 * DV / kThreads;
+  uint32_t tk[kK8][8], tv[kV8][8];
+  float next_d = a.decay[(row0 + min(lane, rows - 1)) * a.decay_ld + h];
   for (int r0 = 0, turn = 0; r0 < rows; r0 += kChunk, turn ^= 1) {
     const int n_rows = min(kChunk, rows - r0);
     const int64_t g0 = row0 + r0;
-    bool odd = false;
+    uint32_t any = 0;
     // Operands to LDS.  Rows behind the last are the last again: no row's weight reaches them, and their share
     // of the state is 0.  q's and k's rows go straight there, in whole lines; what is wanted token by token
     // goes through registers.  No load stands under a branch, so that none waits for another.
     const int last = n_rows - 1;
+    auto ask = [&](int ahead) {   // k and v of the chunk so many rows on, token by token
+      const int behind = min(kChunk, rows - r0 - ahead) - 1;
+      auto fetch = [&](const uint16_t* src, uint32_t ld, int width, int u, uint32_t (&w)[8]) {
+        const int d = 2 * (u % (width / 2)), r = 8 * (u / (width / 2));
+#pragma unroll
+        for (int n = 0; n < 8; ++n) w[n] = *reinterpret_cast<const uint32_t*>(src + (min(r + n, behind) * ld + d));
+      };
+#pragma unroll
+      for (int n = 0; n < kK8; ++n)
+        fetch(a.k + (g0 + ahead) * a.k_ld + kh * DK, (uint32_t)a.k_ld, DK, tid + n * kThreads, tk[n]);
+#pragma unroll
+      for (int n = 0; n < kV8; ++n)
+        fetch(a.v + (g0 + ahead) * a.v_ld + h * DV, (uint32_t)a.v_ld, DV, tid + n * kThreads, tv[n]);
+    };
     if constexpr (OUT) {
       constexpr int kRow = DK / 8;   // pieces of a row; a wave has 64 pieces at a time, whole rows
 #pragma unroll
@@ -299,20 +326,15 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
       }
     }
     {
-      constexpr int kK8 = 4 * DK / kThreads, kV8 = 4 * DV / kThreads;
-      uint32_t tk[kK8][8], tv[kV8][8];
-      auto fetch = [&](const uint16_t* src, uint32_t ld, int width, int u, uint32_t (&w)[8]) {
-        const int d = 2 * (u % (width / 2)), r = 8 * (u / (width / 2));
-#pragma unroll
-        for (int n = 0; n < 8; ++n) w[n] = *reinterpret_cast<const uint32_t*>(src + (min(r + n, last) * ld + d));
-      };
-#pragma unroll
-      for (int n = 0; n < kK8; ++n) fetch(a.k + g0 * a.k_ld + kh * DK, (uint32_t)a.k_ld, DK, tid + n * kThreads, tk[n]);
-#pragma unroll
-      for (int n = 0; n < kV8; ++n) fetch(a.v + g0 * a.v_ld + h * DV, (uint32_t)a.v_ld, DV, tid + n * kThreads, tv[n]);
+      if (OUT || r0 == 0) ask(0);
       if (wave == kWaves - 1) {
-        const float d = decay_of(a, g0 + min(lane, last), h, bad);
+        float d = next_d;
+        if (!(d <= 0.f)) {
+          bad = true;
+          d = 0.f;
+        }
         s_d[lane] = d;
+        if (r0 + kChunk < rows) next_d = a.decay[(g0 + min(kChunk + lane, rows - r0 - 1)) * a.decay_ld + h];
         // in powers of two; exp of less than -1e5 is 0 in fp32, and sums of these stay exact to 2^-30
         double G = lane <= last ? (double)fmaxf(d, -1e5f) * 1.4426950408889634 : 0.0;
 #pragma unroll
@@ -321,7 +343,7 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
           if (lane >= off) G += o;
         }
         s_G[lane] = G;
-        s_since[lane] = __builtin_amdgcn_exp2f((float)G);
+        s_since[lane] = a.scale * __builtin_amdgcn_exp2f((float)G);
         const float left = __builtin_amdgcn_exp2f((float)(__shfl(G, 63) - G));
         s_left[lane] = lane <= last ? left : 0.f;
       }
@@ -329,7 +351,7 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
         const int d = 2 * (u % (width / 2)), r = 8 * (u / (width / 2));
         u32x4 lo, hi;
 #pragma unroll
-        for (int n = 0; n < 8; ++n) odd |= nonfinite2(w[n]);
+        for (int n = 0; n < 8; ++n) any |= nonfinite2(w[n]);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           lo[n] = __builtin_amdgcn_perm(w[2 * n + 1], w[2 * n], 0x05040100u);
@@ -343,9 +365,11 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
       for (int n = 0; n < kK8; ++n) store(DK, kKT, tid + n * kThreads, tk[n]);
 #pragma unroll
       for (int n = 0; n < kV8; ++n) store(DV, kVT, tid + n * kThreads, tv[n]);
+      if (!OUT && r0 + kChunk < rows) ask(kChunk);   // the next chunk's, while this one is worked on
     }
+    bool odd = (any & 0x80008000u) != 0;
     odd |= state_odd();
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if constexpr (OUT) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // what goes straight to LDS
     if (odd) s_odd[turn] = 1;
     __syncthreads();
     asm volatile("" : "+v"(q_turn), "+v"(k_turn));   // or every place is formed ahead of the loop, and spilled
@@ -397,7 +421,7 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
             const int j = 16 * (n >> 3) + (n & 7);
-            w[m][n] = j <= row - 32 * tj - line0 ? w[m][n] * __builtin_amdgcn_exp2f((float)(Gi - Gj[j])) : 0.f;
+            w[m][n] = j <= row - 32 * tj - line0 ? w[m][n] * a.scale * __builtin_amdgcn_exp2f((float)(Gi - Gj[j])) : 0.f;
           }
         }
       }
@@ -462,13 +486,17 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
       uint32_t step = 4u * a.v_heads * DV;
       asm volatile("" : "+s"(step));
       const uint32_t off = 4 * hh * step + 4 * col;
+      auto write = [&](auto whole) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          const int row = 32 * i + 8 * (n >> 2) + (n & 3);
-          if (row + 4 * hh < n_rows) *reinterpret_cast<float*>(op + (off + row * step)) = o[i][n] * a.scale;
-        }
+          for (int n = 0; n < 16; ++n) {
+            const int row = 32 * i + 8 * (n >> 2) + (n & 3);
+            if (whole || row + 4 * hh < n_rows) *reinterpret_cast<float*>(op + (off + row * step)) = o[i][n];
+          }
+      };
+      if (n_rows == kChunk) write(std::true_type{});
+      else write(std::false_type{});
     }
     // the state
     const float f_all = __builtin_amdgcn_exp2f((float)G_last);

@@ -1824,11 +1824,17 @@ LinearShape linear_shape(const q4nx_linear* L, int M) {
   LinearShape sh;
   memset(&sh, 0, sizeof sh);
   sh.total = 256;
-  sh.chunks = L->max_q > 16;
+  // Rows one by one cost about 0.7 us each, a chunk 13 us with its launch (32 heads of 128 x 128: 16 rows 15.4 us, 17
+  // in a chunk 13.0).
+  sh.chunks = L->max_q > 12;
   if (!sh.chunks) return sh;
+  // Sequences that fill the GPU by themselves, or have three chunks at most, run from end to end (8 of 512 rows, 32
+  // heads: 70 us, 87 in segments; one of 128 rows 19).  Others are cut so that segments fill it, in single chunks
+  // while there are few (one of 4096 rows: segments of 2, 4, 8 chunks 114, 92, 110 us; 3 of 333, 8 heads: segments of
+  // 1, 2 chunks 21, 27 us).
   const int64_t chunks = ((int64_t)M + 63) / 64 * L->v_heads;
-  sh.seg = 64 * (int)std::max<int64_t>(2, (chunks + 511) / 512);
-  sh.carried = L->max_q > sh.seg && L->n_seq * (int64_t)L->v_heads < 512;
+  sh.seg = 64 * (int)(chunks <= 384 ? 1 : std::max<int64_t>(2, (chunks + 511) / 512));
+  sh.carried = L->max_q > std::max(sh.seg, 192) && L->n_seq * (int64_t)L->v_heads < 256;
   if (!sh.carried) sh.seg = 1 << 30;
   sh.items = sh.carried ? M / sh.seg + L->n_seq : L->n_seq;
   if (!sh.carried) return sh;

@@ -235,7 +235,7 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
   // neighbouring heads, which share q and k, on one XCD (workgroups go round the eight)
   const int item = blockIdx.x / a.v_heads, nth = blockIdx.x % a.v_heads;
   const int h = a.v_heads % 8 ? nth : (nth & 7) * (a.v_heads >> 3) + (nth >> 3), kh = h / (a.v_heads / a.k_heads);
-  int seq, seg, start, end;
+  int seq, seg, start, end, last_item;
   {
     int32_t* first = reinterpret_cast<int32_t*>(lds);
     linear_plan(a, first, first + kAttnMaxSeq + 1);
@@ -248,6 +248,7 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
     seg = item - first[seq];
     start = first[kAttnMaxSeq + 1 + seq];
     end = first[kAttnMaxSeq + 2 + seq];
+    last_item = first[seq + 1] - 1;
     if (!OUT && seg == first[seq + 1] - first[seq] - 1) return;   // what the last one adds, it adds itself
   }
   const LinearSeq x = linear_seq(a, seq, start, end, &s_taken, OUT && h == 0 && seg == 0);
@@ -260,6 +261,7 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
     const float* from = nullptr;
     if (OUT) {
       if (seg > 0) from = a.seg_state + ((size_t)(item - 1) * a.v_heads + h) * state_size;
+      else if (last_item > item) from = a.seg_state + ((size_t)last_item * a.v_heads + h) * state_size;
       else if (!x.fresh) from = a.state + ((size_t)x.slot * a.v_heads + h) * state_size;
     }
 #pragma unroll
@@ -542,7 +544,9 @@ __global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
 }
 
 // The states that a sequence's segments begin with: what segment s left becomes
-// what segment s + 1 begins with.
+// what segment s + 1 begins with.  What the first begins with goes to the place
+// of the last, which left nothing: the last one's end may go to where the first
+// one's state is, and nothing says which of the two runs first.
 template <int DK, int DV>
 __global__ __launch_bounds__(256) void k_linear_carry(LinearArgs a) {
   __shared__ int32_t s_taken;
@@ -554,6 +558,7 @@ __global__ __launch_bounds__(256) void k_linear_carry(LinearArgs a) {
   const size_t at = (size_t)part * 1024 + 4 * threadIdx.x, size = (size_t)DK * DV;
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   if (!x.fresh) S = *reinterpret_cast<const f32x4*>(a.state + ((size_t)x.slot * a.v_heads + h) * size + at);
+  *reinterpret_cast<f32x4*>(a.seg_state + ((size_t)(first + segs - 1) * a.v_heads + h) * size + at) = S;
   for (int s = 0; s + 1 < segs; ++s) {
     const size_t i = (size_t)(first + s) * a.v_heads + h;
     const float f = __builtin_amdgcn_exp2f((float)a.seg_decay[i]);

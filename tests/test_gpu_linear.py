@@ -257,3 +257,37 @@ def test_a_prompt_in_pieces():
             c.dstart.copy_(torch.tensor([a, b], dtype=torch.int32))
             c.run()
         c.check(ref=ref)
+
+
+@pytest.mark.parametrize("lens,H", [([5000], 32), ([2600, 40, 1100], 8), ([700], 2)])
+def test_in_place_and_apart_end_alike(lens, H):
+    """The last segment's end goes where the first one's state is read from: same bits as with a state of its own."""
+    a = Case("place", lens, H // 2, H, 64, 64, speed=0.002).upload(False).run()
+    b = Case("place", lens, H // 2, H, 64, 64, speed=0.002).upload(True)
+    for _ in range(3):
+        b.dstate.copy_(a.dstate)
+        b.run()
+        torch.cuda.synchronize()
+        assert torch.equal(a.out, b.out)
+        for s in range(len(lens)):
+            assert torch.equal(a.dstate_out[a.slots[s]], b.dstate[a.slots[s]])
+
+
+@pytest.mark.parametrize("max_q", [1, 5, 13, 100, 300, 60000])
+def test_max_q_is_a_hint(max_q):
+    """Rows past max_q are computed all the same."""
+    Case("hint", [1, 70, 9, 330], 1, 2, 64, 64, max_q=max_q).upload(True).run().check()
+
+
+def test_all_rows_in_one_long_sequence_of_many():
+    """One sequence has all the rows of a call that other shapes would share."""
+    for lens in ([0] * 20 + [900] + [0] * 11, [1] * 40 + [500]):
+        Case("uneven", lens, 1, 1, 64, 64).upload(True).run().check()
+
+
+def test_scales():
+    for scale in (0.0, -1.5, 1e-30):
+        for n in (1, 100):
+            c = Case("scale", [n], 1, 1, 64, 64)
+            c.scale = scale
+            c.upload().run().check()

@@ -347,3 +347,61 @@ def test_offsets_past_two_and_four_billion_elements():
     c.cache = q().kv_cache(KH, D, page, pages, k, v, k_scale=ks, v_scale=vs)
     c.dtable += pages - c.pages
     c.run().check()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("max_q", [1, 5, 17, 40, 60000])
+def test_max_q_is_a_hint(kind, max_q):
+    """Whichever kernels max_q leads to, every row is computed."""
+    for prefix in (0, 100):
+        c = Case("hint", [1, 40, 3, 150], [90, 41, 200, 150], prefix, 4, 1, 64, 16, kind, max_q=max_q, extra_rows=2)
+        c.spoil()
+        c.upload().run().check()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("H,KH,D", [(8, 2, 128), (4, 4, 64), (6, 2, 256)])
+@pytest.mark.parametrize("q_len", [(1,) * 40, (4,) * 9, (9,) * 9, (1, 12, 0, 7)])
+def test_shared_prefix(kind, H, KH, D, q_len):
+    """Enough rows together that the prefix's kernel has tiles of its own, of 16, 32 and 128 rows."""
+    print(f"shared {kind} {H}/{KH} x {D}, rows {q_len}", flush=True)
+    for prefix in (40, 700):
+        c = Case("shared", list(q_len), [n + 13 * i % 90 for i, n in enumerate(q_len)], prefix, H, KH, D, 16, kind, extra_rows=1)
+        c.spoil()
+        c.upload().run().check()
+
+
+def test_prefix_alone():
+    """Sequences without tokens of their own, behind a prefix: their rows see it and nothing else."""
+    c = Case("alone", [1, 2, 1], [0, 0, 0], 333, 4, 2, 64, 16)
+    c.spoil()
+    c.upload().run().check()
+
+
+def test_values_that_only_later_rows_see_among_many_sequences():
+    """The same behind a shared prefix, for windows and for prompts, and in the first and the last tokens."""
+    for q_len, kv_len in (([4] * 6, [20] * 6), ([70, 90], [70, 300])):
+        for back in (0, q_len[0] - 1):
+            c, clean = (Case("later2", q_len, kv_len, 50, 4, 1, 64, 16) for _ in range(2))
+            tok = kv_len[0] - 1 - back
+            c.x["v"][c.table[0, tok // 16], 0, tok % 16, :9] = 0xFF80
+            c.spoil()
+            c.upload().run()
+            first = q_len[0] - 1 - back
+            got = synth.bf16_to_f32(host(c.out).view(np.uint16))
+            assert not np.isfinite(got[first:q_len[0], :, :9]).any()
+            out, _, mag, off = clean.reference()
+            keep = np.ones_like(got, bool)
+            keep[first:q_len[0], :, :9] = False
+            d = 2 * (64 + 8) * 2.0 ** -24 * off + 2.0 ** -22 * (4 + (max(kv_len) + 50) / 32)
+            tol = mag * (2 * d[..., None] + 2.0 ** -8 + (max(kv_len) + 114) * 2.0 ** -24) + 2.0 ** -8 * np.abs(out) + 2.0 ** -133
+            assert (np.abs(got - out)[keep] <= tol[keep]).all()
+
+
+def test_without_lse_and_flags():
+    for q_len, kv_len in (([1, 1], [300, 9]), ([90], [500])):
+        c = Case("bare", q_len, kv_len, 30, 4, 2, 64, 16).upload().run()
+        want = c.out.clone()
+        c.out.zero_()
+        q().attention(c.cache, c.batch, c.dq, c.H, c.M, c.scale, c.out, c.ws)
+        assert torch.equal(c.out, want)

@@ -604,15 +604,22 @@ def _row_step(t, columns: int, width: int, what: str) -> int:
     return columns if st[0] < columns and t.shape[0] == 1 else st[0]
 
 
+def _heads(t, n: int, head_dim: int) -> Heads:
+    size = t.element_size()
+    if size != 2 and size != 4:
+        raise Q4nxError(E_ARG, f"heads of type {t.dtype}: fp32 or bf16 are taken")
+    return Heads(t.data_ptr(), _row_step(t, n * head_dim, head_dim, "heads"), n, 1 if size == 2 else 0)
+
+
 def heads(t, n: int, head_dim: int, ld: int | None = None, bf16: bool | None = None) -> Heads:
     """M rows of n heads: fp32, or bf16 (bf16 or int16 tensors), rows ld elements apart (a tensor's first stride)."""
     if isinstance(t, int):
         return Heads(t, n * head_dim if ld is None else ld, n, _BF16 if bf16 else _F32)
-    size = t.element_size()
-    if size != 2 and size != 4:
-        raise Q4nxError(E_ARG, f"heads of type {t.dtype}: fp32 or bf16 are taken")
-    h = Heads(t.data_ptr(), _row_step(t, n * head_dim, head_dim, "heads") if ld is None else ld, n,
-              size == 2 if bf16 is None else bf16)
+    h = _heads(t, n, head_dim)
+    if ld is not None:
+        h.ld = ld
+    if bf16 is not None:
+        h.type = _BF16 if bf16 else _F32
     h._owner = t
     return h
 
@@ -621,18 +628,19 @@ def kv_append(cache: KvCache, k, v, slots, M: int, rope: Rope | None = None, q=N
               q_out=None, flags=None, stream=None) -> None:
     """k and v (tensors of kv_heads heads a row, or what heads() made) to the cache's slots[M], k turned by rope; q turned
     into q_out (bf16 [M][q_heads][head_dim])."""
-    D, n = cache.head_dim, cache.kv_heads
-    if not isinstance(k, Heads):
-        k = heads(k, n, D)
-    if not isinstance(v, Heads):
-        v = heads(v, n, D)
-    if q is not None and not isinstance(q, Heads):
-        if q_heads is None:
-            raise Q4nxError(E_ARG, "kv_append: q without q_heads")
-        q = heads(q, q_heads, D)
-    ref = ctypes.byref
-    _check(_lib.q4nx_kv_append(ref(cache), None if rope is None else ref(rope), None if q is None else ref(q), _ptr(q_out),
-                               ref(k), ref(v), _ptr(slots), M, _ptr(flags), _stream(stream)))
+    D, n, ref = cache.head_dim, cache.kv_heads, ctypes.byref
+    if type(k) is not Heads:
+        k = _heads(k, n, D)
+    if type(v) is not Heads:
+        v = _heads(v, n, D)
+    if q is not None:
+        if type(q) is not Heads:
+            if q_heads is None:
+                raise Q4nxError(E_ARG, "kv_append: q without q_heads")
+            q = _heads(q, q_heads, D)
+        q = ref(q)
+    _check(_lib.q4nx_kv_append(ref(cache), None if rope is None else ref(rope), q, _ptr(q_out), ref(k), ref(v), _ptr(slots), M,
+                               _ptr(flags), _stream(stream)))
 
 
 def attn_batch(q_start, kv_len, pages, max_q: int, prefix_len: int = 0, prefix_pages=None, n_seq: int | None = None,
@@ -663,12 +671,18 @@ def linear_attn_seqs(q_start, slots, max_q: int, fresh=None, n_seq: int | None =
     none), fresh int32 [n_seq] (not 0: begin with zeros) or None."""
     s = Linear(n_seq=slots.numel() if n_seq is None else n_seq, max_q=max_q, q_start=_ptr(q_start), slots=_ptr(slots),
                fresh=_ptr(fresh))
-    s._owners = (q_start, slots, fresh)
+    s._owners, s._made = (q_start, slots, fresh), {}
     return s
 
 
 def _linear(seqs: Linear, k_heads: int, v_heads: int, dk: int, dv: int, n_slots: int) -> Linear:
-    return Linear(k_heads, v_heads, dk, dv, seqs.n_seq, seqs.max_q, n_slots, seqs.q_start, seqs.slots, seqs.fresh)
+    """The sequences with a call's heads; each kind is made once."""
+    key = (k_heads, v_heads, dk, dv, n_slots)
+    made = seqs._made.get(key)
+    if made is None:
+        made = seqs._made[key] = Linear(k_heads, v_heads, dk, dv, seqs.n_seq, seqs.max_q, n_slots, seqs.q_start, seqs.slots,
+                                        seqs.fresh)
+    return made
 
 
 def linear_attn_ws(seqs: Linear, k_heads: int, v_heads: int, dk: int, dv: int, M: int) -> int:
@@ -683,19 +697,20 @@ def linear_attn(seqs: Linear, q, k, v, decay, k_heads: int, v_heads: int, dk: in
     """S = exp(decay) S + k v^T, out[M, v_heads, dv] (fp32) = scale q^T S, row by row of each sequence, from state[n_slots,
     v_heads, dk, dv] (fp32) into state_out (None: state itself).  Row strides come from tensors of two or three dimensions;
     a decay of one dimension is every token's."""
-    def step(t, ld, columns, width):
-        if ld is not None:
-            return ld
-        return columns if isinstance(t, int) else _row_step(t, columns, width, "linear_attn")
+    if q_ld is None:
+        q_ld = k_heads * dk if type(q) is int else _row_step(q, k_heads * dk, dk, "linear_attn")
+    if k_ld is None:
+        k_ld = k_heads * dk if type(k) is int else _row_step(k, k_heads * dk, dk, "linear_attn")
+    if v_ld is None:
+        v_ld = v_heads * dv if type(v) is int else _row_step(v, v_heads * dv, dv, "linear_attn")
     if decay_ld is None:
-        decay_ld = 0 if not isinstance(decay, int) and decay.dim() == 1 else step(decay, None, v_heads, 1)
+        decay_ld = v_heads if type(decay) is int else 0 if decay.dim() == 1 else _row_step(decay, v_heads, 1, "linear_attn")
     if n_slots is None:
         n_slots = state.numel() // (v_heads * dk * dv)
-    L = _linear(seqs, k_heads, v_heads, dk, dv, n_slots)
-    _check(_lib.q4nx_linear_attn(ctypes.byref(L), _ptr(q), step(q, q_ld, k_heads * dk, dk), _ptr(k),
-                                 step(k, k_ld, k_heads * dk, dk), _ptr(v), step(v, v_ld, v_heads * dv, dv), _ptr(decay),
-                                 decay_ld, M, scale, _ptr(state), _ptr(state if state_out is None else state_out), _ptr(out),
-                                 _ptr(ws), _nbytes(ws) if ws_bytes is None else ws_bytes, _ptr(flags), _stream(stream)))
+    _check(_lib.q4nx_linear_attn(ctypes.byref(_linear(seqs, k_heads, v_heads, dk, dv, n_slots)), _ptr(q), q_ld, _ptr(k), k_ld,
+                                 _ptr(v), v_ld, _ptr(decay), decay_ld, M, scale, _ptr(state),
+                                 _ptr(state if state_out is None else state_out), _ptr(out), _ptr(ws),
+                                 _nbytes(ws) if ws_bytes is None else ws_bytes, _ptr(flags), _stream(stream)))
 
 
 def unpack(w: Weight, codes, meta0, meta1=None, row_meta=None, stream=None) -> None:

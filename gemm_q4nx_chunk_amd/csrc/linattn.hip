@@ -217,7 +217,7 @@ __device__ inline void linear_plan(const LinearArgs& a, int32_t* first, int32_t*
 }  // namespace
 
 template <int DK, int DV, bool OUT>
-__global__ __launch_bounds__(2 * DV, 2) void k_linear_chunks(LinearArgs a) {
+__global__ __launch_bounds__(2 * DV, DV == 64 ? 1 : 2) void k_linear_chunks(LinearArgs a) {
   constexpr int kThreads = 2 * DV, kWaves = DV / 32, NT = DK / 32;
   // elements: q [64][DK/8][8] | k likewise, then the rows' weights [3][8][64][8] | k^T [8][DK][8] | v^T [8][DV][8].
   // Piece p of row r of q and k lies at p ^ turned(r), so that 16 rows' pieces of one column are 16 different

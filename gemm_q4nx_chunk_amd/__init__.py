@@ -599,16 +599,22 @@ def _row_step(t, columns: int, width: int, what: str) -> int:
     st = t.stride()
     if len(st) < 2:
         return columns
-    if st[-1] != 1 or (len(st) == 3 and st[1] != width and t.shape[1] > 1):
+    if len(st) > 3 or st[-1] != 1 or (len(st) == 3 and st[1] != width and t.shape[1] > 1):
         raise Q4nxError(E_SHAPE, f"{what}: the columns of a row must be contiguous")
     return columns if st[0] < columns and t.shape[0] == 1 else st[0]
 
 
+_HEAD_TYPES: dict = {}   # by dtype; names are looked at once
+
+
 def _heads(t, n: int, head_dim: int) -> Heads:
-    size = t.element_size()
-    if size != 2 and size != 4:
-        raise Q4nxError(E_ARG, f"heads of type {t.dtype}: fp32 or bf16 are taken")
-    return Heads(t.data_ptr(), _row_step(t, n * head_dim, head_dim, "heads"), n, 1 if size == 2 else 0)
+    kind = _HEAD_TYPES.get(t.dtype)
+    if kind is None:
+        kind = {"float32": _F32, "bfloat16": _BF16, "int16": _BF16}.get(str(t.dtype).rpartition(".")[2])
+        if kind is None:
+            raise Q4nxError(E_ARG, f"heads of type {t.dtype}: fp32 or bf16 (or its bits, int16) are taken")
+        _HEAD_TYPES[t.dtype] = kind
+    return Heads(t.data_ptr(), _row_step(t, n * head_dim, head_dim, "heads"), n, kind)
 
 
 def heads(t, n: int, head_dim: int, ld: int | None = None, bf16: bool | None = None) -> Heads:
@@ -671,17 +677,14 @@ def linear_attn_seqs(q_start, slots, max_q: int, fresh=None, n_seq: int | None =
     none), fresh int32 [n_seq] (not 0: begin with zeros) or None."""
     s = Linear(n_seq=slots.numel() if n_seq is None else n_seq, max_q=max_q, q_start=_ptr(q_start), slots=_ptr(slots),
                fresh=_ptr(fresh))
-    s._owners, s._made = (q_start, slots, fresh), {}
+    s._owners = (q_start, slots, fresh)
     return s
 
 
 def _linear(seqs: Linear, k_heads: int, v_heads: int, dk: int, dv: int, n_slots: int) -> Linear:
-    """The sequences with a call's heads; each kind is made once."""
-    key = (k_heads, v_heads, dk, dv, n_slots)
-    made = seqs._made.get(key)
-    if made is None:
-        made = seqs._made[key] = Linear(k_heads, v_heads, dk, dv, seqs.n_seq, seqs.max_q, n_slots, seqs.q_start, seqs.slots,
-                                        seqs.fresh)
+    """The sequences with a call's heads: a copy, so that calls may share what linear_attn_seqs made."""
+    made = Linear.from_buffer_copy(seqs)
+    made.k_heads, made.v_heads, made.dk, made.dv, made.n_slots = k_heads, v_heads, dk, dv, n_slots
     return made
 
 

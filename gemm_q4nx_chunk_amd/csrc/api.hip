@@ -1943,7 +1943,8 @@ int q4nx_attention(const q4nx_kv_cache* cache, const q4nx_attn_batch* batch, con
   if (!q || !out) return fail(Q4NX_E_ARG, "attention: null q or out");
   if (!b.q_start || !b.kv_len || !b.pages || (b.prefix_len && !b.prefix_pages))
     return fail(Q4NX_E_ARG, "attention: null q_start, kv_len, pages or prefix_pages");
-  if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return fail(Q4NX_E_ARG, "attention: scale = %g is not finite", scale);
+  if (!(scale >= -1e38f && scale <= 1e38f))   // times log2(e) it is still finite
+    return fail(Q4NX_E_ARG, "attention: scale = %g is beyond 1e38 in size, or NaN", scale);
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(flags, 4) || !aligned(b.q_start, 4) ||
       !aligned(b.kv_len, 4) || !aligned(b.pages, 4) || !aligned(b.prefix_pages, 4))
     return fail(Q4NX_E_ALIGN, "attention: q and out must be 16-byte, every other array 4-byte aligned");

@@ -247,6 +247,30 @@ def test_linear_binding(q):
     _expect(q, q.E_SHAPE, _linear, q, decay=torch.zeros(4, 3).t())
 
 
+def test_types_and_dimensions_that_are_not_taken(q):
+    torch = pytest.importorskip("torch")
+    c, k = _cache(q), torch.zeros(3, KH * D)
+    for dtype in (torch.float16, torch.int32, torch.uint8):
+        _expect(q, q.E_ARG, q.kv_append, c, k.to(dtype), k, 0x7000000, 3, stream=0)
+        _expect(q, q.E_ARG, q.kv_append, c, k, k.to(dtype), 0x7000000, 3, stream=0)
+        _expect(q, q.E_ARG, q.heads, k.to(dtype), KH, D)
+    assert q.heads(torch.zeros(3, KH * D, dtype=torch.int16), KH, D).type == 1
+    _expect(q, q.E_SHAPE, q.kv_append, c, torch.zeros(1, 3, KH, D), k, 0x7000000, 3, stream=0)
+    for scale in (3e38, -2.5e38, float("nan")):      # times log2(e) beyond fp32
+        _expect(q, q.E_ARG, _attend, q, scale=scale)
+
+
+def test_linear_sequences_may_change_between_calls(q):
+    s = _seqs(q, max_q=1)
+    few = q.linear_attn_ws(s, 2, 4, 64, 128, 4096)
+    s.max_q = 4096
+    long = q.linear_attn_ws(s, 2, 4, 64, 128, 4096)
+    assert few == q.linear_attn_ws(_seqs(q, max_q=1), 2, 4, 64, 128, 4096) < long == q.linear_attn_ws(_seqs(q, max_q=4096), 2, 4, 64, 128, 4096)
+    _expect(q, q.E_WORKSPACE, _linear, q, s, M=4096, ws_bytes=long - 1, q=0x100000000, k=0x200000000, v=0x300000000, decay=0x400000000,
+            out=0x500000000)
+    assert (s.k_heads, s.v_heads, s.n_slots) == (0, 0, 0)
+
+
 # ----------------------------------------------------------------------------
 # the checks under the host sanitisers
 # ----------------------------------------------------------------------------

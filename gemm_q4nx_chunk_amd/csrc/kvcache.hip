@@ -3,9 +3,9 @@
 //   t = pos * inv_freq[i];  (a, b) -> (a cos t - b sin t, b cos t + a sin t)
 //
 // A workgroup has one token or eight and a part of their heads: it forms the
-// angles of its tokens once (fp64: pos * inv_freq is exact there, and the sine
-// and cosine reduce it without losing a far position's digits), keeps them in
-// LDS, and turns every head with them.  A lane has two pieces of eight values, so
+// angles of its tokens once (in fp64, which holds pos * inv_freq to 53 bits: all
+// of them for positions below 2^29, and what is lost of others is far below a
+// bf16's step), keeps them in LDS, and turns every head with them.  A lane has two pieces of eight values, so
 // that both sides of a pair and what the cache holds together are one lane's.
 // Each value is read once and written once.
 //

@@ -679,8 +679,8 @@ typedef struct q4nx_kv_cache {
 enum { Q4NX_F32 = 0, Q4NX_BF16 = 1 };
 typedef struct q4nx_heads {
   const void* p;        /* DEVICE, aligned to its element */
-  int64_t ld;           /* elements between rows, at least heads * head_dim */
-  int32_t heads;
+  int64_t ld;           /* elements between rows, at least heads * head_dim, at most 2^40 */
+  int32_t heads;        /* heads * head_dim at most 16384 */
   int32_t type;         /* Q4NX_F32 (what a projection wrote) or Q4NX_BF16 (what a norm wrote) */
 } q4nx_heads;
 
@@ -688,7 +688,7 @@ typedef struct q4nx_heads {
 typedef struct q4nx_rope {
   int32_t dim;             /* leading dimensions that turn: a multiple of 16, 16..head_dim */
   int32_t interleaved;     /* 0: pair (i, i + dim/2); 1: pair (2i, 2i + 1) */
-  const float* inv_freq;   /* DEVICE fp32 [dim/2] */
+  const float* inv_freq;   /* DEVICE fp32 [dim/2]; pos * inv_freq below 2^40 in size */
   const int32_t* pos;      /* DEVICE int32 [M], any value */
 } q4nx_rope;
 
@@ -701,7 +701,7 @@ enum { Q4NX_KV_MAX_M = 16384 };   /* most rows of one q4nx_kv_append */
  *   (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = pos[m] * inv_freq[i]
  * The angle is formed and reduced in fp64, so that positions of any size keep
  * their digits.  bf16 values are rounded once, from fp32.  INT8 values are
- * formed in fp64 and cached as scale = fp32(max |x| / 127), code =
+ * formed in fp64 from the fp64 turn and cached as scale = fp32(max |x| / 127), code =
  * round(x / scale), half to even, per token and head; a head of zeros has scale
  * 0, and one with an infinity or NaN an infinite or NaN scale with codes 0.
  *   q      heads * head_dim columns, or NULL (with q_out NULL): only k and v
@@ -747,9 +747,10 @@ enum { Q4NX_ATTN_MAX_SEQ = 1024, Q4NX_ATTN_MAX_M = 65536 };
  *   lse   DEVICE fp32 [M][q_heads], or NULL
  *   M     rows of q, out and lse, 1..Q4NX_ATTN_MAX_M.  Rows behind the last sequence, and
  *         rows before the first, are left as they were.
- *   scale finite
- *   ws    DEVICE workspace of q4nx_attention_ws bytes for these arguments, 256-byte
- *         aligned.  Nothing in it needs initialising; calls that share it must not overlap.
+ *   scale 1e38 at most in size
+ *   ws    DEVICE workspace of q4nx_attention_ws bytes for these arguments (they never fall
+ *         as M alone grows), 256-byte aligned.  Nothing in it needs initialising; calls that
+ *         share it must not overlap.
  *   flags DEVICE uint32 or NULL; the call only sets bits, the caller clears them
  * One token, windows of a few and whole prompts go through the same call; where
  * several sequences have few rows each, the prefix is read once for all.
@@ -760,8 +761,10 @@ enum { Q4NX_ATTN_MAX_SEQ = 1024, Q4NX_ATTN_MAX_M = 65536 };
  * as unseen, and bit 0 of *flags is set.  A kv_len outside 0..pages_ld *
  * page_tokens, and rows of q_start that fall or leave 0..M, are clamped, and
  * bit 1 is set.
- * Scores, maxima, sums and outputs are fp32; the softmax's numerators enter the
- * second product in bf16, the sum of them does not.  Parts of a long row are
+ * Scores, maxima, sums and outputs are fp32 and divided at the end, so that values
+ * near fp32's largest overflow; the softmax's numerators enter the second product
+ * in two bf16 parts (16 bits), and, where sequences have more than 32 rows of one
+ * key head, in one; the sum of them is of the fp32 numerators.  Parts of a long row are
  * joined in a fixed order; how rows are cut into parts goes by the whole batch's
  * lengths, so that a row's last bits may differ between batches.
  * E_SHAPE: q_heads no multiple of kv_heads, or more than 16384 columns of q.
@@ -794,7 +797,7 @@ typedef struct q4nx_linear {
  * over the rows of each sequence in order.  Value head h reads q and k of head
  * h / (v_heads / k_heads).
  *   q, k   DEVICE bf16, row m at q + m*q_ld, k + m*k_ld: [k_heads][dk]; 16-byte aligned, strides a
- *          multiple of 8 elements
+ *          multiple of 8 elements, 2^24 at most
  *   v      DEVICE bf16, row m at v + m*v_ld: [v_heads][dv], likewise
  *   decay  DEVICE fp32, row m at decay + m*decay_ld: [v_heads], decay_ld at least v_heads, or 0:
  *          the same for every token.  Natural logarithms, of 0 at most (-Inf forgets all); a larger
@@ -804,11 +807,14 @@ typedef struct q4nx_linear {
  *              checkpoint to go back to).  Slots of no sequence, or of one without rows, are left as they were.
  *   out    DEVICE fp32 [M][v_heads][dv], 16-byte aligned; rows of no sequence are left as they were
  *   M      1..Q4NX_ATTN_MAX_M rows
- *   ws     DEVICE workspace of q4nx_linear_attn_ws(L, M) bytes, 256-byte aligned.  Nothing in
- *          it needs initialising; calls that share it must not overlap.
+ *   ws     DEVICE workspace of q4nx_linear_attn_ws(L, M) bytes (a smaller M may need more), 256-byte
+ *          aligned.  Nothing in it needs initialising; calls that share it must not overlap.
  *   flags  DEVICE uint32 or NULL; the call only sets bits, the caller clears them
  * Few rows run as the recurrence, prompts in chunks of 64 rows whose products go
- * to the matrix cores with every operand's 24 bits: states and sums are fp32.
+ * to the matrix cores with every operand's 24 bits: states and sums are fp32, and
+ * what passes fp32's range comes out as an infinity or NaN.  An infinity or NaN
+ * that comes in reaches what the recurrence lets it reach: not what is before it,
+ * nor what a decay whose exp is 0 has cut off.
  * A slot outside -1..n_slots-1, or one that an earlier sequence with rows has, is
  * taken as -1 and sets bit 0.  Rows of q_start that fall or leave 0..M are
  * clamped, and bit 2 is set.

@@ -168,6 +168,14 @@ def test_attention_workspace(q, q_heads, max_q, prefix):
     assert q.attention_ws(_cache(q, k=0, v=0), b, q_heads, 1) > 0      # pointers are not looked at
 
 
+@pytest.mark.parametrize("max_q", [1, 4, 9, 16, 100])
+@pytest.mark.parametrize("prefix", [0, 20])
+@pytest.mark.parametrize("q_heads", [2, 4, 32])
+def test_attention_workspace_grows_with_the_rows(q, max_q, prefix, q_heads):
+    need = [q.attention_ws(_cache(q), _batch(q, max_q=max_q, prefix_len=prefix), q_heads, M) for M in [*range(1, 300), 4096, 65536]]
+    assert need == sorted(need)
+
+
 def test_attention_outputs_apart(q):
     c, b = _cache(q), _batch(q)
     need, size, cb = q.attention_ws(c, b, 4, 3), 3 * 4 * D * 2, TOKENS * D * 2

@@ -550,7 +550,7 @@ __global__ __launch_bounds__(2 * DV, DV == 64 ? 1 : 2) void k_linear_chunks(Line
 template <int DK, int DV>
 __global__ __launch_bounds__(256) void k_linear_carry(LinearArgs a) {
   __shared__ int32_t s_taken;
-  constexpr int kParts = DK * DV / 1024;
+  constexpr int kParts = DK * DV / 1024, kAhead = 8;
   const int part = blockIdx.x % kParts, h = blockIdx.x / kParts, seq = blockIdx.y;
   const int first = a.plan[seq], segs = a.plan[seq + 1] - first;
   if (segs < 2) return;
@@ -559,14 +559,24 @@ __global__ __launch_bounds__(256) void k_linear_carry(LinearArgs a) {
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   if (!x.fresh) S = *reinterpret_cast<const f32x4*>(a.state + ((size_t)x.slot * a.v_heads + h) * size + at);
   *reinterpret_cast<f32x4*>(a.seg_state + ((size_t)(first + segs - 1) * a.v_heads + h) * size + at) = S;
-  for (int s = 0; s + 1 < segs; ++s) {
-    const size_t i = (size_t)(first + s) * a.v_heads + h;
-    const float f = __builtin_amdgcn_exp2f((float)a.seg_decay[i]);
-    float* p = a.seg_state + i * size + at;
-    const f32x4 u = *reinterpret_cast<const f32x4*>(p);
+  for (int s0 = 0; s0 + 1 < segs; s0 += kAhead) {   // their loads together: they wait for nothing, the sums for each other
+    f32x4 u[kAhead];
+    double d[kAhead];
+    const int last = segs - 2;
 #pragma unroll
-    for (int n = 0; n < 4; ++n) S[n] = (f == 0.f ? 0.f : f * S[n]) + u[n];
-    *reinterpret_cast<f32x4*>(p) = S;
+    for (int j = 0; j < kAhead; ++j) {
+      const size_t i = (size_t)(first + min(s0 + j, last)) * a.v_heads + h;
+      d[j] = a.seg_decay[i];
+      u[j] = *reinterpret_cast<const f32x4*>(a.seg_state + i * size + at);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (s0 + j > last) break;
+      const float f = __builtin_amdgcn_exp2f((float)d[j]);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) S[n] = (f == 0.f ? 0.f : f * S[n]) + u[j][n];
+      *reinterpret_cast<f32x4*>(a.seg_state + ((size_t)(first + s0 + j) * a.v_heads + h) * size + at) = S;
+    }
   }
 }
 

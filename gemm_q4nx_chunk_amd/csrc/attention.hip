@@ -71,6 +71,9 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, int D, 
 // keys are asked for as soon as the products have taken the last ones, the next
 // values likewise: 16 KB a wave are always on the way.  Bound by memory, so that
 // the softmax's numerators can enter in two bf16 parts, which hold 16 bits.
+// (32 heads of 128: one token of 1000, 8192, 32768: 10.9, 15.4, 32.8 us a call, 4.1
+// TB/s at the last; 64 tokens of 2000: 72 us, 4.6 TB/s; over 8 bits 46, where turning
+// codes to bf16 holds it back.)
 template <int D, bool I8, int RB>
 __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, int block, int blocks, AttnPlan& plan, uint8_t* lds) {
   constexpr int kRows = 16 * RB, NS = D / 32, NJ = D / 16, kLd = D + 4;
@@ -329,6 +332,14 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
 // The maximum that scores are taken against is raised only when a row's grows
 // by 2^8: numerators up to 2^8 lose nothing in bf16 or in the fp32 sums, and the
 // outputs are rescaled a few times a row instead of once a tile.
+//
+// Bound by the matrix cores (44 % busy) and the softmax between them: 4096 tokens
+// over 16384 of 32 heads of 128 run at 940 TFLOP/s, where a large library product
+// reaches 1235; 2048 over 8192 at 820 (64 wide: 620, 256 wide: 610).  Eight waves of
+// 256 rows, half of them at the products while the others are at the softmax, with
+// a barrier at each change, were slower (319 us for 300, 64 wide 232 for 193): the
+// barriers and what is done between them cost more than the overlap gave, which two
+// workgroups a CU find by themselves.
 template <int D, bool I8, int KT>
 __device__ __forceinline__ void attn_many(const AttnArgs& a, const AttnParts& p, int block, int blocks, AttnPlan& plan, uint8_t* lds) {
   constexpr int kRows = 128, NQ = D / 16, NB = KT / 32, NO = D / 32, kBlocks = KT / 16, kTiles = kAttnUnit / KT;
@@ -653,7 +664,7 @@ __global__ __launch_bounds__(256, attn_occupancy(D, I8, ROWS)) void k_attn(AttnA
 // prefix's parts (tiles of PRE rows), the others the sequences' (OWN rows).  Side
 // by side, the prefix's products fill the matrix cores while the sequences' keys
 // and values stream (16 windows over 8 bits: 45 us, one after the other 71; 64
-// tokens behind 8192: 97 for 109).
+// tokens behind 8192: 92 for 109, of which this kernel has 82, 4.4 TB/s).
 template <int D, bool I8, int OWN, int PRE>
 __global__ __launch_bounds__(256, attn_occupancy(D, I8, OWN > PRE ? OWN : PRE)) void k_attn_shared(AttnArgs a, AttnPair sets, int pre_grid) {
   __shared__ AttnPlan plan;
@@ -785,7 +796,8 @@ hipError_t launch_attn(const AttnArgs& a, const AttnParts& own, int own_grid, co
 }
 
 hipError_t launch_attn_join(const AttnArgs& a, const AttnParts& own, const AttnParts& prefix, hipStream_t s) {
-  // from about 64 rows of 32 heads on the heads alone fill the GPU (64 rows, 26 parts: TBD)
+  // from about 64 rows of 32 heads on the heads alone fill the GPU (64 rows of 26 parts: 8.3 us); under it a head's
+  // parts are shared out (16 windows of 28 heads: 7.9 us; a call is the same within 1 us with the border at 1024)
 #define Q4NX_JOIN(D)                                                                                                     \
   if ((int64_t)a.M * a.q_heads < 2048)                                                                                   \
     hipLaunchKernelGGL((k_attn_join<D, 1024 / D>), dim3(a.M, a.q_heads), dim3(256), 0, s, a, own, prefix);               \

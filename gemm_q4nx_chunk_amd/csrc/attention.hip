@@ -125,17 +125,27 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
       if (u < pre_units && u * kAttnUnit + 32 * wave >= x.pre) u = pre_units;
       return u < u1 && (u < pre_units || (u - pre_units) * kAttnUnit + 32 * wave < lim_last) ? u : u1;
     };
-    auto keys_of = [&](int u) {
+    // The pages of a unit's halves are asked for ahead of the keys of the unit before: loads come back in order, and a
+    // page that is waited for would be waited for behind all keys and values on the way.
+    struct Pages { int p0, p1; };
+    auto ask_pages = [&](int u) {
+      const bool pre = u < pre_units;
+      const int key0 = (pre ? u : u - pre_units) * kAttnUnit + 32 * wave, last = (pre ? x.pre : lim_last) - 1;
+      const int32_t* table = pre ? a.prefix_pages : own_pages;
+      return Pages{table[key0 >> ps], table[min(key0 + 16, last) >> ps]};
+    };
+    auto keys_of = [&](int u, const Pages& g) {
       Keys k;
       k.u = u;
       k.pre = u < pre_units;
       k.key0 = (k.pre ? u : u - pre_units) * kAttnUnit + 32 * wave;
       k.have = k.pre ? x.pre : lim_last;
-      const int32_t* table = k.pre ? a.prefix_pages : own_pages;
-      k.ok0 = attn_page(a.c, a.flags, table[k.key0 >> ps], head, k.at0);
-      k.ok1 = false;   // a half of no keys reads what is there of the first one's page
-      if (k.key0 + 16 >= k.have) k.at1 = k.at0;
-      else k.ok1 = attn_page(a.c, a.flags, table[(k.key0 + 16) >> ps], head, k.at1);
+      k.ok0 = attn_page(a.c, a.flags, __builtin_amdgcn_readfirstlane(g.p0), head, k.at0);
+      k.ok1 = attn_page(a.c, a.flags, __builtin_amdgcn_readfirstlane(g.p1), head, k.at1);
+      if (k.key0 + 16 >= k.have) {   // a half of no keys reads what is there of the first one's page
+        k.ok1 = false;
+        k.at1 = k.at0;
+      }
       k.t0 = k.key0 & ((1 << ps) - 1);
       k.t1 = (k.key0 + 16) & ((1 << ps) - 1);
       return k;
@@ -163,16 +173,22 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
       if constexpr (I8) scales(a.c.vs, k, vs);
     };
 
-    int u = next_unit(u0);
+    // what follows the last unit is the last again: no load stands under a branch
+    auto after = [&](int u) {
+      const int n = next_unit(u + 1);
+      return n < u1 ? n : u;
+    };
+    int u = next_unit(u0), un = u;
     Keys cur;
+    Pages pages;
     if (u < u1) {
-      cur = keys_of(u);
+      cur = keys_of(u, ask_pages(u));
+      un = after(u);
+      pages = ask_pages(un);
       ask_keys(cur);
       ask_values(cur);
     }
-    while (u < u1) {
-      const int un = next_unit(u + 1);
-      const Keys nxt = un < u1 ? keys_of(un) : cur;   // the last keys are asked for twice: no load stands under a branch
+    for (bool more = u < u1; more;) {
       f32x4 st[RB][2];
 #pragma unroll
       for (int b = 0; b < RB; ++b) st[b][0] = st[b][1] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -193,6 +209,9 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
           if constexpr (I8) z[b][n] *= ks[n >> 2][n & 3];
         }
       __builtin_amdgcn_sched_barrier(0);
+      const Keys nxt = keys_of(un, pages);
+      const int uf = after(un);
+      pages = ask_pages(uf);
       ask_keys(nxt);
       __builtin_amdgcn_sched_barrier(0);
       const int mine = cur.key0 + 8 * g;   // the lane's first key
@@ -272,7 +291,9 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
       __builtin_amdgcn_sched_barrier(0);
       ask_values(nxt);
       cur = nxt;
+      more = un != u;
       u = un;
+      un = uf;
     }
     // the four waves' parts become one
     const bool whole = at.split == 1 && p.set == ATTN_ALL;

@@ -178,122 +178,123 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
       const int n = next_unit(u + 1);
       return n < u1 ? n : u;
     };
-    int u = next_unit(u0), un = u;
-    Keys cur;
-    Pages pages;
+    int u = next_unit(u0);
     if (u < u1) {
-      cur = keys_of(u, ask_pages(u));
-      un = after(u);
-      pages = ask_pages(un);
+      Keys cur = keys_of(u, ask_pages(u));
+      int un = after(u);
+      Pages pages = ask_pages(un);
+      __builtin_amdgcn_sched_barrier(0);   // in the loop's order, or the loop waits for values before its first product
       ask_keys(cur);
+      __builtin_amdgcn_sched_barrier(0);
       ask_values(cur);
-    }
-    for (bool more = u < u1; more;) {
-      f32x4 st[RB][2];
-#pragma unroll
-      for (int b = 0; b < RB; ++b) st[b][0] = st[b][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < NS; ++s)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const bf16x8 k8 = kf[2 * s + n].get();
-#pragma unroll
-          for (int b = 0; b < RB; ++b) st[b][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8, qf[b][s], st[b][n], 0, 0, 0);
-        }
-      float z[RB][8];
-#pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          z[b][n] = st[b][n >> 2][n & 3] * a.scale;
-          if constexpr (I8) z[b][n] *= ks[n >> 2][n & 3];
-        }
       __builtin_amdgcn_sched_barrier(0);
-      const Keys nxt = keys_of(un, pages);
-      const int uf = after(un);
-      pages = ask_pages(uf);
-      ask_keys(nxt);
-      __builtin_amdgcn_sched_barrier(0);
-      const int mine = cur.key0 + 8 * g;   // the lane's first key
-      const bool ok = g & 2 ? cur.ok1 : cur.ok0;
-      const bool masked = cur.key0 + 32 > (cur.pre ? x.pre : lim_first) || !cur.ok0 || !cur.ok1;
-      if (masked) {
+      for (bool more = true; more;) {   // in here, or the compiler sees a way to it past the loads and waits for all
+        f32x4 st[RB][2];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) st[b][0] = st[b][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const bf16x8 k8 = kf[2 * s + n].get();
+#pragma unroll
+            for (int b = 0; b < RB; ++b) st[b][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8, qf[b][s], st[b][n], 0, 0, 0);
+          }
+        float z[RB][8];
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            z[b][n] = st[b][n >> 2][n & 3] * a.scale;
+            if constexpr (I8) z[b][n] *= ks[n >> 2][n & 3];
+          }
+        __builtin_amdgcn_sched_barrier(0);
+        const Keys nxt = keys_of(un, pages);
+        const int uf = after(un);
+        pages = ask_pages(uf);
+        ask_keys(nxt);
+        __builtin_amdgcn_sched_barrier(0);
+        const int mine = cur.key0 + 8 * g;   // the lane's first key
+        const bool ok = g & 2 ? cur.ok1 : cur.ok0;
+        const bool masked = cur.key0 + 32 > (cur.pre ? x.pre : lim_first) || !cur.ok0 || !cur.ok1;
+        if (masked) {
+#pragma unroll
+          for (int b = 0; b < RB; ++b) {
+            const int lim = ok ? (cur.pre ? x.pre : lim_own[b]) - mine : 0;
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+              if (n >= lim) z[b][n] = kNegInf;
+          }
+        }
+        bf16x8 hi[RB], lo[RB];
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-          const int lim = ok ? (cur.pre ? x.pre : lim_own[b]) - mine : 0;
+          float top = z[b][0];
 #pragma unroll
-          for (int n = 0; n < 8; ++n)
-            if (n >= lim) z[b][n] = kNegInf;
+          for (int n = 1; n < 8; ++n) top = fmaxf(top, z[b][n]);
+          top = fmaxf(top, __shfl_xor(top, 16));
+          top = fmaxf(top, __shfl_xor(top, 32));
+          if (__ballot(top > m_run[b] + 8.f)) {   // as below, in many rows
+            const float m_new = fmaxf(m_run[b], top);
+            const float alpha = __builtin_amdgcn_exp2f(m_run[b] - (m_new == kNegInf ? 0.f : m_new));
+            m_run[b] = m_new;
+            l_run[b] *= alpha;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) acc[b][j] *= alpha;
+          }
+          const float base = m_run[b] == kNegInf ? 0.f : m_run[b];
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            float e = __builtin_amdgcn_exp2f(z[b][n] - base);
+            l_run[b] += e;
+            if constexpr (I8) e = z[b][n] == kNegInf ? 0.f : e * vs[n >> 2][n & 3];
+            hi[b][n] = (__bf16)e;
+            lo[b][n] = (__bf16)(e - (float)hi[b][n]);
+          }
         }
-      }
-      bf16x8 hi[RB], lo[RB];
+        uint32_t odd = 0;
+        if (!I8 && masked) {
+          // values behind the tokens may be anything: 0 instead.  An infinity or NaN that only some of the rows
+          // see is kept out of the product, which has a 0 for the others, and added to those rows.
+          const int there = ok ? cur.have - mine : 0;
+          const bool some = !cur.pre && lim_first < lim_last;
 #pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        float top = z[b][0];
-#pragma unroll
-        for (int n = 1; n < 8; ++n) top = fmaxf(top, z[b][n]);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        if (__ballot(top > m_run[b] + 8.f)) {   // as below, in many rows
-          const float m_new = fmaxf(m_run[b], top);
-          const float alpha = __builtin_amdgcn_exp2f(m_run[b] - (m_new == kNegInf ? 0.f : m_new));
-          m_run[b] = m_new;
-          l_run[b] *= alpha;
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) acc[b][j] *= alpha;
+          for (int j = 0; j < NJ; ++j) odd |= vf[j].keep(there, some);
         }
-        const float base = m_run[b] == kNegInf ? 0.f : m_run[b];
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          float e = __builtin_amdgcn_exp2f(z[b][n] - base);
-          l_run[b] += e;
-          if constexpr (I8) e = z[b][n] == kNegInf ? 0.f : e * vs[n >> 2][n & 3];
-          hi[b][n] = (__bf16)e;
-          lo[b][n] = (__bf16)(e - (float)hi[b][n]);
+        for (int j = 0; j < NJ; ++j) {
+          const bf16x8 v8 = vf[j].get();
+#pragma unroll
+          for (int b = 0; b < RB; ++b) {
+            acc[b][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8, lo[b], acc[b][j], 0, 0, 0);
+            acc[b][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8, hi[b], acc[b][j], 0, 0, 0);
+          }
         }
-      }
-      uint32_t odd = 0;
-      if (!I8 && masked) {
-        // values behind the tokens may be anything: 0 instead.  An infinity or NaN that only some of the rows
-        // see is kept out of the product, which has a 0 for the others, and added to those rows.
-        const int there = ok ? cur.have - mine : 0;
-        const bool some = !cur.pre && lim_first < lim_last;
+        if (!I8 && __ballot(odd != 0)) {
+          for (int n = 0; n < 32 && cur.key0 + n < cur.have; ++n) {
+            const bool half = n & 16;
+            if (!(half ? cur.ok1 : cur.ok0)) continue;
+            const uint16_t* vp = static_cast<const uint16_t*>(a.c.v) + (half ? cur.at1 : cur.at0);
+            const int tok = half ? cur.t1 + (n & 15) : cur.t0 + n;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) odd |= vf[j].keep(there, some);
-      }
+            for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const bf16x8 v8 = vf[j].get();
+              for (int d = 0; d < 4; ++d) {
+                const float v = bf16lo(vp[v_place(D, tok, 16 * j + 4 * g + d)]);
 #pragma unroll
-        for (int b = 0; b < RB; ++b) {
-          acc[b][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8, lo[b], acc[b][j], 0, 0, 0);
-          acc[b][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8, hi[b], acc[b][j], 0, 0, 0);
+                for (int b = 0; b < RB; ++b)
+                  if (!(fabsf(v) <= __FLT_MAX__) && cur.key0 + n < lim_own[b]) acc[b][j][d] += v;
+                if (d == 3) __builtin_amdgcn_sched_barrier(0);   // or all are read at once, and spill others
+              }
+          }
         }
+        __builtin_amdgcn_sched_barrier(0);
+        ask_values(nxt);
+        cur = nxt;
+        more = un != u;
+        u = un;
+        un = uf;
       }
-      if (!I8 && __ballot(odd != 0)) {
-        for (int n = 0; n < 32 && cur.key0 + n < cur.have; ++n) {
-          const bool half = n & 16;
-          if (!(half ? cur.ok1 : cur.ok0)) continue;
-          const uint16_t* vp = static_cast<const uint16_t*>(a.c.v) + (half ? cur.at1 : cur.at0);
-          const int tok = half ? cur.t1 + (n & 15) : cur.t0 + n;
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-              const float v = bf16lo(vp[v_place(D, tok, 16 * j + 4 * g + d)]);
-#pragma unroll
-              for (int b = 0; b < RB; ++b)
-                if (!(fabsf(v) <= __FLT_MAX__) && cur.key0 + n < lim_own[b]) acc[b][j][d] += v;
-              if (d == 3) __builtin_amdgcn_sched_barrier(0);   // or all are read at once, and spill others
-            }
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      ask_values(nxt);
-      cur = nxt;
-      more = un != u;
-      u = un;
-      un = uf;
     }
     // the four waves' parts become one
     const bool whole = at.split == 1 && p.set == ATTN_ALL;

@@ -1920,7 +1920,7 @@ int q4nx_kv_append(const q4nx_kv_cache* cache, const q4nx_rope* rope, const q4nx
   }
   // One token a workgroup, its heads over several of them, until there are many; then eight, so that values can be
   // stored eight tokens at a time (32 + 8 heads of 128, fp32 in: 64 tokens 4.9 us, eight a workgroup 6.3; 256 tokens
-  // 6.5 and 7.0; 512 tokens 9.2 and 7.8; 4096 tokens 48 and 30).  About 2048 workgroups (4001 tokens: 31 us, 36
+  // 6.5 and 7.0; 512 tokens 9.2 and 7.6; 4096 tokens 48 and 30).  About 2048 workgroups (4001 tokens: 31 us, 36
   // with half of them, 35 with half as many more).
   a.tile = M >= 512 ? q4nx::kAppendTile : 1;
   const int tiles = q4nx::append_tiles(a), heads = a.q.heads + 2 * a.c.heads;

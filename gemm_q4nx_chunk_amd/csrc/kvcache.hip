@@ -8,8 +8,8 @@
 // bf16's step), keeps them in LDS, and turns every head with them.  A lane has two pieces of eight values, so
 // that both sides of a pair and what the cache holds together are one lane's.
 // Each value is read once and written once.  Bound by memory where there are many
-// rows (4001 of 32 + 8 heads of 128, bf16: 29 us, 107 MB at 3.6 TB/s; 4096 of fp32 30
-// us, 5.0 TB/s), by the launch and a few latencies where there are few (3.6 us).
+// rows (4096 of 32 + 8 heads of 128, fp32: 30 us, 5.1 TB/s; bf16 24 us, 4.2 TB/s), by
+// the launch and a few latencies where there are few (3.7 us).
 //
 // Eight tokens whose slots are a run (a prompt's; the tiles begin where the first
 // row's run of eight does) have their values exchanged through LDS and stored
@@ -30,21 +30,12 @@ namespace q4nx {
 namespace {
 
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
-typedef unsigned int u32x2u __attribute__((ext_vector_type(2), aligned(2)));
+typedef unsigned int u32x4u __attribute__((ext_vector_type(4), aligned(2)));
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   const f32x2 v = {a, b};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-}
-
-// Four neighbouring values of a row.
-__device__ __forceinline__ f32x4 load4(const HeadRows& h, int64_t at) {
-  if (h.bf16) {
-    const u32x2u w = *reinterpret_cast<const u32x2u*>(static_cast<const uint16_t*>(h.p) + at);
-    return f32x4{bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y)};
-  }
-  return *reinterpret_cast<const f32x4u*>(static_cast<const float*>(h.p) + at);
 }
 
 template <typename T>
@@ -64,9 +55,10 @@ __device__ __forceinline__ double mul_add(double a, double b, double c) { return
 
 }  // namespace
 
-// I8: the cache's type; T: what values are turned in; TM: tokens of a workgroup.
+// I8: the cache's type; T: what values are turned in; TM: tokens of a workgroup.  (All eight waves a SIMD for many rows
+// of bf16: 16384 rows 122 us for 133 with seven; 8 bits need their registers, 51 for 35 us at 4096 rows with fewer.)
 template <int D, bool I8, typename T, int TM>
-__global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
+__global__ __launch_bounds__(256, !I8 && TM == 8 ? 8 : 1) void k_kv_append(AppendArgs a) {
   constexpr int L = D / 16;            // lanes of a head: 4, 8 or 16
   constexpr int kItems = 256 / L;      // heads at a time
   typedef typename std::conditional<I8, uint8_t, uint16_t>::type Elem;
@@ -138,11 +130,21 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
     }
   };
   auto load16 = [&](const HeadRows& src, int64_t row, int e0, int e1, T (&y)[16]) {
+    if (src.bf16) {
+      const uint16_t* p = static_cast<const uint16_t*>(src.p) + row;
+      const u32x4u w[2] = {*reinterpret_cast<const u32x4u*>(p + 8 * e0), *reinterpret_cast<const u32x4u*>(p + 8 * e1)};
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const f32x4 x = load4(src, row + 8 * (n < 2 ? e0 : e1) + 4 * (n & 1));
+      for (int i = 0; i < 8; ++i) {
+        y[2 * i] = bf16lo(w[i >> 2][i & 3]);
+        y[2 * i + 1] = bf16hi(w[i >> 2][i & 3]);
+      }
+    } else {
+      const float* p = static_cast<const float*>(src.p) + row;
+      f32x4u x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[4 * n + i] = x[i];
+      for (int n = 0; n < 4; ++n) x[n] = *reinterpret_cast<const f32x4u*>(p + 8 * (n < 2 ? e0 : e1) + 4 * (n & 1));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[i] = x[i >> 2][i & 3];
     }
   };
 

@@ -116,7 +116,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
 
     // 32 keys: the 16 of each half may lie in pages of their own
     struct Keys {
-      int u, key0, have;     // keys from `have` on are no row's
+      int key0, have;        // keys from `have` on are no row's
       bool pre, ok0, ok1;
       size_t at0, at1;       // first elements of the halves' pages, and the tokens there
       int t0, t1;
@@ -136,7 +136,6 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
     };
     auto keys_of = [&](int u, const Pages& g) {
       Keys k;
-      k.u = u;
       k.pre = u < pre_units;
       k.key0 = (k.pre ? u : u - pre_units) * kAttnUnit + 32 * wave;
       k.have = k.pre ? x.pre : lim_last;
@@ -345,7 +344,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
 }
 
 // Many rows (128 a tile): prompts, and the shared prefix of a batch.  Each wave
-// has 32 rows, in matrix instructions of 32 x 32; the four share a tile of KT
+// has 32 rows, in matrix instructions of 32 x 32; the four share a tile of 64
 // keys that goes from memory straight to LDS, in the order in which it lies,
 // while the tile before it is worked on.  Lines of S^T are dealt as above, so
 // that a lane's scores of 16 keys are eight neighbouring tokens': P never
@@ -362,9 +361,10 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
 // a barrier at each change, were slower (319 us for 300, 64 wide 232 for 193): the
 // barriers and what is done between them cost more than the overlap gave, which two
 // workgroups a CU find by themselves.
-template <int D, bool I8, int KT>
+template <int D, bool I8>
 __device__ __forceinline__ void attn_many(const AttnArgs& a, const AttnParts& p, int block, int blocks, AttnPlan& plan, uint8_t* lds) {
-  constexpr int kRows = 128, NQ = D / 16, NB = KT / 32, NO = D / 32, kBlocks = KT / 16, kTiles = kAttnUnit / KT;
+  constexpr int kRows = 128, KT = 64, NQ = D / 16, NB = KT / 32, NO = D / 32, kBlocks = KT / 16, kTiles = kAttnUnit / KT;
+  static_assert(kBlocks == 4, "a block of K and of V for each wave");
   constexpr int kTile = KT * D;   // elements of K or V
   __shared__ __align__(16) int32_t s_valid[2][4];     // tokens that count of each 16
   __shared__ int32_t s_odd;
@@ -416,13 +416,13 @@ __device__ __forceinline__ void attn_many(const AttnArgs& a, const AttnParts& p,
       for (int n = 0; n < 16; ++n) acc[o][n] = 0.f;
     float m_run = kNegInf, l_run = 0.f;
 
-    // A tile's loading: wave w has 16-token block w of K and of V (two blocks: the upper two waves V).
+    // A tile's loading: wave w has 16-token block w of K and of V.
     // 8-bit tiles go through registers, 16 bytes of codes at a time, and become bf16 on the way.
     constexpr int kRaw = I8 ? KT * D / 16 / 256 : 1;
     u32x4 raw_k[kRaw], raw_v[kRaw];
     float raw_scale = 0.f;
     // the 16-token block of the wave's n-th piece, and of the lane's scale (8 bits)
-    auto block_of = [&](int n) { return I8 ? (wave * 64 + 256 * n) / D : kBlocks == 4 ? wave : wave & 1; };
+    auto block_of = [&](int n) { return I8 ? (wave * 64 + 256 * n) / D : wave; };
     const int scale_block = tid % KT / 16;
     auto page_of = [&](int t, int blk) {   // 0 where nothing is to be loaded
       const bool pre = t < own_begin;
@@ -461,19 +461,18 @@ __device__ __forceinline__ void attn_many(const AttnArgs& a, const AttnParts& p,
         const int blk = block_of(0), key = key0 + 16 * blk, page = __builtin_amdgcn_readfirstlane(g.piece[0]);
         const bool ok = (uint32_t)page < (uint32_t)a.c.n_pages;
         if (!ok) set_flag(a.flags, kFlagIndex);
-        if ((kBlocks == 4 || wave < 2) && lane == 0) s_valid[buf][blk] = ok ? min(max(have - key, 0), 16) : 0;
+        if (lane == 0) s_valid[buf][blk] = ok ? min(max(have - key, 0), 16) : 0;
         if (key < have) {
           const size_t at = kv_page(a.c, ok ? page : 0, head) + (size_t)(key & ((1 << ps) - 1)) * D + lane * 8;
           uint16_t* to = s_kv + buf * 2 * kTile + blk * 16 * D;
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv)
-            if (kBlocks == 4 || (wave >> 1) == kv) {
-              const uint16_t* from = static_cast<const uint16_t*>(kv ? a.c.v : a.c.k) + at;
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint16_t* from = static_cast<const uint16_t*>(kv ? a.c.v : a.c.k) + at;
 #pragma unroll
-              for (int n = 0; n < D / 32; ++n)
-                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + 512 * n),
-                                                 (lds_void*)(to + kv * kTile + 512 * n), 16, 0, 0);
-            }
+            for (int n = 0; n < D / 32; ++n)
+              __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + 512 * n),
+                                               (lds_void*)(to + kv * kTile + 512 * n), 16, 0, 0);
+          }
         }
       }
     };
@@ -671,7 +670,7 @@ constexpr int attn_occupancy(int dim, bool i8, int rows) {
 
 template <int D, bool I8, int ROWS>
 __device__ __forceinline__ void attn_rows(const AttnArgs& a, const AttnParts& p, int block, int blocks, AttnPlan& plan, uint8_t* lds) {
-  if constexpr (ROWS == 128) attn_many<D, I8, 64>(a, p, block, blocks, plan, lds);
+  if constexpr (ROWS == 128) attn_many<D, I8>(a, p, block, blocks, plan, lds);
   else attn_few<D, I8, ROWS / 16>(a, p, block, blocks, plan, lds);
 }
 

@@ -405,3 +405,40 @@ def test_without_lse_and_flags():
         c.out.zero_()
         q().attention(c.cache, c.batch, c.dq, c.H, c.M, c.scale, c.out, c.ws)
         assert torch.equal(c.out, want)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("q_len", [(1, 1, 1), (20, 3, 70)])
+def test_a_page_several_times(kind, q_len):
+    """Pages that sequences share, one twice in a sequence, and one that is the prefix's too."""
+    c = Case("shared-pages", q_len, [200, 170, 150], 40, 8, 2, 128, 32, kind)
+    c.table[1, :3] = c.table[0, :3]
+    c.table[2, 1] = c.table[2, 0]
+    c.table[2, 2] = c.shared[0]
+    c.upload().run().check()
+
+
+@pytest.mark.parametrize("q_len", [(1, 1), (90, 30)])
+def test_two_graphs_that_share_a_workspace(q_len):
+    """Captured apart, replayed in turn with eager calls of another shape on the same workspace between them."""
+    cs = [Case("one-workspace", q_len, L, pre, 8, 2, 128, 16).upload() for L, pre in (([700, 90], 0), ([300, 555], 130))]
+    other = Case("one-workspace-eager", [3], [400], 0, 8, 2, 128, 16).upload()
+    ws = torch.empty(max(c.ws.numel() for c in (*cs, other)), dtype=torch.uint8, device="cuda")
+    for c in (*cs, other):
+        c.ws = ws
+    graphs = []
+    for c in cs:
+        c.run().check()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run()
+        graphs.append(g)
+    want = [(c.out.clone(), c.lse.clone()) for c in cs]
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        cs[i].out.fill_(7)
+        cs[i].lse.fill_(7)
+        graphs[i].replay()
+        other.run()
+        assert torch.equal(cs[i].out, want[i][0]) and torch.equal(cs[i].lse, want[i][1])
+    other.check()

@@ -239,3 +239,12 @@ def test_captured_and_on_another_stream():
     call(1, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("q_bf16,v_bf16", [(True, True), (False, True), (True, False)])
+@pytest.mark.parametrize("run", [True, False])
+def test_rows_at_odd_strides(kind, q_bf16, v_bf16, run):
+    """Rows that lie at no more than their element's alignment, in tiles of eight."""
+    slots = (np.arange(777) + 3).astype(np.int32) if run else None
+    _run(kind, 777, 3, 2, 128, 64, 64, False, q_bf16, v_bf16, pad=3, slots=slots)

@@ -204,8 +204,9 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
         for (int b = 0; b < RB; ++b)
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
-            z[b][n] = st[b][n >> 2][n & 3] * a.scale;
-            if constexpr (I8) z[b][n] *= ks[n >> 2][n & 3];
+            z[b][n] = st[b][n >> 2][n & 3];
+            if constexpr (I8) z[b][n] *= ks[n >> 2][n & 3];   // first: q times codes may be 127 times what q k is
+            z[b][n] *= a.scale;
           }
         __builtin_amdgcn_sched_barrier(0);
         const Keys nxt = keys_of(un, pages);

@@ -442,3 +442,48 @@ def test_two_graphs_that_share_a_workspace(q_len):
         other.run()
         assert torch.equal(cs[i].out, want[i][0]) and torch.equal(cs[i].lse, want[i][1])
     other.check()
+
+
+def _scores(c):
+    """Of each row and head the scores that it sees, in float64, and their values (prefix first)."""
+    qv = synth.bf16_to_f32(c.q).astype(np.float64)
+    for s in range(c.n):
+        for kh in range(c.KH):
+            k, v = (np.concatenate([c._tokens(n, c.shared, c.prefix, kh), c._tokens(n, c.table[s], c.kv_len[s], kh)]) for n in "kv")
+            for m in range(c.q_start[s], c.q_start[s + 1]):
+                see = c.prefix + c.kv_len[s] - (c.q_start[s + 1] - m) + 1
+                for h in range(kh * (c.H // c.KH), (kh + 1) * (c.H // c.KH)):
+                    off = abs(c.scale) * (np.abs(k[:see]) @ np.abs(qv[m, h])).max()
+                    yield m, h, c.scale * (k[:see] @ qv[m, h]), v[:see], off
+
+
+def _far_scores(kind, scale, q_len, more, prefix, D):
+    """Scores so large that one key has all the weight: its value comes out, whichever kernel the rows take.
+
+    A score is off by at most (D + 8) 2^-24 sum |q_i k_i|; where the largest is further than twice that and 200 above
+    the next, every other weight is below 2^-288 and 0 in fp32.  The value is then off by a bf16 weight's and the output's
+    rounding, 2^-8 each; lse by its score's error and fp32's rounding."""
+    c = Case("far-scores", list(q_len), [n + more for n in q_len], prefix, 4, 2, D, 16, kind)
+    c.scale = scale
+    c.upload().run()
+    got, lse = synth.bf16_to_f32(host(c.out).view(np.uint16)).astype(np.float64), host(c.lse).astype(np.float64)
+    assert np.isfinite(got).all() and np.isfinite(lse).all()
+    alone = rows = 0
+    for m, h, s, v, off in _scores(c):
+        rows += 1
+        err = (D + 8) * 2.0 ** -24 * off
+        a, b = np.sort(s)[-1:-3:-1]
+        assert abs(lse[m, h] - a) <= err + np.log(len(s)) + 2.0 ** -22 * abs(a)
+        if a - b <= 2 * err + 200:
+            continue
+        alone += 1
+        want = v[np.argmax(s)]
+        assert (np.abs(got[m, h] - want) <= 2.1 * 2.0 ** -8 * np.abs(want)).all()
+    assert alone > rows / 2
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("scale", [2.0 ** 18, 2.0 ** 31, -(2.0 ** 34), 1e36])
+@pytest.mark.parametrize("q_len,prefix,D", [((1, 3), 0, 128), ((1, 3), 40, 64), ((4,), 0, 128)])
+def test_scores_far_from_zero_of_few_rows(kind, scale, q_len, prefix, D):
+    _far_scores(kind, scale, q_len, 500, prefix, D)

@@ -45,6 +45,12 @@ struct Raw<true> {
   __device__ __forceinline__ uint32_t keep(int, bool) { return 0u; }
 };
 
+// x - y of an x that has been rounded: a product is not taken into a fused multiply-add.
+__device__ __forceinline__ float rounded_less(float x, float y) {
+#pragma clang fp contract(off)
+  return x - y;
+}
+
 // Four dimensions of a row and head, from d.  A sum of 0 is that of a row that
 // sees nothing (any other has its largest term, 1, or a NaN).
 __device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, int D, int d, f32x4 o, float m, float l) {
@@ -245,7 +251,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
           const float base = m_run[b] == kNegInf ? 0.f : m_run[b];
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
-            float e = __builtin_amdgcn_exp2f(z[b][n] - base);
+            float e = __builtin_amdgcn_exp2f(rounded_less(z[b][n], base));
             l_run[b] += e;
             if constexpr (I8) e = z[b][n] == kNegInf ? 0.f : e * vs[n >> 2][n & 3];
             hi[b][n] = (__bf16)e;
@@ -579,13 +585,24 @@ __device__ __forceinline__ void attn_many(const AttnArgs& a, const AttnParts& p,
             for (int n = 0; n < 16; ++n) acc[o][n] *= alpha;
         }
         const float base = m_run == kNegInf ? 0.f : m_run;
+        // Below 2^24 the product that is not rounded before the subtraction is within 1/2 of the one that base was
+        // rounded from, which both sums have alike.  Beyond, numerators would leave fp32: scores are rounded first, as
+        // base was, so that the largest one's exponent is 0.
+        const bool far = __ballot(fabsf(base) > 16777216.f) != 0;
+        if (far) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int n = 0; n < 16; ++n) st[b][n] = rounded_less(st[b][n] * scale, base);
+        }
+        const float by = far ? 1.f : scale, less = far ? 0.f : base;
         float sum = 0.f;
         bf16x8 pf[NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
-            const float e2 = __builtin_amdgcn_exp2f(fmaf(st[b][n], scale, -base));
+            const float e2 = __builtin_amdgcn_exp2f(fmaf(st[b][n], by, -less));
             sum += e2;
             if constexpr (I8) st[b][n] = e2;
             else pf[b][n >> 3][n & 7] = (__bf16)e2;

@@ -487,3 +487,11 @@ def _far_scores(kind, scale, q_len, more, prefix, D):
 @pytest.mark.parametrize("q_len,prefix,D", [((1, 3), 0, 128), ((1, 3), 40, 64), ((4,), 0, 128)])
 def test_scores_far_from_zero_of_few_rows(kind, scale, q_len, prefix, D):
     _far_scores(kind, scale, q_len, 500, prefix, D)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("scale", [2.0 ** 18, 2.0 ** 22, 2.0 ** 28, 2.0 ** 31, -(2.0 ** 34), 2.0 ** 80, 1e36])
+@pytest.mark.parametrize("q_len,more,prefix,D", [((150,), 250, 0, 128), ((70, 40), 30, 90, 64), ((40,), 9, 0, 256),
+                                                 ((1,) * 40, 20, 300, 128), ((4,) * 9, 50, 200, 64)])
+def test_scores_far_from_zero_of_many_rows(kind, scale, q_len, more, prefix, D):
+    _far_scores(kind, scale, q_len, more, prefix, D)

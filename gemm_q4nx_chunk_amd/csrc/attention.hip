@@ -361,6 +361,12 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
 // by 2^8: numerators up to 2^8 lose nothing in bf16 or in the fp32 sums, and the
 // outputs are rescaled a few times a row instead of once a tile.
 //
+// Numerators enter the second product as one bf16 part, half a step of 2^-8 each: of the outputs' own size they are
+// off by 0.0023 in all, 0.0017 of it the outputs' rounding.  Two parts take a third product for every two (2048 tokens
+// over 8192: 425 us for 322, 64 wide 256 for 196, 256 wide 447 for 365).  With TWO they do: rows of few-row sequences
+// over a prefix, which have two over their own keys, so that a request's bits do not go by how many others are behind
+// the prefix (64 tokens behind 16384: 59 us for 52; 64 of 2000 behind 8192: the same).
+//
 // Bound by the matrix cores (44 % busy) and the softmax between them: 4096 tokens
 // over 16384 of 32 heads of 128 run at 966 TFLOP/s, where a large library product
 // reaches 1235; 2048 over 8192 at 820 (64 wide: 620, 256 wide: 610).  Eight waves of
@@ -368,7 +374,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
 // a barrier at each change, were slower (319 us for 300, 64 wide 232 for 193): the
 // barriers and what is done between them cost more than the overlap gave, which two
 // workgroups a CU find by themselves.
-template <int D, bool I8>
+template <int D, bool I8, bool TWO>
 __device__ __forceinline__ void attn_many(const AttnArgs& a, const AttnParts& p, int block, int blocks, AttnPlan& plan, uint8_t* lds) {
   constexpr int kRows = 128, KT = 64, NQ = D / 16, NB = KT / 32, NO = D / 32, kBlocks = KT / 16, kTiles = kAttnUnit / KT;
   static_assert(kBlocks == 4, "a block of K and of V for each wave");
@@ -597,7 +603,12 @@ __device__ __forceinline__ void attn_many(const AttnArgs& a, const AttnParts& p,
         }
         const float by = far ? 1.f : scale, less = far ? 0.f : base;
         float sum = 0.f;
-        bf16x8 pf[NB][2];
+        bf16x8 pf[NB][2], pl[TWO ? NB : 1][2];
+        auto enter = [&](int b, int n, float w) {
+          const __bf16 hi = (__bf16)w;
+          pf[b][n >> 3][n & 7] = hi;
+          if constexpr (TWO) pl[b][n >> 3][n & 7] = (__bf16)(w - (float)hi);
+        };
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
 #pragma unroll
@@ -605,7 +616,7 @@ __device__ __forceinline__ void attn_many(const AttnArgs& a, const AttnParts& p,
             const float e2 = __builtin_amdgcn_exp2f(fmaf(st[b][n], by, -less));
             sum += e2;
             if constexpr (I8) st[b][n] = e2;
-            else pf[b][n >> 3][n & 7] = (__bf16)e2;
+            else enter(b, n, e2);
           }
           __builtin_amdgcn_sched_barrier(0);   // or the values' reads come ahead of all this, and registers spill
         }
@@ -617,7 +628,7 @@ __device__ __forceinline__ void attn_many(const AttnArgs& a, const AttnParts& p,
 #pragma unroll
               for (int n = 0; n < 16; ++n) {
                 const float v = st[b][n] * s_vs[buf][32 * b + 16 * (n >> 3) + 8 * hh + (n & 7)];
-                pf[b][n >> 3][n & 7] = (__bf16)(some && st[b][n] == 0.f ? 0.f : v);
+                enter(b, n, some && st[b][n] == 0.f ? 0.f : v);
               }
           };
           if (masked) weigh(std::true_type{});
@@ -627,6 +638,8 @@ __device__ __forceinline__ void attn_many(const AttnArgs& a, const AttnParts& p,
         fed<D == 64 ? 2 : 4, NB * 2 * NO>(
             [&](int n) { return *reinterpret_cast<const bf16x8*>(sv + (n / NO) * 2 * 8 * D + (n % NO) * 256); },
             [&](int n, bf16x8 v) {
+              if constexpr (TWO)
+                acc[n % NO] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pl[n / NO / 2][n / NO % 2], acc[n % NO], 0, 0, 0);
               acc[n % NO] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pf[n / NO / 2][n / NO % 2], acc[n % NO], 0, 0, 0);
             });
         if (odd) {
@@ -686,9 +699,9 @@ constexpr int attn_occupancy(int dim, bool i8, int rows) {
   return dim == 256 ? 1 : dim == 64 ? (rows == 32 ? 2 : 3) : i8 && rows == 16 ? 3 : 2;
 }
 
-template <int D, bool I8, int ROWS>
+template <int D, bool I8, int ROWS, bool TWO = false>
 __device__ __forceinline__ void attn_rows(const AttnArgs& a, const AttnParts& p, int block, int blocks, AttnPlan& plan, uint8_t* lds) {
-  if constexpr (ROWS == 128) attn_many<D, I8>(a, p, block, blocks, plan, lds);
+  if constexpr (ROWS == 128) attn_many<D, I8, TWO>(a, p, block, blocks, plan, lds);
   else attn_few<D, I8, ROWS / 16>(a, p, block, blocks, plan, lds);
 }
 
@@ -712,7 +725,7 @@ __global__ __launch_bounds__(256, attn_occupancy(D, I8, OWN > PRE ? OWN : PRE)) 
   const bool is_pre = (int)blockIdx.x < pre_grid;
   const int block = is_pre ? blockIdx.x : blockIdx.x - pre_grid, blocks = is_pre ? pre_grid : gridDim.x - pre_grid;
   if constexpr (OWN == PRE) attn_rows<D, I8, OWN>(a, sets.p[is_pre], block, blocks, plan, lds);
-  else if (is_pre) attn_rows<D, I8, PRE>(a, sets.p[1], block, blocks, plan, lds);
+  else if (is_pre) attn_rows<D, I8, PRE, true>(a, sets.p[1], block, blocks, plan, lds);
   else attn_rows<D, I8, OWN>(a, sets.p[0], block, blocks, plan, lds);
 }
 

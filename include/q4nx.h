@@ -762,9 +762,10 @@ enum { Q4NX_ATTN_MAX_SEQ = 1024, Q4NX_ATTN_MAX_M = 65536 };
  * page_tokens, and rows of q_start that fall or leave 0..M, are clamped, and
  * bit 1 is set.
  * Scores, maxima, sums and outputs are fp32 and divided at the end, so that values
- * near fp32's largest overflow; the softmax's numerators enter the second product
- * in two bf16 parts (16 bits), and, where sequences have more than 32 rows of one
- * key head, in one; the sum of them is of the fp32 numerators.  Parts of a long row are
+ * near fp32's largest overflow; the softmax's numerators (times the value's scale,
+ * INT8) enter the second product in two bf16 parts (16 bits) where max_q rows of a
+ * sequence make up to 32 of one key head, over the prefix too, and in one (8 bits)
+ * where they make more; the sum of them is of the fp32 numerators.  Parts of a long row are
  * joined in a fixed order; how rows are cut into parts goes by the whole batch's
  * lengths, so that a row's last bits may differ between batches.
  * E_SHAPE: q_heads no multiple of kv_heads, or more than 16384 columns of q.

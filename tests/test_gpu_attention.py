@@ -495,3 +495,58 @@ def test_scores_far_from_zero_of_few_rows(kind, scale, q_len, prefix, D):
                                                  ((1,) * 40, 20, 300, 128), ((4,) * 9, 50, 200, 64)])
 def test_scores_far_from_zero_of_many_rows(kind, scale, q_len, more, prefix, D):
     _far_scores(kind, scale, q_len, more, prefix, D)
+
+
+def _even_keys(kind):
+    """Scores at which bf16 rounds the weight exp(s) up by most of half a step, and down: (up, down)."""
+    if kind == "bf16":
+        s = synth.bf16_to_f32(synth.bf16_bits(-np.arange(300, 700) / 1024.0)).astype(np.float64)
+    else:
+        s = -np.arange(300, 700) / 1024.0
+    e = np.exp(s)
+    r = synth.bf16_to_f32(synth.bf16_bits(e)).astype(np.float64) / e - 1
+    return s[np.argmax(r)], s[np.argmin(r)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("q_len,own,prefix", [((1,), 4001, 0), ((1, 1, 1), 700, 0), ((4, 2), 999, 0), ((8,), 300, 2000), ((1,) * 40, 20, 3000),
+                                              ((4,) * 9, 40, 2777), ((1,) * 5, 100, 1000)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_few_rows_keep_sixteen_bits_of_their_weights(kind, q_len, own, prefix, D):
+    """Sequences of up to 32 rows of a key head, with and without a prefix, however many they are together.
+
+    Half of the keys have a weight that bf16 rounds up, half one that it rounds down, and their values cancel: weights of
+    8 bits would be off by about 2^-8 sum p|v|, far past what is allowed here, where the second part's half step is
+    2^-8 of the first's, 2^-8 of the weight:  |out - ref| <= sum p|v| (2 d + 2^-16 + (n + 64) 2^-24) + 2^-8 |ref| + 2^-133
+    (d: above; 8 bits: one more rounding, of the weight times the value's scale).  One key of 16 has the largest score
+    and a value of 0, so that every part of a row counts from the same maximum."""
+    H, KH = 8, 2
+    up, down = _even_keys(kind)
+    c = Case("even", list(q_len), [n + own for n in q_len], prefix, H, KH, D, 16, kind)
+    c.scale = 1.0
+    c.q[:] = 0
+    c.q[..., 0] = 0x3F80
+    tok = np.arange(16)
+    first, odd = tok == 0, tok % 2 == 1
+    ratio = 8 * np.exp(up) / (7 * np.exp(down))
+    for name in "kv":
+        c.x[name][:] = 0
+    if kind == "bf16":
+        c.x["k"][..., 0] = synth.bf16_bits(np.where(first, 0.0, np.where(odd, up, down)))
+        c.x["v"][:] = synth.bf16_bits(np.where(first, 0.0, np.where(odd, 1.0, -ratio)))[:, None]
+    else:
+        c.x["k"][..., 0] = np.where(first, 0, -1)
+        c.x["ks"][:] = np.where(odd, -up, -down).astype(np.float32)
+        c.x["v"][:] = np.where(first, 0, np.where(odd, 80, -np.rint(80 * ratio))).astype(np.int8)[:, None]
+        c.x["vs"][:] = 1 / 64
+    c.upload().run()
+    out, lse, mag, off = c.reference()
+    got = synth.bf16_to_f32(host(c.out).view(np.uint16)).astype(np.float64)
+    n = prefix + own + max(q_len)
+    d = 2 * (D + 8) * 2.0 ** -24 * off + 2.0 ** -22 * (4 + n / 32)
+    tol = mag * (2 * d[..., None] + 2.0 ** -16 + (n + 65) * 2.0 ** -24) + 2.0 ** -8 * np.abs(out) + 2.0 ** -133
+    assert tol.max() < 2.0 ** -10 * mag.max()                   # what this is for: a fourth of one bf16 part's error
+    bad = ~(np.abs(got - out) <= tol)
+    assert not bad.any(), (bad.sum(), np.argwhere(bad)[:4], got[bad][:4], out[bad][:4], tol[bad][:4])
+    ltol = d + (n + 64) * 2.0 ** -24 + 2.0 ** -22 * (1 + np.abs(lse))
+    assert (np.abs(host(c.lse) - lse) <= ltol).all()

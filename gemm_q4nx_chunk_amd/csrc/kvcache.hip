@@ -120,13 +120,27 @@ __global__ __launch_bounds__(256, !I8 && TM == 8 ? 8 : 1) void k_kv_append(Appen
     }
     scale = nan ? __builtin_nanf("") : (float)(top / (T)127);
     const bool plain = scale > 0.f && scale <= __FLT_MAX__;
-    const T inv = plain ? (T)1 / (T)scale : 0;   // a quotient's last bits of 53 are all that this costs
+    // A product with the reciprocal is the quotient but for its last bits of 53: it rounds to the same code unless it
+    // lies next to a half step, where the quotient itself decides.
+    const T inv = plain ? (T)1 / (T)scale : 0;
+    bool border = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = 0u;
+    auto put = [&](int i, T quotient) {
+      const int code = plain ? (int)fmin(fmax(rint(quotient), (T)-127), (T)127) : 0;
+      w[i >> 2] |= (uint32_t)(code & 255) << (8 * (i & 3));
+    };
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int code = plain ? (int)fmin(fmax(rint(y[i] * inv), (T)-127), (T)127) : 0;
-      w[i >> 2] |= (uint32_t)(code & 255) << (8 * (i & 3));
+      const T quotient = y[i] * inv;
+      border |= fabs(quotient - rint(quotient)) > (T)0.499999999;
+      put(i, quotient);
+    }
+    if (border) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = 0u;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) put(i, y[i] / (T)scale);
     }
   };
   auto load16 = [&](const HeadRows& src, int64_t row, int e0, int e1, T (&y)[16]) {

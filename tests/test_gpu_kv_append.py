@@ -248,3 +248,33 @@ def test_rows_at_odd_strides(kind, q_bf16, v_bf16, run):
     """Rows that lie at no more than their element's alignment, in tiles of eight."""
     slots = (np.arange(777) + 3).astype(np.int32) if run else None
     _run(kind, 777, 3, 2, 128, 64, 64, False, q_bf16, v_bf16, pad=3, slots=slots)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("M,run", [(7, False), (700, False), (700, True)])
+def test_eight_bit_codes_at_half_steps(D, M, run):
+    """Codes are round(x / scale), half to even, at exact half steps and right beside them.
+
+    Each row's largest value is 127 s for a whole s, which makes the scale s; the others are odd multiples of s / 2, and
+    their neighbours in fp32 on either side: every code is known."""
+    g = synth.rng("kv-append-half", D, M, run)
+    s = g.integers(1, 1 << 14, M).astype(np.float64)
+    s[0] = 49
+    half = (2 * g.integers(0, 127, (M, 1, D)) + 1) * s[:, None, None] / 2 * g.choice([-1.0, 1.0], (M, 1, D))
+    x = half.astype(np.float32)
+    assert (x == half).all()
+    side = g.integers(0, 4, x.shape)
+    x = np.where(side == 0, np.nextafter(x, np.float32(0)), np.where(side == 1, np.nextafter(x, np.float32(np.inf) * np.sign(x)), x))
+    x[0, 0, 1] = 73.5                                           # over 49: one and a half
+    x[:, 0, 0] = 127 * s
+    pages = M // 16 + 2
+    slots = (np.arange(M) + 8 if run else g.permutation(pages * 16)[:M]).astype(np.int32)
+    cache = Cache("int8", 1, D, 16, pages)
+    q().kv_append(cache.c, _dev(x, None), _dev(x, None), dev_i32(slots), M)
+    want = np.rint(x.astype(np.float64) / s[:, None, None])
+    want[:, :, 1:] = np.clip(want[:, :, 1:], -127, 127)
+    k, v, ks, vs = cache.logical()
+    for codes, scale in ((k, ks), (v, vs)):
+        np.testing.assert_array_equal(scale[slots, 0], s)
+        bad = codes[slots] != want
+        assert not bad.any(), (bad.sum(), x[bad][:4], codes[slots][bad][:4], want[bad][:4])

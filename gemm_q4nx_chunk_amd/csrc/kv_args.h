@@ -156,7 +156,7 @@ struct LinearArgs {
   // prompts: rows of a segment (a multiple of 64), and, where a sequence may have several, in the workspace
   int32_t seg;
   int32_t* plan;       // [n_seq + 1] first segment of each sequence
-  double* seg_decay;   // [segment][v_heads] sum of its decays
+  double* seg_decay;   // [segment][v_heads] sum of its decays, -Inf if one of them has exp 0
   float* seg_state;    // [segment][v_heads][dk][dv], or null: a sequence is one segment
 };
 hipError_t launch_linear_rows(const LinearArgs& a, hipStream_t s);

@@ -350,7 +350,10 @@ __global__ __launch_bounds__(2 * DV, DV == 64 ? 1 : 2) void k_linear_chunks(Line
           const double o = __shfl_up(G, off);
           if (lane >= off) G += o;
         }
-        s_G[lane] = G;
+        // A decay whose exp is 0 cuts off an infinite or NaN state, which a sum of others never does: the segment's
+        // sum is -Inf then.
+        const bool cut = !OUT && __ballot(lane <= last && expf(d) == 0.f);
+        s_G[lane] = cut && lane == 63 ? -__builtin_huge_val() : G;
         s_since[lane] = a.scale * __builtin_amdgcn_exp2f((float)G);
         const float left = __builtin_amdgcn_exp2f((float)(__shfl(G, 63) - G));
         s_left[lane] = lane <= last ? left : 0.f;
@@ -579,8 +582,10 @@ __global__ __launch_bounds__(256) void k_linear_carry(LinearArgs a) {
     for (int j = 0; j < kAhead; ++j) {
       if (s0 + j > last) break;
       const float f = __builtin_amdgcn_exp2f((float)d[j]);
+      const bool cut = d[j] == -__builtin_huge_val();
 #pragma unroll
-      for (int n = 0; n < 4; ++n) S[n] = (f == 0.f ? 0.f : f * S[n]) + u[j][n];
+      for (int n = 0; n < 4; ++n)   // 0 for what has decayed so far; an infinity or NaN stays unless it is cut off
+        S[n] = (cut ? 0.f : f == 0.f && !(fabsf(S[n]) <= __FLT_MAX__) ? S[n] : f * S[n]) + u[j][n];
       *reinterpret_cast<f32x4*>(a.seg_state + ((size_t)(first + s0 + j) * a.v_heads + h) * size + at) = S;
     }
   }

@@ -291,3 +291,34 @@ def test_scales():
             c = Case("scale", [n], 1, 1, 64, 64)
             c.scale = scale
             c.upload().run().check()
+
+
+@pytest.mark.parametrize("lens,H", [([700], 2), ([260, 5, 400], 4), ([3000], 32)])
+@pytest.mark.parametrize("rate", [-0.01, -2.0, -100.0])
+@pytest.mark.parametrize("what", ["state", "k", "v"])
+def test_infinities_and_nans_that_no_decay_cuts_off(lens, H, rate, what):
+    """They stay in the state however far it has decayed, as no single decay's exp is 0, over any number of segments;
+    one of -Inf cuts them off."""
+    f = lambda x: synth.bf16_to_f32(x).astype(np.float64)  # noqa: E731
+    for mark, cut in ((0x7FC0, False), (0x7F80, False), (0xFF80, False), (0x7FC0, True), (0xFF80, True)):
+        c = Case("kept", lens, H, H, 64, 64)
+        c.decay[:] = rate
+        slot, begin, end = c.slots[-1], c.q_start[-2], c.q_start[-1]
+        if what == "state":
+            c.state[slot, 1, 3, 5] = f(np.array([mark], np.uint16))[0]
+        else:
+            getattr(c, what)[begin + 9, 1, 3] = mark
+        if cut:
+            c.decay[begin + 150, 1] = -np.inf
+        c.upload().run()
+        r = slice(begin, end)
+        with np.errstate(invalid="ignore"):
+            out, S, _, _ = oracle.linear_attn_ref(f(c.q[r, 1]), f(c.k[r, 1]), f(c.v[r, 1]), c.decay[r, 1], c.scale, c.state[slot, 1])
+        assert np.isfinite(out[-1]).all() == cut and not np.isfinite(out[9]).all()
+        got, state = host(c.out), host(c.dstate_out)
+        np.testing.assert_array_equal(np.isfinite(got[r, 1]), np.isfinite(out))
+        np.testing.assert_array_equal(np.isfinite(state[slot, 1]), np.isfinite(S))
+        np.testing.assert_array_equal(np.isnan(state[slot, 1]), np.isnan(S))
+        got[r, 1] = state[slot, 1] = 0
+        assert np.isfinite(got).all() and np.isfinite(state).all()
+        assert host(c.flags)[0] == 0

@@ -245,8 +245,11 @@ __global__ __launch_bounds__(2 * DV, DV == 64 ? 1 : 2) void k_linear_chunks(Line
   {
     int32_t* first = reinterpret_cast<int32_t*>(lds);
     linear_plan(a, first, first + kAttnMaxSeq + 1);
-    if (!OUT && blockIdx.x == 0)
-      for (int e = tid; e <= a.n_seq; e += kThreads) a.plan[e] = first[e];
+    if (blockIdx.x == 0)
+      for (int e = tid; e <= a.n_seq; e += kThreads) {
+        if (!OUT) a.plan[e] = first[e];
+        else if (a.q_start[e] != first[kAttnMaxSeq + 1 + e]) set_flag(a.flags, kFlagRows);   // of sequences without rows too
+      }
     if (item >= first[a.n_seq]) return;
     int count = 0;
     for (int b = 0; b < a.n_seq; b += 64) count += __popcll(__ballot(b + lane < a.n_seq && first[b + lane] <= item));

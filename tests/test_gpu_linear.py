@@ -322,3 +322,17 @@ def test_infinities_and_nans_that_no_decay_cuts_off(lens, H, rate, what):
         got[r, 1] = state[slot, 1] = 0
         assert np.isfinite(got).all() and np.isfinite(state).all()
         assert host(c.flags)[0] == 0
+
+
+@pytest.mark.parametrize("max_q", [4, 100, 300])
+@pytest.mark.parametrize("start,clamped", [([0, 100, 50], [0, 100, 100]), ([0, 100, 107], [0, 100, 100]), ([-5, 0, 100], [0, 0, 100]),
+                                           ([10, 5], [10, 10]), ([0, 3, 1, 99], [0, 3, 3, 99]), ([0, 40, -1, -1, 60], [0, 40, 40, 40, 60]),
+                                           ([0] * 70 + [100, 99], [0] * 70 + [100, 100])])
+def test_row_starts_that_do_not_fit_are_told(max_q, start, clamped):
+    """Falling starts and such as leave the rows, of sequences without rows too, whichever kernels run."""
+    lens = np.diff(clamped).tolist()
+    c = Case("told", lens, 1, 2, 64, 64, max_q=max_q, first_row=clamped[0], extra_rows=100 - clamped[-1])
+    c.upload().run().check()
+    c.upload()
+    c.dstart.copy_(torch.tensor(start, dtype=torch.int32))
+    c.run().check(flags=4)

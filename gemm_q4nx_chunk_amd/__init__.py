@@ -649,12 +649,25 @@ def kv_append(cache: KvCache, k, v, slots, M: int, rope: Rope | None = None, q=N
                                _ptr(flags), _stream(stream)))
 
 
+def _table_step(t) -> int:
+    """Elements between a table's rows.  They count as its columns too, so that each row must have as many."""
+    shape, st = t.shape, t.stride()
+    if len(st) != 2 or (shape[1] > 1 and st[1] != 1):
+        raise Q4nxError(E_SHAPE, "pages: a table of contiguous rows is taken")
+    if shape[0] < 2:
+        return shape[1]
+    if st[0] < shape[1] or (t.storage_offset() + shape[0] * st[0]) * t.element_size() > t.untyped_storage().nbytes():
+        raise Q4nxError(E_SHAPE, f"pages: rows {st[0]} apart overlap, or the last one's end is not in the tensor's memory")
+    return st[0]
+
+
 def attn_batch(q_start, kv_len, pages, max_q: int, prefix_len: int = 0, prefix_pages=None, n_seq: int | None = None,
                pages_ld: int | None = None) -> AttnBatch:
-    """The sequences of an attention call: q_start int32 [n_seq + 1], kv_len int32 [n_seq], pages int32 [n_seq][pages_ld],
-    at most max_q rows a sequence, behind a prefix of prefix_len tokens in prefix_pages."""
+    """The sequences of an attention call: q_start int32 [n_seq + 1], kv_len int32 [n_seq], pages int32 [n_seq][pages_ld]
+    (the first columns of a wider table too: pages_ld is its rows' step), at most max_q rows a sequence, behind a prefix of
+    prefix_len tokens in prefix_pages."""
     b = AttnBatch(kv_len.numel() if n_seq is None else n_seq, max_q, _ptr(q_start), _ptr(kv_len), _ptr(pages),
-                  pages.shape[1] if pages_ld is None else pages_ld, prefix_len, _ptr(prefix_pages))
+                  _table_step(pages) if pages_ld is None else pages_ld, prefix_len, _ptr(prefix_pages))
     b._owners = (q_start, kv_len, pages, prefix_pages)
     return b
 

@@ -279,6 +279,22 @@ def test_linear_sequences_may_change_between_calls(q):
     assert (s.k_heads, s.v_heads, s.n_slots) == (0, 0, 0)
 
 
+def test_page_tables_that_are_strided_binding(q):
+    """A table's rows are as far apart as its strides say; what cannot be said so is refused."""
+    torch = pytest.importorskip("torch")
+    wide, lens = torch.arange(60, dtype=torch.int32).view(4, 15), torch.ones(4, dtype=torch.int32)
+    start = torch.arange(5, dtype=torch.int32)
+    b = q.attn_batch(start, lens, wide[:, :6], 1)
+    assert (b.pages, b.pages_ld, b.n_seq) == (wide.data_ptr(), 15, 4)
+    assert q.attn_batch(start, lens, wide, 1).pages_ld == 15
+    assert q.attn_batch(start, lens[::2][:2].contiguous(), wide[::2, :6], 1).pages_ld == 30
+    assert q.attn_batch(start[:4], lens[:3], wide[:3, 4:9], 1).pages_ld == 15       # the fourth row is there behind them
+    assert q.attn_batch(start[:2], lens[:1], wide[:1, 4:9], 1).pages_ld == 5        # one row: its own columns
+    assert q.attn_batch(start, lens, wide[:, :6], 1, pages_ld=15).pages_ld == 15
+    for bad in (wide.t(), wide[:, ::2], wide[:1].expand(4, 15), wide[:, 4:9], wide[0], wide.view(2, 2, 15)):
+        _expect(q, q.E_SHAPE, q.attn_batch, start, lens, bad, 1)
+
+
 # ----------------------------------------------------------------------------
 # the checks under the host sanitisers
 # ----------------------------------------------------------------------------

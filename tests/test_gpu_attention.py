@@ -550,3 +550,17 @@ def test_few_rows_keep_sixteen_bits_of_their_weights(kind, q_len, own, prefix, D
     assert not bad.any(), (bad.sum(), np.argwhere(bad)[:4], got[bad][:4], out[bad][:4], tol[bad][:4])
     ltol = d + (n + 64) * 2.0 ** -24 + 2.0 ** -22 * (1 + np.abs(lse))
     assert (np.abs(host(c.lse) - lse) <= ltol).all()
+
+
+@pytest.mark.parametrize("q_len", [(1, 1, 1), (3, 2, 90)])
+def test_a_table_within_a_wider_one(q_len):
+    """The first columns of a table whose others are pages of the cache as well."""
+    for prefix in (0, 100):
+        c = Case("wide-table", q_len, [200, 170, 150], prefix, 8, 2, 128, 16)
+        c.upload()
+        wide = torch.randint(0, c.pages, (3, c.cols + 9), dtype=torch.int32, device="cuda")
+        wide[:, : c.cols] = c.dtable
+        c.batch = q().attn_batch(c.dstart, c.dlen, wide[:, : c.cols], c.max_q, prefix_len=prefix,
+                                 prefix_pages=dev_i32(c.shared) if prefix else None)
+        assert c.batch.pages_ld == c.cols + 9
+        c.run().check()

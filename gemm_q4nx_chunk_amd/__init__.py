@@ -573,13 +573,23 @@ KV_BF16, KV_INT8 = 0, 1
 _F32, _BF16 = 0, 1
 
 
+def _whole(t, what: str) -> int:
+    """The address of an array that a call takes in one piece."""
+    if t is None or isinstance(t, int):
+        return t or 0
+    if not t.is_contiguous():
+        raise Q4nxError(E_SHAPE, f"{what} must be contiguous")
+    return t.data_ptr()
+
+
 def kv_cache(kv_heads: int, head_dim: int, page_tokens: int, n_pages: int, k, v, k_scale=None, v_scale=None,
              k_bytes: int | None = None, v_bytes: int | None = None, k_scale_bytes: int | None = None,
              v_scale_bytes: int | None = None) -> KvCache:
     """A paged cache over device memory (layout: include/q4nx.h): k and v of n_pages * kv_heads * page_tokens *
     head_dim bf16 values, or int8 codes beside k_scale and v_scale, fp32 [n_pages][kv_heads][page_tokens]."""
     c = KvCache(kv_heads, head_dim, page_tokens, n_pages, KV_BF16 if k_scale is None and v_scale is None else KV_INT8,
-                _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _nbytes(k) if k_bytes is None else k_bytes,
+                _whole(k, "k"), _whole(v, "v"), _whole(k_scale, "k_scale"), _whole(v_scale, "v_scale"),
+                _nbytes(k) if k_bytes is None else k_bytes,
                 _nbytes(v) if v_bytes is None else v_bytes, _nbytes(k_scale) if k_scale_bytes is None else k_scale_bytes,
                 _nbytes(v_scale) if v_scale_bytes is None else v_scale_bytes)
     c._owners = (k, v, k_scale, v_scale)
@@ -589,7 +599,7 @@ def kv_cache(kv_heads: int, head_dim: int, page_tokens: int, n_pages: int, k, v,
 def rope(inv_freq, pos, dim: int, interleaved: bool = False) -> Rope:
     """Rotation of the first dim dimensions by pos[m] * inv_freq[i] (fp32 [dim/2], int32 [M]), in pairs (i, i + dim/2) or
     (2i, 2i + 1)."""
-    r = Rope(dim, 1 if interleaved else 0, _ptr(inv_freq), _ptr(pos))
+    r = Rope(dim, 1 if interleaved else 0, _whole(inv_freq, "inv_freq"), _whole(pos, "pos"))
     r._owners = (inv_freq, pos)
     return r
 
@@ -598,6 +608,8 @@ def _row_step(t, columns: int, width: int, what: str) -> int:
     """Elements between a tensor's rows of heads `width` wide; its other dimensions lie as they come."""
     st = t.stride()
     if len(st) < 2:
+        if st and st[0] != 1 and t.shape[0] > 1:
+            raise Q4nxError(E_SHAPE, f"{what}: the columns of a row must be contiguous")
         return columns
     if len(st) > 3 or st[-1] != 1 or (len(st) == 3 and st[1] != width and t.shape[1] > 1):
         raise Q4nxError(E_SHAPE, f"{what}: the columns of a row must be contiguous")
@@ -645,8 +657,8 @@ def kv_append(cache: KvCache, k, v, slots, M: int, rope: Rope | None = None, q=N
                 raise Q4nxError(E_ARG, "kv_append: q without q_heads")
             q = _heads(q, q_heads, D)
         q = ref(q)
-    _check(_lib.q4nx_kv_append(ref(cache), None if rope is None else ref(rope), q, _ptr(q_out), ref(k), ref(v), _ptr(slots), M,
-                               _ptr(flags), _stream(stream)))
+    _check(_lib.q4nx_kv_append(ref(cache), None if rope is None else ref(rope), q, _whole(q_out, "q_out"), ref(k), ref(v),
+                               _whole(slots, "slots"), M, _ptr(flags), _stream(stream)))
 
 
 def _table_step(t) -> int:
@@ -666,8 +678,9 @@ def attn_batch(q_start, kv_len, pages, max_q: int, prefix_len: int = 0, prefix_p
     """The sequences of an attention call: q_start int32 [n_seq + 1], kv_len int32 [n_seq], pages int32 [n_seq][pages_ld]
     (the first columns of a wider table too: pages_ld is its rows' step), at most max_q rows a sequence, behind a prefix of
     prefix_len tokens in prefix_pages."""
-    b = AttnBatch(kv_len.numel() if n_seq is None else n_seq, max_q, _ptr(q_start), _ptr(kv_len), _ptr(pages),
-                  _table_step(pages) if pages_ld is None else pages_ld, prefix_len, _ptr(prefix_pages))
+    b = AttnBatch(kv_len.numel() if n_seq is None else n_seq, max_q, _whole(q_start, "q_start"), _whole(kv_len, "kv_len"),
+                  _ptr(pages), _table_step(pages) if pages_ld is None else pages_ld, prefix_len,
+                  _whole(prefix_pages, "prefix_pages"))
     b._owners = (q_start, kv_len, pages, prefix_pages)
     return b
 
@@ -681,15 +694,16 @@ def attention(cache: KvCache, batch: AttnBatch, q, q_heads: int, M: int, scale: 
               stream=None, ws_bytes: int | None = None) -> None:
     """out[M, q_heads, head_dim] (bf16) = softmax(scale q k^T) v over the prefix and each sequence's cached tokens, causal;
     lse[M, q_heads] the logarithm of the sums."""
-    _check(_lib.q4nx_attention(ctypes.byref(cache), ctypes.byref(batch), _ptr(q), q_heads, M, scale, _ptr(out), _ptr(lse),
-                               _ptr(ws), _nbytes(ws) if ws_bytes is None else ws_bytes, _ptr(flags), _stream(stream)))
+    _check(_lib.q4nx_attention(ctypes.byref(cache), ctypes.byref(batch), _whole(q, "q"), q_heads, M, scale, _whole(out, "out"),
+                               _whole(lse, "lse"), _ptr(ws), _nbytes(ws) if ws_bytes is None else ws_bytes, _ptr(flags),
+                               _stream(stream)))
 
 
 def linear_attn_seqs(q_start, slots, max_q: int, fresh=None, n_seq: int | None = None) -> Linear:
     """The sequences of a linear attention call: q_start int32 [n_seq + 1], slots int32 [n_seq] (each one's state, -1:
     none), fresh int32 [n_seq] (not 0: begin with zeros) or None."""
-    s = Linear(n_seq=slots.numel() if n_seq is None else n_seq, max_q=max_q, q_start=_ptr(q_start), slots=_ptr(slots),
-               fresh=_ptr(fresh))
+    s = Linear(n_seq=slots.numel() if n_seq is None else n_seq, max_q=max_q, q_start=_whole(q_start, "q_start"),
+               slots=_whole(slots, "slots"), fresh=_whole(fresh, "fresh"))
     s._owners = (q_start, slots, fresh)
     return s
 
@@ -720,12 +734,14 @@ def linear_attn(seqs: Linear, q, k, v, decay, k_heads: int, v_heads: int, dk: in
     if v_ld is None:
         v_ld = v_heads * dv if type(v) is int else _row_step(v, v_heads * dv, dv, "linear_attn")
     if decay_ld is None:
-        decay_ld = v_heads if type(decay) is int else 0 if decay.dim() == 1 else _row_step(decay, v_heads, 1, "linear_attn")
+        decay_ld = v_heads if type(decay) is int else _row_step(decay, v_heads, 1, "linear_attn")
+        if type(decay) is not int and decay.dim() == 1:
+            decay_ld = 0
     if n_slots is None:
         n_slots = state.numel() // (v_heads * dk * dv)
     _check(_lib.q4nx_linear_attn(ctypes.byref(_linear(seqs, k_heads, v_heads, dk, dv, n_slots)), _ptr(q), q_ld, _ptr(k), k_ld,
-                                 _ptr(v), v_ld, _ptr(decay), decay_ld, M, scale, _ptr(state),
-                                 _ptr(state if state_out is None else state_out), _ptr(out), _ptr(ws),
+                                 _ptr(v), v_ld, _ptr(decay), decay_ld, M, scale, _whole(state, "state"),
+                                 _whole(state if state_out is None else state_out, "state_out"), _whole(out, "out"), _ptr(ws),
                                  _nbytes(ws) if ws_bytes is None else ws_bytes, _ptr(flags), _stream(stream)))
 
 

@@ -295,6 +295,33 @@ def test_page_tables_that_are_strided_binding(q):
         _expect(q, q.E_SHAPE, q.attn_batch, start, lens, bad, 1)
 
 
+def test_arrays_in_one_piece_binding(q):
+    """A strided tensor is refused where the call takes no stride: it would be read or written at other places."""
+    torch = pytest.importorskip("torch")
+    i32, f32, bf = torch.int32, torch.float32, torch.bfloat16
+    z = lambda *s, t=f32: torch.zeros(*s, dtype=t)  # noqa: E731
+    shape = (PAGES, KH, PAGE * D)
+    for over in (dict(k=z(PAGES, 2, KH, PAGE * D, t=bf)[:, 0]), dict(v=z(*shape[:2], 2 * PAGE * D, t=bf)[..., ::2])):
+        _expect(q, q.E_SHAPE, _cache, q, **over)
+    for name in ("k_scale", "v_scale"):
+        _expect(q, q.E_SHAPE, _cache, q, True, **{name: z(PAGES, PAGE, KH).transpose(1, 2)})
+    _expect(q, q.E_SHAPE, q.rope, z(2 * D)[::2], 0x8100000, D)
+    _expect(q, q.E_SHAPE, q.rope, 0x8000000, z(6, t=i32)[::2], D)
+    _expect(q, q.E_SHAPE, _append, q, slots=z(3, 2, t=i32)[:, 0])
+    _expect(q, q.E_SHAPE, _append, q, q_out=z(3, 8, D, t=bf)[:, :4])
+    for name, bad in (("k", z(2 * KH * D)[::2]), ("v", z(2 * KH * D, t=bf)[::2]), ("q", z(8 * D)[::2])):
+        _expect(q, q.E_SHAPE, _append, q, M=1, q_heads=4, **{name: bad})
+    for over in (dict(q_start=z(8, t=i32)[::2]), dict(kv_len=z(6, t=i32)[::2]), dict(prefix_pages=z(2, 2, t=i32)[:, 1])):
+        _expect(q, q.E_SHAPE, _batch, q, **over)
+    for over in (dict(q=z(3, 8, D, t=bf)[:, :4]), dict(out=z(4, 3, D, t=bf).transpose(0, 1)), dict(lse=z(4, 3).t())):
+        _expect(q, q.E_SHAPE, _attend, q, **over)
+    for over in (dict(q_start=z(6, t=i32)[::2]), dict(slots=z(2, 2, t=i32)[:, 0]), dict(fresh=z(4, t=i32)[::2])):
+        _expect(q, q.E_SHAPE, _seqs, q, **over)
+    for over in (dict(state=z(3, 4, 128, 64).transpose(2, 3)), dict(state_out=z(3, 8, 64, 128)[:, :4]), dict(out=z(3, 4, 256)[..., :128]),
+                 dict(decay=z(4, 2)[:, 0]), dict(q=z(256, t=bf)[::2])):
+        _expect(q, q.E_SHAPE, _linear, q, **over)
+
+
 # ----------------------------------------------------------------------------
 # the checks under the host sanitisers
 # ----------------------------------------------------------------------------

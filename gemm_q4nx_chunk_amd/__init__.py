@@ -573,6 +573,24 @@ KV_BF16, KV_INT8 = 0, 1
 _F32, _BF16 = 0, 1
 
 
+_INT32S = {"int32", "uint32"}   # and, once met, their dtypes
+
+
+def _int32(t, what: str) -> None:
+    """Refuses indexes of another type: a wider one's halves would be taken for indexes of their own."""
+    if t.dtype not in _INT32S:
+        if str(t.dtype).rpartition(".")[2] not in _INT32S:
+            raise Q4nxError(E_ARG, f"{what} of type {t.dtype}: int32 is taken")
+        _INT32S.add(t.dtype)
+
+
+def _indexes(t, what: str) -> int:
+    """The address of an array of indexes that a call takes in one piece."""
+    if t is not None and not isinstance(t, int):
+        _int32(t, what)
+    return _whole(t, what)
+
+
 def _whole(t, what: str) -> int:
     """The address of an array that a call takes in one piece."""
     if t is None or isinstance(t, int):
@@ -599,7 +617,7 @@ def kv_cache(kv_heads: int, head_dim: int, page_tokens: int, n_pages: int, k, v,
 def rope(inv_freq, pos, dim: int, interleaved: bool = False) -> Rope:
     """Rotation of the first dim dimensions by pos[m] * inv_freq[i] (fp32 [dim/2], int32 [M]), in pairs (i, i + dim/2) or
     (2i, 2i + 1)."""
-    r = Rope(dim, 1 if interleaved else 0, _whole(inv_freq, "inv_freq"), _whole(pos, "pos"))
+    r = Rope(dim, 1 if interleaved else 0, _whole(inv_freq, "inv_freq"), _indexes(pos, "pos"))
     r._owners = (inv_freq, pos)
     return r
 
@@ -658,11 +676,12 @@ def kv_append(cache: KvCache, k, v, slots, M: int, rope: Rope | None = None, q=N
             q = _heads(q, q_heads, D)
         q = ref(q)
     _check(_lib.q4nx_kv_append(ref(cache), None if rope is None else ref(rope), q, _whole(q_out, "q_out"), ref(k), ref(v),
-                               _whole(slots, "slots"), M, _ptr(flags), _stream(stream)))
+                               _indexes(slots, "slots"), M, _ptr(flags), _stream(stream)))
 
 
 def _table_step(t) -> int:
     """Elements between a table's rows.  They count as its columns too, so that each row must have as many."""
+    _int32(t, "pages")
     shape, st = t.shape, t.stride()
     if len(st) != 2 or (shape[1] > 1 and st[1] != 1):
         raise Q4nxError(E_SHAPE, "pages: a table of contiguous rows is taken")
@@ -678,9 +697,9 @@ def attn_batch(q_start, kv_len, pages, max_q: int, prefix_len: int = 0, prefix_p
     """The sequences of an attention call: q_start int32 [n_seq + 1], kv_len int32 [n_seq], pages int32 [n_seq][pages_ld]
     (the first columns of a wider table too: pages_ld is its rows' step), at most max_q rows a sequence, behind a prefix of
     prefix_len tokens in prefix_pages."""
-    b = AttnBatch(kv_len.numel() if n_seq is None else n_seq, max_q, _whole(q_start, "q_start"), _whole(kv_len, "kv_len"),
-                  _ptr(pages), _table_step(pages) if pages_ld is None else pages_ld, prefix_len,
-                  _whole(prefix_pages, "prefix_pages"))
+    b = AttnBatch(kv_len.numel() if n_seq is None else n_seq, max_q, _indexes(q_start, "q_start"),
+                  _indexes(kv_len, "kv_len"), _ptr(pages), _table_step(pages) if pages_ld is None else pages_ld, prefix_len,
+                  _indexes(prefix_pages, "prefix_pages"))
     b._owners = (q_start, kv_len, pages, prefix_pages)
     return b
 
@@ -702,8 +721,8 @@ def attention(cache: KvCache, batch: AttnBatch, q, q_heads: int, M: int, scale: 
 def linear_attn_seqs(q_start, slots, max_q: int, fresh=None, n_seq: int | None = None) -> Linear:
     """The sequences of a linear attention call: q_start int32 [n_seq + 1], slots int32 [n_seq] (each one's state, -1:
     none), fresh int32 [n_seq] (not 0: begin with zeros) or None."""
-    s = Linear(n_seq=slots.numel() if n_seq is None else n_seq, max_q=max_q, q_start=_whole(q_start, "q_start"),
-               slots=_whole(slots, "slots"), fresh=_whole(fresh, "fresh"))
+    s = Linear(n_seq=slots.numel() if n_seq is None else n_seq, max_q=max_q, q_start=_indexes(q_start, "q_start"),
+               slots=_indexes(slots, "slots"), fresh=_indexes(fresh, "fresh"))
     s._owners = (q_start, slots, fresh)
     return s
 

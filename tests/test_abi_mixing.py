@@ -322,6 +322,22 @@ def test_arrays_in_one_piece_binding(q):
         _expect(q, q.E_SHAPE, _linear, q, **over)
 
 
+def test_indexes_of_another_type_binding(q):
+    """Slots, positions, starts, lengths and pages of a wider type are refused: its halves would be taken for indexes."""
+    torch = pytest.importorskip("torch")
+    for t in (torch.int64, torch.int16, torch.float32, torch.bool):
+        z = lambda *s: torch.zeros(*s, dtype=t)  # noqa: B023, E731
+        _expect(q, q.E_ARG, _append, q, slots=z(3))
+        _expect(q, q.E_ARG, q.rope, 0x8000000, z(3), D)
+        for over in (dict(q_start=z(4)), dict(kv_len=z(3)), dict(prefix_pages=z(2)), dict(pages=z(3, 2), pages_ld=None)):
+            _expect(q, q.E_ARG, _batch, q, **over)
+        for over in (dict(q_start=z(3)), dict(slots=z(2)), dict(fresh=z(2))):
+            _expect(q, q.E_ARG, _seqs, q, **over)
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    b = q.attn_batch(z(4), z(3), z(3, 2), 1, prefix_len=5, prefix_pages=z(1))
+    assert (b.n_seq, b.pages_ld) == (3, 2) and q.linear_attn_seqs(z(4), z(3), 1, fresh=z(3)).n_seq == 3
+
+
 # ----------------------------------------------------------------------------
 # the checks under the host sanitisers
 # ----------------------------------------------------------------------------

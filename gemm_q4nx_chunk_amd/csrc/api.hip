@@ -1834,16 +1834,20 @@ LinearShape linear_shape(const q4nx_linear* L, int M) {
   // 1, 2 chunks 21, 27 us).
   const int64_t chunks = ((int64_t)M + 63) / 64 * L->v_heads;
   sh.seg = 64 * (int)(chunks <= 384 ? 1 : std::max<int64_t>(2, (chunks + 511) / 512));
-  sh.carried = L->max_q > std::max(sh.seg, 192) && L->n_seq * (int64_t)L->v_heads < 256;
+  const bool few = L->max_q > 192 && L->n_seq * (int64_t)L->v_heads < 256;
+  sh.carried = few && L->max_q > sh.seg;
   if (!sh.carried) sh.seg = 1 << 30;
   sh.items = sh.carried ? M / sh.seg + L->n_seq : L->n_seq;
-  if (!sh.carried) return sh;
+  if (!few) return sh;
+  // Room for the most segments that M rows or fewer are cut into, so that a workspace for many rows holds fewer: whole
+  // segments are M / 64 at most, and 512 / v_heads, as seg is 64 * chunks / 512 at least (or, of up to 384, one).
+  const size_t items = std::min<int64_t>(M / 64, 512 / L->v_heads) + L->n_seq;
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   size_t o = up(((size_t)L->n_seq + 1) * 4);
   sh.decay = o;
-  o = up(o + (size_t)sh.items * L->v_heads * 8);
+  o = up(o + items * L->v_heads * 8);
   sh.state = o;
-  sh.total = up(o + (size_t)sh.items * L->v_heads * L->dk * L->dv * 4);
+  sh.total = up(o + items * L->v_heads * L->dk * L->dv * 4);
   return sh;
 }
 

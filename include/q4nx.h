@@ -808,8 +808,8 @@ typedef struct q4nx_linear {
  *              checkpoint to go back to).  Slots of no sequence, or of one without rows, are left as they were.
  *   out    DEVICE fp32 [M][v_heads][dv], 16-byte aligned; rows of no sequence are left as they were
  *   M      1..Q4NX_ATTN_MAX_M rows
- *   ws     DEVICE workspace of q4nx_linear_attn_ws(L, M) bytes (a smaller M may need more), 256-byte
- *          aligned.  Nothing in it needs initialising; calls that share it must not overlap.
+ *   ws     DEVICE workspace of q4nx_linear_attn_ws(L, M) bytes (they never fall as M alone grows),
+ *          256-byte aligned.  Nothing in it needs initialising; calls that share it must not overlap.
  *   flags  DEVICE uint32 or NULL; the call only sets bits, the caller clears them
  * Few rows run as the recurrence, prompts in chunks of 64 rows whose products go
  * to the matrix cores with every operand's 24 bits: states and sums are fp32, and

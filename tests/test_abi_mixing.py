@@ -338,6 +338,14 @@ def test_indexes_of_another_type_binding(q):
     assert (b.n_seq, b.pages_ld) == (3, 2) and q.linear_attn_seqs(z(4), z(3), 1, fresh=z(3)).n_seq == 3
 
 
+@pytest.mark.parametrize("max_q", [12, 100, 193, 1000, 65536])
+@pytest.mark.parametrize("k_heads,v_heads,n_seq", [(1, 1, 1), (2, 4, 3), (16, 32, 1), (16, 32, 7), (100, 200, 1), (16, 128, 2), (1, 1, 255)])
+def test_linear_workspace_grows_with_the_rows(q, max_q, k_heads, v_heads, n_seq):
+    s = _seqs(q, max_q=max_q, n_seq=n_seq)
+    need = [q.linear_attn_ws(s, k_heads, v_heads, 64, 128, M) for M in [*range(1, 4000), 4096, 8192, 8193, 20000, 65535, 65536]]
+    assert min(need) > 0 and need == sorted(need)
+
+
 # ----------------------------------------------------------------------------
 # the checks under the host sanitisers
 # ----------------------------------------------------------------------------

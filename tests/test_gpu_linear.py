@@ -336,3 +336,17 @@ def test_row_starts_that_do_not_fit_are_told(max_q, start, clamped):
     c.upload()
     c.dstart.copy_(torch.tensor(start, dtype=torch.int32))
     c.run().check(flags=4)
+
+
+@pytest.mark.parametrize("KH,H", [(1, 2), (16, 32)])
+def test_a_workspace_for_many_rows_holds_fewer(KH, H):
+    """One workspace, sized for the largest batch, for shorter ones whose segments are cut otherwise."""
+    seqs = Case("one-ws", [4096], KH, H, 64, 64).upload().seqs
+    ws = torch.empty(q().linear_attn_ws(seqs, KH, H, 64, 64, 4096), dtype=torch.uint8, device="cuda")
+    for lens in ([768], [769], [300], [1500, 41], [5]):
+        c = Case("one-ws", lens, KH, H, 64, 64, max_q=4096).upload()
+        assert len(lens) > 1 or c.ws.numel() <= ws.numel()
+        guard = torch.full((ws.numel() + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+        c.ws = guard[: ws.numel()] if len(lens) == 1 else c.ws
+        c.run().check()
+        assert (host(guard[ws.numel():]) == 0xFF).all()

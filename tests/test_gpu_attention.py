@@ -564,3 +564,24 @@ def test_a_table_within_a_wider_one(q_len):
                                  prefix_pages=dev_i32(c.shared) if prefix else None)
         assert c.batch.pages_ld == c.cols + 9
         c.run().check()
+
+
+@pytest.mark.parametrize("q_len", [(1,) * 9, (3, 70, 150)])
+def test_two_streams_write_every_row_each_time(q_len):
+    """Calls that run beside each other, each behind a fill of its outputs, leave the same bits every time."""
+    cs = [Case("stream-fill", q_len, [n + 50 + 40 * i for i, n in enumerate(q_len)], 300 + j, 8, 2, 64, 16).upload() for j in range(2)]
+    for c in cs:
+        c.run().check()
+    want = [(c.out.clone(), c.lse.clone()) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, s in zip(cs, streams):
+            with torch.cuda.stream(s):
+                c.out.fill_(0x1234)
+                c.lse.fill_(-77)
+                c.ws.fill_(0xFF)
+                c.run()
+        torch.cuda.synchronize()
+        for c, (out, lse) in zip(cs, want):
+            assert torch.equal(c.out, out) and torch.equal(c.lse, lse)

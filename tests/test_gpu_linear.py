@@ -350,3 +350,24 @@ def test_a_workspace_for_many_rows_holds_fewer(KH, H):
         c.ws = guard[: ws.numel()] if len(lens) == 1 else c.ws
         c.run().check()
         assert (host(guard[ws.numel():]) == 0xFF).all()
+
+
+@pytest.mark.parametrize("lens", [(1,) * 9, (70, 200), (700, 3)])
+def test_two_streams_write_every_row_each_time(lens):
+    """Calls that run beside each other, each behind a fill of its outputs, leave the same bits every time."""
+    cs = [Case("stream-fill", [n + i for n in lens], 1, 2, 64, 64).upload() for i in range(2)]
+    for c in cs:
+        c.run().check()
+    want = [(c.out.clone(), c.dstate_out.clone()) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, s in zip(cs, streams):
+            with torch.cuda.stream(s):
+                c.out.fill_(-9.0)
+                c.dstate_out.fill_(-5.0)
+                c.ws.fill_(0xFF)
+                c.run()
+        torch.cuda.synchronize()
+        for c, (out, state) in zip(cs, want):
+            assert torch.equal(c.out, out) and torch.equal(c.dstate_out, state)

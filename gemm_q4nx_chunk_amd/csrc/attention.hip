@@ -78,7 +78,7 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, int D, 
 // values likewise: 16 KB a wave are always on the way.  Bound by memory, so that
 // the softmax's numerators can enter in two bf16 parts, which hold 16 bits.
 // (32 heads of 128: one token of 1000, 8192, 32768: 11.4, 16.0, 32.5 us a call, 4.1
-// TB/s at the last; 64 tokens of 2000: 65 us, 5.1 TB/s; over 8 bits 42, where turning
+// TB/s at the last; 64 tokens of 2000: 66 us, 5.0 TB/s; over 8 bits 42, where turning
 // codes to bf16 holds it back.)
 template <int D, bool I8, int RB>
 __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, int block, int blocks, AttnPlan& plan, uint8_t* lds) {
@@ -368,8 +368,8 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, const AttnParts& p, 
 // the prefix (64 tokens behind 16384: 59 us for 52; 64 of 2000 behind 8192: the same).
 //
 // Bound by the matrix cores (44 % busy) and the softmax between them: 4096 tokens
-// over 16384 of 32 heads of 128 run at 966 TFLOP/s, where a large library product
-// reaches 1235; 2048 over 8192 at 820 (64 wide: 620, 256 wide: 610).  Eight waves of
+// over 16384 of 32 heads of 128 run at 960 TFLOP/s, where a large library product
+// reaches 1235; 2048 over 8192 at 750 (64 wide: 610, 256 wide: 660).  Eight waves of
 // 256 rows, half of them at the products while the others are at the softmax, with
 // a barrier at each change, were slower (319 us for 300, 64 wide 232 for 193): the
 // barriers and what is done between them cost more than the overlap gave, which two
@@ -694,7 +694,10 @@ __device__ __forceinline__ void attn_many(const AttnArgs& a, const AttnParts& p,
 constexpr int attn_lds(int dim, int rows) { return rows == 128 ? 2 * 2 * 64 * dim * 2 : 4 * 16 * (dim + 4) * 4; }
 
 // Workgroups a CU that the registers are cut for.  (Three of 16 rows at 128 dimensions: 8 bits 46 us for 52, 64
-// tokens of 2000; bf16 spills, 72 for 64.)
+// tokens of 2000; bf16 spills, 72 for 64.  256 dimensions take all registers, and bf16 tiles of 32 rows spill 76 to 104
+// bytes a lane even so: 16 windows of 8 rows and 4000 tokens, 16 heads over 4, 44 us, of 4 rows in tiles of 16, which do
+// not, 42.  64 dimensions of few rows beside a prefix's two parts spill 12 bytes, over 8 bits 76; two workgroups for
+// three: 64 tokens of 2000 behind 4096 45 us for 41, over 8 bits 45 for 40, but of 300 behind 16384 48 for 47 and 53 for 65.)
 constexpr int attn_occupancy(int dim, bool i8, int rows) {
   return dim == 256 ? 1 : dim == 64 ? (rows == 32 ? 2 : 3) : i8 && rows == 16 ? 3 : 2;
 }
@@ -717,7 +720,7 @@ __global__ __launch_bounds__(256, attn_occupancy(D, I8, ROWS)) void k_attn(AttnA
 // by side, the prefix's products fill the matrix cores while the sequences' keys
 // and values stream (16 windows over 8 bits: 45 us, one after the other 71; 64
 // tokens behind 8192: 92 for 109.  Since then the few rows' loop has become faster:
-// 40 and 89, of which this kernel has 35 and 74, 4.9 TB/s).
+// 41 and 89, of which this kernel has 35 and 75, 4.9 TB/s).
 template <int D, bool I8, int OWN, int PRE>
 __global__ __launch_bounds__(256, attn_occupancy(D, I8, OWN > PRE ? OWN : PRE)) void k_attn_shared(AttnArgs a, AttnPair sets, int pre_grid) {
   __shared__ AttnPlan plan;

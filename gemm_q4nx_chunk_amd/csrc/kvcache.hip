@@ -8,8 +8,9 @@
 // bf16's step), keeps them in LDS, and turns every head with them.  A lane has two pieces of eight values, so
 // that both sides of a pair and what the cache holds together are one lane's.
 // Each value is read once and written once.  Bound by memory where there are many
-// rows (4096 of 32 + 8 heads of 128, fp32: 30 us, 5.1 TB/s; bf16 24 us, 4.2 TB/s), by
-// the launch and a few latencies where there are few (3.7 us).
+// rows (4096 of 32 + 8 heads of 128, fp32: 30 us, 5.1 TB/s; bf16 26 us, 4.1 TB/s), by
+// the launch and a few latencies where there are few (3.5 us).  Over 8 bits the fp64
+// turns and codes make it 36 us (from bf16 rows, 2.5 TB/s).
 //
 // Eight tokens whose slots are a run (a prompt's; the tiles begin where the first
 // row's run of eight does) have their values exchanged through LDS and stored
@@ -42,7 +43,7 @@ template <typename T>
 struct Turn { T c, s; };
 
 // To fp32: the angle less whole turns in fp64 (2 pi in two parts, so that nothing of a turn's digits is lost), then
-// the fp32 functions.
+// the fp32 functions: what is left, below pi, is off by 2^-23 at most, a bf16's half step by 2^-8 of the value.
 __device__ __forceinline__ void turn_of(double angle, Turn<float>& t) {
   const double turns = rint(angle * 0.15915494309189535);
   const double rest = fma(-turns, 2.4492935982947064e-16, fma(-turns, 6.283185307179586, angle));

@@ -757,7 +757,8 @@ enum { Q4NX_ATTN_MAX_SEQ = 1024, Q4NX_ATTN_MAX_M = 65536 };
  * A row that sees no key, or only keys with a score of -Inf, has out 0 and lse
  * -Inf.  What lies past a sequence's tokens, in its last page or in its table,
  * may hold anything, infinities and NaNs among it; so may tokens that a row does
- * not see.  A page number outside the cache is never followed: its tokens count
+ * not see.  An infinity in a value that it does see comes out as an infinity or
+ * NaN of that dimension.  A page number outside the cache is never followed: its tokens count
  * as unseen, and bit 0 of *flags is set.  A kv_len outside 0..pages_ld *
  * page_tokens, and rows of q_start that fall or leave 0..M, are clamped, and
  * bit 1 is set.
@@ -814,8 +815,8 @@ typedef struct q4nx_linear {
  * Few rows run as the recurrence, prompts in chunks of 64 rows whose products go
  * to the matrix cores with every operand's 24 bits: states and sums are fp32, and
  * what passes fp32's range comes out as an infinity or NaN.  An infinity or NaN
- * that comes in reaches what the recurrence lets it reach: not what is before it,
- * nor what a decay whose exp is 0 has cut off.
+ * that comes in reaches what the recurrence lets it reach, as one or the other: not
+ * what is before it, nor what a decay whose exp is 0 has cut off.
  * A slot outside -1..n_slots-1, or one that an earlier sequence with rows has, is
  * taken as -1 and sets bit 0.  Rows of q_start that fall or leave 0..M are
  * clamped, and bit 2 is set.

@@ -629,7 +629,7 @@ def _row_step(t, columns: int, width: int, what: str) -> int:
         if st and st[0] != 1 and t.shape[0] > 1:
             raise Q4nxError(E_SHAPE, f"{what}: the columns of a row must be contiguous")
         return columns
-    if len(st) > 3 or st[-1] != 1 or (len(st) == 3 and st[1] != width and t.shape[1] > 1):
+    if len(st) > 3 or (st[-1] != 1 and t.shape[-1] > 1) or (len(st) == 3 and st[1] != width and t.shape[1] > 1):
         raise Q4nxError(E_SHAPE, f"{what}: the columns of a row must be contiguous")
     return columns if st[0] < columns and t.shape[0] == 1 else st[0]
 

@@ -346,6 +346,14 @@ def test_linear_workspace_grows_with_the_rows(q, max_q, k_heads, v_heads, n_seq)
     assert min(need) > 0 and need == sorted(need)
 
 
+def test_one_column_at_any_stride_binding(q):
+    """The decays of a single head may be a column of a transposed array: the step between rows is all that counts."""
+    torch = pytest.importorskip("torch")
+    for decay in (torch.zeros(1, 3).t(), torch.zeros(2, 3).t()[:, :1], torch.zeros(3, 5)[:, 2:3]):
+        _expect(q, q.E_WORKSPACE, _linear, q, k_heads=1, v_heads=1, decay=decay, ws=0)       # past the strides' checks
+    _expect(q, q.E_SHAPE, _linear, q, k_heads=1, v_heads=2, decay=torch.zeros(2, 3).t())
+
+
 # ----------------------------------------------------------------------------
 # the checks under the host sanitisers
 # ----------------------------------------------------------------------------
